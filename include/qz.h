@@ -513,6 +513,234 @@ qz_status qz_split_fused_experts(const qz_fused_split *d_table, int n, int fmt, 
 qz_status qz_quantize_grouped_nvfp4_compute_noalloc(const qz_expert *d_table, int n_experts, int layout,
                                                     void *stream, const qz_launch_opts *opts);
 
+/* ===========================================================================
+ * The mixture-of-experts layer around the quantizers: routing, the experts'
+ * block-scaled products, and the moves between token order and expert order.
+ *
+ * A routed layer works on SLOTS: the (token, choice) pairs sorted by expert.
+ * qz_plan_experts gives expert e the slots [offsets[e], offsets[e] + counts[e]);
+ * offsets are multiples of the plan's `align`, so up to align - 1 unused slots
+ * follow each expert.  The entry points below read offsets and counts on the
+ * device (no call synchronizes), write no row outside the live slots unless
+ * their text says so, and skip an expert whose range does not fit the buffers
+ * (counts < 0, offsets < 0, offsets + counts > slots: QZ_DERR_SHAPE in
+ * *opts->d_err).
+ * ======================================================================== */
+
+/* Largest number of experts of the entry points below. */
+#define QZ_MAX_ROUTE_EXPERTS 1024
+/* Largest number of experts a token is routed to, and of expert groups. */
+#define QZ_MAX_TOP_K 32
+#define QZ_MAX_GROUPS 32
+
+typedef enum qz_type {
+    QZ_TYPE_BF16 = 0,
+    QZ_TYPE_F32 = 1
+} qz_type;
+
+typedef enum qz_score {
+    QZ_SCORE_SOFTMAX = 0, /* exp(x_i) / sum_j exp(x_j) over all experts */
+    QZ_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-x_i)) */
+} qz_score;
+
+typedef enum qz_activation {
+    QZ_ACT_NONE = 0,
+    QZ_ACT_RELU = 1, /* max(z, 0) */
+    QZ_ACT_SILU = 2, /* z / (1 + exp(-z)) */
+    QZ_ACT_GELU = 3  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+} qz_activation;
+
+/* How a router turns logits into choices (HOST struct, read during the call). */
+typedef struct qz_router {
+    int score;       /* qz_score */
+    int top_k;       /* experts per token, 1 .. QZ_MAX_TOP_K */
+    int n_groups;    /* 1: no groups; otherwise E / n_groups consecutive experts form a group */
+    int top_groups;  /* groups a token may choose from, 1 .. n_groups */
+    int renormalize; /* != 0: the chosen scores are divided by their sum */
+    float scale;     /* factor on every weight */
+} qz_router;
+
+/* Router: T rows of E logits to top_k experts and their weights.
+ *   s_i = the score of x_i; v_i = s_i + bias[i] (d_bias given) steers the choice
+ *   only, as a bias for balance does; without d_bias the experts are compared
+ *   by their logits (which orders them as their scores).
+ *   n_groups > 1: a group's value is the sum of its two largest v_i (its
+ *   largest, when it has one; scores without a bias); only the top_groups
+ *   groups of largest value keep their experts.
+ *   ids = the top_k experts in descending order; equal values go to the lower
+ *   index.  Biased scores and group values are compared in binary64.
+ *   w_j = s_j (over sum_j s_j if renormalize; 0 if that sum is 0) * scale, fp32.
+ * A logit of -inf or NaN, or a biased score of -inf or NaN, masks an expert: it
+ * is never chosen and counts 0 in a softmax.  Choices that remain empty get
+ * id -1 and weight 0 (all of them in a row that is masked entirely).  A logit
+ * of +inf counts as the largest finite float.
+ *   d_logits: [T, E] of `type`, row stride ld elements, any alignment of the type
+ *   d_bias:   float [E] or NULL;  d_ids: int32 [T, top_k];  d_weights: float [T, top_k]
+ * Errors: QZ_ERR_INVALID_ARG for T < 0, E outside 1 .. QZ_MAX_ROUTE_EXPERTS,
+ * ld < E, unknown enums, top_k outside 1 .. min(E, QZ_MAX_TOP_K), n_groups outside
+ * 1 .. QZ_MAX_GROUPS or not dividing E, top_groups outside 1 .. n_groups, top_k
+ * larger than the experts of top_groups groups, a scale that is not finite, null
+ * pointers; QZ_ERR_ALIGNMENT for pointers not aligned to their type. */
+qz_status qz_route_experts(const void *d_logits, int type, int64_t T, int E, int64_t ld, const float *d_bias,
+                           const qz_router *router, int32_t *d_ids, float *d_weights, void *stream);
+
+/* Gradient of the router's weights with respect to the logits, for given
+ * choices (the choice itself, the groups and the bias have none):
+ *   softmax, renormalized: dx_i = w_i (g_i - sum_j g_j w_j) on the chosen, 0 elsewhere
+ *   softmax:               dx_i = p_i (g_i [i chosen] - sum_j g_j p_j) on all experts
+ *   sigmoid, renormalized: dx_i = s_i (1 - s_i) (g_i - sum_j g_j s_j / S) / S, S = sum_j s_j
+ *   sigmoid:               dx_i = g_i s_i (1 - s_i)
+ * with g = scale * d_dweights; ids outside [0, E) take no part, a repeated id
+ * adds.  Every element of d_dlogits ([T, E] of `type`, row stride ldd) is written.
+ * Of the router, score, top_k, renormalize and scale are read.
+ * Errors: as qz_route_experts. */
+qz_status qz_route_experts_grad(const void *d_logits, int type, int64_t T, int E, int64_t ld, const qz_router *router,
+                                const int32_t *d_ids, const float *d_dweights, void *d_dlogits, int64_t ldd,
+                                void *stream);
+
+/* Slots a plan of T tokens with top_k choices over E experts can need:
+ * T * top_k + min(E, T * top_k) * (align - 1), rounded up to align; 0 for
+ * arguments qz_plan_experts refuses. */
+int64_t qz_plan_slots(int64_t T, int top_k, int E, int align);
+
+/* Device scratch of qz_plan_experts in bytes (0: none needed). */
+size_t qz_plan_bytes(int64_t T, int top_k, int E);
+
+/* Expert order of the choices: a stable sort of the (token, choice) pairs by
+ * expert, pairs of one expert in token order.
+ *   d_ids:     int32 [T, top_k]; an id outside [0, E) has no slot
+ *   d_offsets: int32 [E + 1], first slot of each expert, multiples of align; [E] = slots in use
+ *   d_counts:  int32 [E], live slots of each expert
+ *   d_rows:    int32 [qz_plan_slots(...)], the token of each slot, -1 in unused slots
+ *   d_slots:   int32 [T, top_k], the slot of each pair, -1 where it has none
+ *   d_workspace: qz_plan_bytes(T, top_k, E) bytes, 4-byte aligned (NULL when that is 0);
+ *              calls sharing it must not overlap
+ * Results do not depend on the launch's timing.  T == 0 writes offsets and counts of 0.
+ * Errors: QZ_ERR_INVALID_ARG for T < 0, top_k outside 1 .. QZ_MAX_TOP_K, E outside
+ * 1 .. QZ_MAX_ROUTE_EXPERTS, align outside 1 .. 1024 or not a power of two, more than 2^31 - 1
+ * slots, null pointers, a workspace smaller than needed; QZ_ERR_ALIGNMENT. */
+qz_status qz_plan_experts(const int32_t *d_ids, int64_t T, int top_k, int E, int align, int32_t *d_offsets,
+                          int32_t *d_counts, int32_t *d_rows, int32_t *d_slots, void *d_workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* The experts' matrix product (HOST struct, read during the call).  Operands are
+ * what the quantizers above write: x row-wise with LINEAR scales (rows are
+ * gathered one by one), every expert's weight row-wise with SWIZZLED scales. */
+typedef struct qz_product {
+    int fmt;               /* QZ_FMT_MXFP8 or QZ_FMT_NVFP4, both operands */
+    int activation;        /* qz_activation */
+    int n_experts;         /* 1 .. QZ_MAX_ROUTE_EXPERTS */
+    int x_amax_per_row;    /* NVFP4: != 0: x_amax[x_rows], else x_amax[1] */
+    int64_t n;             /* output columns, a multiple of 8 (of 32 with q) */
+    int64_t k;             /* contraction length, a multiple of 32 */
+    int64_t x_rows;        /* rows of x */
+    int64_t slots;         /* rows of out, residual, pre and q; entries of d_rows */
+    const void *x_q;       /* [x_rows, k] e4m3 or [x_rows, k/2] packed e2m1, 16-byte aligned */
+    const uint8_t *x_sf;   /* linear scales [x_rows, k/32] or [x_rows, k/16] */
+    const float *x_amax;   /* NVFP4 */
+    const int32_t *d_rows; /* [slots] row of x of each slot, or NULL: slot s reads row s */
+    const int32_t *d_offsets; /* [n_experts] (or more) first slot of each expert */
+    const int32_t *d_counts;  /* [n_experts] live slots of each expert */
+    const void *w_q;       /* expert e's [n, k] (packed) payload at w_q + e * w_stride bytes, 16-byte aligned */
+    const uint8_t *w_sf;   /* expert e's swizzled scales of an [n, k] matrix at w_sf + e * w_sf_stride */
+    const float *w_amax;   /* NVFP4: [n_experts], each expert's tensor amax */
+    const void *up_q;      /* gated: a second weight of the same layout and strides, or NULL */
+    const uint8_t *up_sf;
+    const float *up_amax;
+    int64_t w_stride;      /* bytes, a multiple of 16, >= n * (bytes of a row) */
+    int64_t w_sf_stride;   /* bytes, a multiple of 16 */
+    const void *bias;      /* bf16 [n_experts, n] or NULL, 16-byte aligned */
+    const void *up_bias;   /* gated: bf16 [n_experts, n] or NULL */
+    const void *residual;  /* bf16 [slots, n], row stride ld_residual, or NULL */
+    int64_t ld_residual;   /* elements, multiples of 8 */
+    void *out;             /* bf16 [slots, n], row stride ld_out, 16-byte aligned */
+    int64_t ld_out;
+    void *pre;             /* bf16 [slots, n] (gated: [slots, 2n], z then u), row stride ld_pre, or NULL */
+    int64_t ld_pre;
+    void *q;               /* MXFP8 form of out: e4m3 [slots, n], 16-byte aligned, or NULL */
+    uint8_t *sf;           /* its linear scales [slots, n/32] */
+} qz_product;
+
+/* For every live slot s of expert e, with A the dequantized row of x and W, U
+ * the dequantized weights (values as in
+ * qz_dequantize_grouped; NVFP4's g = RN32(amax / 2688) of both operands
+ * multiply the finished sum):
+ *   z = A W_e^T + bias_e          (fp32 accumulation)       -> pre[s]
+ *   h = act(z),  gated: h = act(z) * u,  u = A U_e^T + up_bias_e   -> pre[s] (second half)
+ *   out[s] = bf16(h + residual[s]),  q, sf[s] = the MXFP8 form of out[s]
+ * Only live slots are written.  A d_rows entry outside [0, x_rows) stands for a
+ * row of zeros.  One launch, no allocation, no dependence of the results on the
+ * grid.  The same call is the data gradient: dA = dZ W is the product of the
+ * row-wise quantized dZ with W quantized column-wise ([k, n] payloads from
+ * qz_quantize_grouped_colwise).
+ * Errors: QZ_ERR_INVALID_ARG for sizes, enums, null pointers or strides outside
+ * the above, slots or x_rows above 2^31 - 1, up_bias or up_amax without up_q;
+ * QZ_ERR_ALIGNMENT; QZ_ERR_CUDA when a tensor map or the launch is refused. */
+qz_status qz_expert_product(const qz_product *p, void *stream, const qz_launch_opts *opts);
+
+/* The experts' weight gradients (HOST struct, read during the call).  Operands
+ * are column-wise quantized over ALL slots at once (one entry of
+ * qz_quantize_grouped_colwise each), scales swizzled. */
+typedef struct qz_weight_grad {
+    int fmt;               /* QZ_FMT_MXFP8 or QZ_FMT_NVFP4, both operands */
+    int n_experts;
+    int out_type;          /* qz_type of out */
+    int accumulate;        /* != 0: out += the gradient (rounded once), else out = */
+    int64_t n, k;          /* out is [n_experts, n, k]; multiples of 8 */
+    int64_t slots;         /* rows of dz and x, a multiple of 32 */
+    const void *dz_q;      /* dZ^T: [n, slots] (packed: [n, slots/2]), 16-byte aligned */
+    const uint8_t *dz_sf;  /* swizzled scales of an [n, slots] matrix, 16-byte aligned */
+    const float *dz_amax;  /* NVFP4: one float */
+    const void *x_q;       /* X^T: [k, slots], likewise */
+    const uint8_t *x_sf;
+    const float *x_amax;
+    const int32_t *d_offsets; /* [n_experts], multiples of 128 (QZ_DERR_ALIGN and no output otherwise) */
+    const int32_t *d_counts;
+    void *out;             /* [n_experts, n, k], 16-byte aligned */
+} qz_weight_grad;
+
+/* out[e] (+)= sum over the live slots s of expert e of dZ[s]^T X[s], fp32
+ * accumulation; an expert without slots gets zeros (is left, when accumulating).
+ * Slots from counts[e] up to the next multiple of 64 must hold zeros in both
+ * operands (qz_dispatch_experts and qz_expert_activation_grad write them).
+ * Errors: as qz_expert_product. */
+qz_status qz_expert_weight_grad(const qz_weight_grad *p, void *stream, const qz_launch_opts *opts);
+
+/* Gradient of qz_expert_product's activation and biases:
+ *   dz = dout act'(z);  gated: dz = dout u act'(z), du = dout act(z)
+ *   dbias[e] = the sum of its rows' dz (du) before they are rounded, fp32, in a fixed order
+ *   d_dout: bf16 [slots, n];  d_pre, d_dpre: bf16 [slots, n] (gated: [slots, 2n], z then u),
+ *   row strides ld_* (multiples of 8, pointers 16-byte aligned);  d_dbias: float [n_experts, n]
+ *   (gated [n_experts, 2n]) or NULL;  d_offsets: int32 [n_experts + 1], ascending
+ * Rows of d_dpre that are no live slot are written as zeros.
+ * Errors: QZ_ERR_INVALID_ARG for sizes, enums or null pointers outside the above; QZ_ERR_ALIGNMENT. */
+qz_status qz_expert_activation_grad(const void *d_dout, int64_t ld_dout, const void *d_pre, int64_t ld_pre,
+                                    int64_t slots, int64_t n, int activation, int gated, const int32_t *d_offsets,
+                                    const int32_t *d_counts, int n_experts, void *d_dpre, int64_t ld_dpre,
+                                    float *d_dbias, void *stream, const qz_launch_opts *opts);
+
+/* Token order -> expert order: y[slots[t][j]] = bf16(w[t][j] x[t]); every slot
+ * whose d_rows entry is -1 gets a row of zeros.  With d_other also
+ * dots[t][j] = <x[t], other[slots[t][j]]> (fp32; 0 where the pair has no slot).
+ * With x the gradient of the layer's output, w the routing weights and other
+ * the experts' outputs, y and dots are qz_combine_experts's gradients; with
+ * d_weights NULL (1) it is the copy that the column-wise quantizer of the
+ * weight gradient reads.
+ *   d_x: bf16 [T, H]; d_y, d_other: bf16 [slots, H]; H a multiple of 8, row strides
+ *   multiples of 8, pointers 16-byte aligned; d_weights, d_dots: float [T, top_k]
+ *   d_slots: int32 [T, top_k] (entries outside [0, slots) are skipped); d_rows: int32 [slots]
+ * Errors: QZ_ERR_INVALID_ARG, QZ_ERR_ALIGNMENT as above; d_other and d_dots come together. */
+qz_status qz_dispatch_experts(const void *d_x, int64_t ld_x, const int32_t *d_slots, const int32_t *d_rows, int64_t T,
+                              int top_k, int64_t slots, int64_t H, const float *d_weights, void *d_y, int64_t ld_y,
+                              const void *d_other, int64_t ld_other, float *d_dots, void *stream);
+
+/* Expert order -> token order: out[t] = bf16(residual[t] + sum_j w[t][j] y[slots[t][j]]),
+ * summed in fp32 in the order of j from the residual (0 without one); pairs without a slot add
+ * nothing.  Every row of out is written.  Arguments as qz_dispatch_experts; out may be residual. */
+qz_status qz_combine_experts(const void *d_y, int64_t ld_y, const int32_t *d_slots, int64_t T, int top_k,
+                             int64_t slots, int64_t H, const float *d_weights, const void *d_residual,
+                             int64_t ld_residual, void *d_out, int64_t ld_out, void *stream);
+
 /* A static, human-readable name for a status code. */
 const char *qz_status_string(qz_status status);
 

@@ -17,6 +17,10 @@ from .binding import (  # noqa: F401
     dequantize_grouped, ipc_close, ipc_export, ipc_import, load, quantize_experts, quantize_grouped_colwise, quantize_grouped_mxfp8,
     quantize_grouped_nvfp4, quantize_grouped_nvfp4_compute_noalloc, rmsnorm_quantize, sf_bytes,
     split_fused_experts, status_string, swizzle_scales, workspace_bytes,
+    ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, MAX_GROUPS, MAX_ROUTE_EXPERTS, MAX_TOP_K, SCORE_SIGMOID, SCORE_SOFTMAX,
+    ExpertPlan, combine_experts, dispatch_experts, expert_activation_grad, expert_product, expert_weight_grad,
+    plan_experts, plan_slots, quantize_expert_weights, quantize_slots_colwise, quantize_tokens, route_experts,
+    route_experts_grad,
 )
 
 __version__ = "0.1.0"

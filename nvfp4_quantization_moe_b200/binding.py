@@ -12,7 +12,7 @@ import ctypes
 import os
 import threading
 from dataclasses import dataclass
-from typing import Iterable, Optional, Sequence
+from typing import Iterable, NamedTuple, Optional, Sequence
 
 import numpy as np
 import torch
@@ -33,6 +33,10 @@ OPT_INDEPENDENT = 0x1
 MAX_EXPERTS = 4096
 MAX_HIDDEN = 16384
 MAX_RANKS = 8
+TYPE_BF16, TYPE_F32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
+MAX_ROUTE_EXPERTS, MAX_TOP_K, MAX_GROUPS = 1024, 32, 32
 
 EXPORTED = (
     "qz_sf_bytes",
@@ -52,6 +56,16 @@ EXPORTED = (
     "qz_ipc_export",
     "qz_ipc_import",
     "qz_ipc_close",
+    "qz_route_experts",
+    "qz_route_experts_grad",
+    "qz_plan_slots",
+    "qz_plan_bytes",
+    "qz_plan_experts",
+    "qz_expert_product",
+    "qz_expert_weight_grad",
+    "qz_expert_activation_grad",
+    "qz_dispatch_experts",
+    "qz_combine_experts",
 )
 STATIC_WS_MAX_EXPERTS = 1024
 
@@ -90,6 +104,33 @@ class IpcHandle(ctypes.Structure):
     of the exported pointer in it."""
     _fields_ = [("handle", ctypes.c_ubyte * 64), ("offset", ctypes.c_uint64), ("alloc_bytes", ctypes.c_uint64),
                 ("device", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class _Router(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("top_k", ctypes.c_int), ("n_groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class _Product(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int), ("activation", ctypes.c_int), ("n_experts", ctypes.c_int),
+                ("x_amax_per_row", ctypes.c_int), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("x_rows", ctypes.c_int64), ("slots", ctypes.c_int64), ("x_q", ctypes.c_void_p),
+                ("x_sf", ctypes.c_void_p), ("x_amax", ctypes.c_void_p), ("d_rows", ctypes.c_void_p),
+                ("d_offsets", ctypes.c_void_p), ("d_counts", ctypes.c_void_p), ("w_q", ctypes.c_void_p),
+                ("w_sf", ctypes.c_void_p), ("w_amax", ctypes.c_void_p), ("up_q", ctypes.c_void_p),
+                ("up_sf", ctypes.c_void_p), ("up_amax", ctypes.c_void_p), ("w_stride", ctypes.c_int64),
+                ("w_sf_stride", ctypes.c_int64), ("bias", ctypes.c_void_p), ("up_bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("ld_out", ctypes.c_int64), ("pre", ctypes.c_void_p), ("ld_pre", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("sf", ctypes.c_void_p)]
+
+
+class _WeightGrad(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int), ("n_experts", ctypes.c_int), ("out_type", ctypes.c_int),
+                ("accumulate", ctypes.c_int), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("slots", ctypes.c_int64),
+                ("dz_q", ctypes.c_void_p), ("dz_sf", ctypes.c_void_p), ("dz_amax", ctypes.c_void_p),
+                ("x_q", ctypes.c_void_p), ("x_sf", ctypes.c_void_p), ("x_amax", ctypes.c_void_p),
+                ("d_offsets", ctypes.c_void_p), ("d_counts", ctypes.c_void_p), ("out", ctypes.c_void_p)]
 
 
 class _Opts(ctypes.Structure):
@@ -151,6 +192,26 @@ def load(path: str = LIB_PATH):
         lib.qz_allreduce_rmsnorm_quantize.restype = I
         lib.qz_allreduce_rmsnorm_quantize.argtypes = [P, I, P, P, ctypes.c_float, i64, i64, i64, i64, P, I, I, I,
                                                       P, P]
+        lib.qz_route_experts.restype = I
+        lib.qz_route_experts.argtypes = [P, I, i64, I, i64, P, P, P, P, P]
+        lib.qz_route_experts_grad.restype = I
+        lib.qz_route_experts_grad.argtypes = [P, I, i64, I, i64, P, P, P, P, i64, P]
+        lib.qz_plan_slots.restype = i64
+        lib.qz_plan_slots.argtypes = [i64, I, I, I]
+        lib.qz_plan_bytes.restype = ctypes.c_size_t
+        lib.qz_plan_bytes.argtypes = [i64, I, I]
+        lib.qz_plan_experts.restype = I
+        lib.qz_plan_experts.argtypes = [P, i64, I, I, I, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.qz_expert_product.restype = I
+        lib.qz_expert_product.argtypes = [P, P, P]
+        lib.qz_expert_weight_grad.restype = I
+        lib.qz_expert_weight_grad.argtypes = [P, P, P]
+        lib.qz_expert_activation_grad.restype = I
+        lib.qz_expert_activation_grad.argtypes = [P, i64, P, i64, i64, i64, I, I, P, P, I, P, i64, P, P, P]
+        lib.qz_dispatch_experts.restype = I
+        lib.qz_dispatch_experts.argtypes = [P, i64, P, P, i64, I, i64, i64, P, P, i64, P, i64, P, P]
+        lib.qz_combine_experts.restype = I
+        lib.qz_combine_experts.argtypes = [P, i64, P, i64, I, i64, i64, P, P, i64, P, i64, P]
         _lib = lib
         return lib
 
@@ -510,6 +571,318 @@ def swizzle_scales(table: SfPairTable, stream=None, err=None, max_ctas: int = 0)
 
 
 # ---------------------------------------------------------------------------
+# the mixture-of-experts layer: routing, the experts' products, the moves
+# between token order and expert order
+# ---------------------------------------------------------------------------
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, name: str, dtype, shape=None, optional: bool = False) -> int:
+    """Address of a contiguous CUDA tensor of the given type (and shape), 0 for an absent optional one."""
+    if t is None:
+        _require(optional, f"{name} is required")
+        return 0
+    _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _require(t.is_contiguous(), f"{name} must be contiguous")
+    _require(shape is None or tuple(t.shape) == shape, f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    _on_device(t, name)
+    return t.data_ptr()
+
+
+def _on_device(t, name: str):
+    """Every tensor must be on the current CUDA device, where the kernels are launched."""
+    _require(t.is_cuda and t.device.index == torch.cuda.current_device(),
+             f"{name} must be on the current CUDA device, not {t.device}")
+
+
+def _matrix(t, name: str, dtype, shape, optional: bool = False):
+    """(address, row stride) of a CUDA matrix whose rows are contiguous; (0, 0) for an absent optional one."""
+    if t is None:
+        _require(optional, f"{name} is required")
+        return 0, 0
+    _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _require(tuple(t.shape) == shape, f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    _require(shape[1] == 1 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
+    _on_device(t, name)
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def _codes(t, name: str, cols: int, fmt: int):
+    """Payloads come as uint8 bytes (or, for MXFP8, as torch.float8_e4m3fn): [..., cols] or [..., cols / 2]."""
+    _require(t.dtype == torch.uint8 or (fmt == FMT_MXFP8 and t.dtype == torch.float8_e4m3fn),
+             f"{name} must be a quantized payload, not {t.dtype}")
+    _require(t.shape[-1] == (cols if fmt == FMT_MXFP8 else cols // 2), f"the last axis of {name} does not match")
+    _on_device(t, name)
+    return t.data_ptr()
+
+
+def _parts(x, name: str):
+    _require(isinstance(x, (tuple, list)) and len(x) in (2, 3), f"{name} must be (payload, scales) or "
+             "(payload, scales, amax)")
+    return x[0], x[1], (x[2] if len(x) == 3 else None)
+
+
+def _router(top_k, score, n_groups, top_groups, renormalize, scale):
+    return ctypes.byref(_Router(int(score), int(top_k), int(n_groups), int(top_groups), 1 if renormalize else 0,
+                                float(scale)))
+
+
+def _float_type(t, name: str) -> int:
+    _require(t.dtype in (torch.bfloat16, torch.float32), f"{name} must be bfloat16 or float32, not {t.dtype}")
+    return TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32
+
+
+def route_experts(logits: torch.Tensor, top_k: int, *, score: int = SCORE_SOFTMAX, bias=None, n_groups: int = 1,
+                  top_groups: Optional[int] = None, renormalize: bool = True, scale: float = 1.0, ids=None,
+                  weights=None, stream=None):
+    """Router (qz_route_experts): bf16 or fp32 logits [T, E] to the top_k experts
+    of each token.  Returns (ids int32 [T, top_k], weights fp32 [T, top_k]),
+    written into ``ids`` and ``weights`` when given.  ``bias`` (fp32 [E]) steers
+    the choice only; ``top_groups`` (default all) of ``n_groups`` groups of
+    consecutive experts stay in the choice."""
+    _require(logits.dim() == 2, "logits must be [T, E]")
+    kind = _float_type(logits, "logits")
+    T, E = logits.shape
+    x, ld = _matrix(logits, "logits", logits.dtype, (T, E))
+    b = _tensor(bias, "bias", torch.float32, (E,), optional=True)
+    if ids is None:
+        ids = torch.empty((T, max(int(top_k), 0)), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, max(int(top_k), 0)), dtype=torch.float32, device=logits.device)
+    i = _tensor(ids, "ids", torch.int32, (T, top_k))
+    w = _tensor(weights, "weights", torch.float32, (T, top_k))
+    _check(load().qz_route_experts(x, kind, T, E, ld, b,
+                                   _router(top_k, score, n_groups, n_groups if top_groups is None else top_groups,
+                                           renormalize, scale), i, w, _stream_ptr(stream)), "qz_route_experts")
+    return ids, weights
+
+
+def route_experts_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, *, score: int = SCORE_SOFTMAX,
+                       renormalize: bool = True, scale: float = 1.0, dlogits=None, stream=None):
+    """Gradient of the router's weights with respect to the logits, for the
+    choices ``ids`` (qz_route_experts_grad); returns dlogits [T, E] of the
+    logits' type."""
+    _require(logits.dim() == 2 and ids.dim() == 2, "logits must be [T, E] and ids [T, top_k]")
+    kind = _float_type(logits, "logits")
+    T, E = logits.shape
+    k = ids.shape[1]
+    x, ld = _matrix(logits, "logits", logits.dtype, (T, E))
+    i = _tensor(ids, "ids", torch.int32, (T, k))
+    g = _tensor(dweights, "dweights", torch.float32, (T, k))
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    d, ldd = _matrix(dlogits, "dlogits", logits.dtype, (T, E))
+    _check(load().qz_route_experts_grad(x, kind, T, E, ld, _router(k, score, 1, 1, renormalize, scale), i, g, d, ldd,
+                                        _stream_ptr(stream)), "qz_route_experts_grad")
+    return dlogits
+
+
+def plan_slots(T: int, top_k: int, n_experts: int, align: int = 1) -> int:
+    """Slots a plan of T tokens can need (qz_plan_slots)."""
+    return int(load().qz_plan_slots(int(T), int(top_k), int(n_experts), int(align)))
+
+
+class ExpertPlan(NamedTuple):
+    """Expert order of a router's choices: expert e has the slots [offsets[e],
+    offsets[e] + counts[e]); rows gives each slot's token (-1: unused), slots
+    each (token, choice) pair's slot (-1: none).  All int32 on the device."""
+    offsets: torch.Tensor
+    counts: torch.Tensor
+    rows: torch.Tensor
+    slots: torch.Tensor
+
+
+def plan_experts(ids: torch.Tensor, n_experts: int, *, align: int = 1, plan: Optional[ExpertPlan] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> ExpertPlan:
+    """Sort the choices ``ids`` [T, top_k] by expert (qz_plan_experts), each
+    expert's slots starting at a multiple of ``align``.  The outputs (and, for
+    many pairs, the scratch) are allocated unless given."""
+    _require(ids.dim() == 2, "ids must be [T, top_k]")
+    T, k = ids.shape
+    i = _tensor(ids, "ids", torch.int32)
+    lib = load()
+    n = lib.qz_plan_slots(T, k, int(n_experts), int(align))
+    need = lib.qz_plan_bytes(T, k, int(n_experts))
+    if plan is None:
+        E = max(int(n_experts), 0)
+        buf = torch.empty(2 * E + 1 + n + T * k, dtype=torch.int32, device=ids.device)
+        plan = ExpertPlan(buf[:E + 1], buf[E + 1:2 * E + 1], buf[2 * E + 1:2 * E + 1 + n],
+                          buf[2 * E + 1 + n:].view(T, k))
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    ws = 0 if workspace is None else _tensor(workspace, "workspace", torch.uint8)
+    _check(lib.qz_plan_experts(i, T, k, int(n_experts), int(align),
+                               _tensor(plan.offsets, "offsets", torch.int32, (n_experts + 1,)),
+                               _tensor(plan.counts, "counts", torch.int32, (n_experts,)),
+                               _tensor(plan.rows, "rows", torch.int32, (n,)),
+                               _tensor(plan.slots, "slots", torch.int32, (T, k)), ws,
+                               0 if workspace is None else workspace.numel(), _stream_ptr(stream)), "qz_plan_experts")
+    return plan
+
+
+def _expert_lists(offsets, counts, n_experts: int):
+    """Addresses of offsets ([n_experts] or [n_experts + 1]) and counts."""
+    _require(offsets.dim() == 1 and offsets.numel() in (n_experts, n_experts + 1), "offsets must be [n_experts + 1]")
+    return _tensor(offsets, "offsets", torch.int32), _tensor(counts, "counts", torch.int32, (n_experts,))
+
+
+def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, out: torch.Tensor, *, rows=None,
+                   up=None, bias=None, up_bias=None, activation: int = ACT_NONE, residual=None, pre=None, q=None,
+                   sf=None, stream=None, err=None, max_ctas: int = 0):
+    """The experts' matrix products with bias, activation, gate and residual in
+    the epilogue (qz_expert_product).
+
+    x:  (payload [R, K], linear scales [R, K/block], NVFP4: amax [R] or [1])
+    w:  (payload [E, N, K], swizzled scales [E, region], NVFP4: amax [E]); an
+        expert's payload rows and region are dense, experts may be further
+        apart (a view of the gate or up half of fused weights)
+    up: a second weight like w (same strides): out = act(x w) * (x up)
+    out: bf16 [slots, N]; rows: int32 [slots] row of x of each slot (None: the
+    slot's own number); bias, up_bias: bf16 [E, N]; residual: bf16 [slots, N];
+    pre: bf16 [slots, N or 2N] receives the pre-activations; q [slots, N] and
+    sf [slots, N/32] receive the MXFP8 form of out."""
+    xq, xsf, xa = _parts(x, "x")
+    wq, wsf, wa = _parts(w, "w")
+    _require(xq.dim() == 2 and wq.dim() == 3 and out.dim() == 2, "x must be [R, K], w [E, N, K], out [slots, N]")
+    _require(fmt in (FMT_MXFP8, FMT_NVFP4), "fmt must be FMT_MXFP8 or FMT_NVFP4")
+    fp4 = fmt == FMT_NVFP4
+    E, N = wq.shape[:2]
+    K = xq.shape[1] * (2 if fp4 else 1)
+    R, S = xq.shape[0], out.shape[0]
+    _require(xq.is_contiguous(), "x must be contiguous")
+    kv = K // (16 if fp4 else 32)
+
+    def weight(part, name):
+        pq, psf, pa = part
+        _require(pq.dim() == 3 and pq.shape[:2] == (E, N), f"{name} must be [E, N, K]")
+        _require(pq.stride(2) == 1 and (N == 1 or pq.stride(1) == pq.shape[2]), f"{name}: an expert's rows must be dense")
+        _require(psf.dim() == 2 and psf.shape[0] == E and psf.dtype == torch.uint8 and psf.stride(1) == 1
+                 and psf.shape[1] >= sf_bytes(N, K, fmt, SF_SWIZZLED), f"{name}: scales must be [E, region] bytes")
+        _on_device(psf, f"{name}'s scales")
+        return (_codes(pq, name, K, fmt), psf.data_ptr(),
+                _tensor(pa, f"{name}'s amax", torch.float32, (E,)) if fp4 else 0,
+                pq.stride(0) if E > 1 else N * pq.shape[2], psf.stride(0) if E > 1 else (psf.shape[1] + 15) // 16 * 16)
+
+    wp = weight((wq, wsf, wa), "w")
+    upp = (0, 0, 0)
+    if up is not None:
+        upp = weight(_parts(up, "up"), "up")
+        _require(upp[3:] == wp[3:], "w and up must have the same strides")
+    offs, cnts = _expert_lists(offsets, counts, E)
+    o, ldo = _matrix(out, "out", torch.bfloat16, (S, N))
+    r, ldr = _matrix(residual, "residual", torch.bfloat16, (S, N), optional=True)
+    z, ldz = _matrix(pre, "pre", torch.bfloat16, (S, N if up is None else 2 * N), optional=True)
+    _require((q is None) == (sf is None), "q and sf come together")
+    if q is not None:
+        _require(q.is_contiguous() and q.shape == (S, N), "q must be a contiguous [slots, N]")
+        _require(sf.is_contiguous() and sf.dtype == torch.uint8 and sf.shape == (S, N // 32), "sf must be [slots, N/32] bytes")
+        _on_device(sf, "sf")
+    amax = 0
+    if fp4:
+        _require(xa is not None and xa.numel() in (1, R), "x's amax must be [R] or [1]")
+        amax = _tensor(xa, "x's amax", torch.float32)
+    p = _Product(fmt, int(activation), E, 1 if fp4 and xa.numel() == R and R > 1 else 0, N, K, R, S,
+                 _codes(xq, "x", K, fmt), _tensor(xsf, "x's scales", torch.uint8, (R, kv)), amax,
+                 _tensor(rows, "rows", torch.int32, (S,), optional=True), offs, cnts, wp[0], wp[1], wp[2], upp[0],
+                 upp[1], upp[2], wp[3], wp[4], _tensor(bias, "bias", torch.bfloat16, (E, N), optional=True),
+                 _tensor(up_bias, "up_bias", torch.bfloat16, (E, N), optional=True), r, ldr, o, ldo, z, ldz,
+                 0 if q is None else _codes(q, "q", N, FMT_MXFP8), 0 if sf is None else sf.data_ptr())
+    _check(load().qz_expert_product(ctypes.byref(p), _stream_ptr(stream), _opts(err, max_ctas)), "qz_expert_product")
+    return out
+
+
+def expert_weight_grad(fmt: int, dz, x, offsets: torch.Tensor, counts: torch.Tensor, out: torch.Tensor, *,
+                       accumulate: bool = False, stream=None, err=None, max_ctas: int = 0):
+    """The experts' weight gradients out[e] (+)= dZ_e^T X_e (qz_expert_weight_grad).
+
+    dz, x: column-wise quantized over all slots: (payload [N, slots] / [K,
+    slots] (packed: slots / 2), swizzled scales of that matrix, NVFP4: amax
+    [1]); out: [E, N, K] fp32 or bf16.  offsets must be multiples of 128 (a
+    plan with align=128) and unused slots must hold zeros."""
+    zq, zsf, za = _parts(dz, "dz")
+    xq, xsf, xa = _parts(x, "x")
+    _require(zq.dim() == 2 and xq.dim() == 2 and out.dim() == 3, "dz must be [N, slots], x [K, slots], out [E, N, K]")
+    _require(fmt in (FMT_MXFP8, FMT_NVFP4), "fmt must be FMT_MXFP8 or FMT_NVFP4")
+    fp4 = fmt == FMT_NVFP4
+    E, N, K = out.shape
+    S = zq.shape[1] * (2 if fp4 else 1)
+    _require(zq.shape[0] == N and xq.shape[0] == K, "dz, x and out do not match")
+    _require(zq.is_contiguous() and xq.is_contiguous(), "dz and x must be contiguous")
+    _require(zsf.numel() >= sf_bytes(N, S, fmt, SF_SWIZZLED) and xsf.numel() >= sf_bytes(K, S, fmt, SF_SWIZZLED),
+             "the scales are smaller than the swizzled region")
+    offs, cnts = _expert_lists(offsets, counts, E)
+    p = _WeightGrad(fmt, E, _float_type(out, "out"), 1 if accumulate else 0, N, K, S, _codes(zq, "dz", S, fmt),
+                    _tensor(zsf, "dz's scales", torch.uint8),
+                    _tensor(za, "dz's amax", torch.float32, (1,)) if fp4 else 0, _codes(xq, "x", S, fmt),
+                    _tensor(xsf, "x's scales", torch.uint8),
+                    _tensor(xa, "x's amax", torch.float32, (1,)) if fp4 else 0, offs, cnts,
+                    _tensor(out, "out", out.dtype))
+    _check(load().qz_expert_weight_grad(ctypes.byref(p), _stream_ptr(stream), _opts(err, max_ctas)),
+           "qz_expert_weight_grad")
+    return out
+
+
+def expert_activation_grad(dout: torch.Tensor, pre: torch.Tensor, offsets: torch.Tensor, counts: torch.Tensor,
+                           dpre: torch.Tensor, *, activation: int, gated: bool = False, dbias=None, stream=None,
+                           err=None):
+    """Gradient of expert_product's activation from its saved pre-activations,
+    with the bias gradients (qz_expert_activation_grad): dout [slots, N], pre
+    and dpre bf16 [slots, N or 2N], dbias fp32 [E, N or 2N] or None.  offsets
+    must be [E + 1] or [E], as the plan writes them; rows of dpre that are no
+    live slot become zeros."""
+    S, N = dout.shape
+    width = 2 * N if gated else N
+    E = counts.numel()
+    offs, cnts = _expert_lists(offsets, counts, E)
+    d, ldd = _matrix(dout, "dout", torch.bfloat16, (S, N))
+    z, ldz = _matrix(pre, "pre", torch.bfloat16, (S, width))
+    g, ldg = _matrix(dpre, "dpre", torch.bfloat16, (S, width))
+    _check(load().qz_expert_activation_grad(d, ldd, z, ldz, S, N, int(activation), 1 if gated else 0, offs, cnts, E,
+                                            g, ldg, _tensor(dbias, "dbias", torch.float32, (E, width), optional=True),
+                                            _stream_ptr(stream), _opts(err, 0)), "qz_expert_activation_grad")
+    return dpre
+
+
+def dispatch_experts(x: torch.Tensor, slots: torch.Tensor, rows: torch.Tensor, y: torch.Tensor, *, weights=None,
+                     other=None, dots=None, stream=None):
+    """Token order to expert order (qz_dispatch_experts): y[slots[t, j]] =
+    weights[t, j] * x[t], zeros in unused slots; with ``other`` [slots, H] also
+    dots[t, j] = <x[t], other[slots[t, j]]>.  The gradient of combine_experts."""
+    _require(x.dim() == 2 and slots.dim() == 2 and y.dim() == 2, "x must be [T, H], slots [T, top_k], y [slots, H]")
+    T, H = x.shape
+    k, S = slots.shape[1], y.shape[0]
+    a, lda = _matrix(x, "x", torch.bfloat16, (T, H))
+    b, ldb = _matrix(y, "y", torch.bfloat16, (S, H))
+    o, ldo = _matrix(other, "other", torch.bfloat16, (S, H), optional=True)
+    _check(load().qz_dispatch_experts(a, lda, _tensor(slots, "slots", torch.int32, (T, k)),
+                                      _tensor(rows, "rows", torch.int32, (S,)), T, k, S, H,
+                                      _tensor(weights, "weights", torch.float32, (T, k), optional=True), b, ldb, o,
+                                      ldo, _tensor(dots, "dots", torch.float32, (T, k), optional=True),
+                                      _stream_ptr(stream)), "qz_dispatch_experts")
+    return y
+
+
+def combine_experts(y: torch.Tensor, slots: torch.Tensor, out: torch.Tensor, *, weights=None, residual=None,
+                    stream=None):
+    """Expert order to token order (qz_combine_experts): out[t] = residual[t] +
+    sum_j weights[t, j] * y[slots[t, j]] (a missing weight counts 1).  The
+    gradient of dispatch_experts."""
+    _require(y.dim() == 2 and slots.dim() == 2 and out.dim() == 2, "y must be [slots, H], slots [T, top_k], out [T, H]")
+    T, H = out.shape
+    S, k = y.shape[0], slots.shape[1]
+    a, lda = _matrix(y, "y", torch.bfloat16, (S, H))
+    o, ldo = _matrix(out, "out", torch.bfloat16, (T, H))
+    r, ldr = _matrix(residual, "residual", torch.bfloat16, (T, H), optional=True)
+    _check(load().qz_combine_experts(a, lda, _tensor(slots, "slots", torch.int32, (T, k)), T, k, S, H,
+                                     _tensor(weights, "weights", torch.float32, (T, k), optional=True), r, ldr, o, ldo,
+                                     _stream_ptr(stream)), "qz_combine_experts")
+    return out
+
+
+# ---------------------------------------------------------------------------
 # conveniences that allocate outputs with torch and call the entry points
 # ---------------------------------------------------------------------------
 
@@ -545,3 +918,41 @@ def quantize_experts(xs: Sequence[torch.Tensor], fmt: int, layout: int, mode: in
         rows, cols = e.x.shape
         e.sf = e.sf[: sf_bytes(rows, cols, fmt, layout)]
     return entries
+
+
+def quantize_expert_weights(w: torch.Tensor, fmt: int, stream=None):
+    """Quantize stacked bf16 expert weights [E, N, K] in one launch into the
+    form expert_product takes: (payload [E, N, K or K/2], swizzled scales
+    [E, region], NVFP4: amax [E], computed)."""
+    E, N, K = w.shape
+    q = torch.empty((E, N, K if fmt == FMT_MXFP8 else K // 2), dtype=torch.uint8, device=w.device)
+    sf = torch.empty((E, sf_bytes(N, K, fmt, SF_SWIZZLED)), dtype=torch.uint8, device=w.device)
+    amax = torch.empty(E, dtype=torch.float32, device=w.device) if fmt == FMT_NVFP4 else None
+    table = ExpertTable([Entry(w[e], q[e], sf[e], None if amax is None else amax[e:e + 1]) for e in range(E)],
+                        device=w.device)
+    if fmt == FMT_MXFP8:
+        quantize_grouped_mxfp8(table, SF_SWIZZLED, stream)
+    else:
+        quantize_grouped_nvfp4(table, NVFP4_PER_TENSOR_COMPUTE, SF_SWIZZLED, stream)
+    return q, sf, amax
+
+
+def quantize_tokens(x: torch.Tensor, fmt: int, stream=None):
+    """Quantize bf16 rows [R, K] into the form expert_product takes as x:
+    (payload, linear scales [R, K/block], NVFP4: amax [R], one per row)."""
+    R, K = x.shape
+    (e,) = quantize_experts([x], fmt, SF_LINEAR, NVFP4_PER_ROW, stream=stream)
+    return e.q, e.sf.view(R, -1), (None if e.amax is None else e.amax[:R])
+
+
+def quantize_slots_colwise(x: torch.Tensor, fmt: int, amax: Optional[torch.Tensor] = None, stream=None):
+    """Quantize bf16 [slots, n] down its columns into the form
+    expert_weight_grad takes: (payload [n, slots or slots/2], swizzled scales,
+    NVFP4: amax [1], max |x| unless given)."""
+    S, n = x.shape
+    q = torch.empty((n, S if fmt == FMT_MXFP8 else S // 2), dtype=torch.uint8, device=x.device)
+    sf = torch.empty(max(sf_bytes(n, S, fmt, SF_SWIZZLED), 16), dtype=torch.uint8, device=x.device)
+    if fmt == FMT_NVFP4 and amax is None:
+        amax = x.abs().amax().to(torch.float32).reshape(1)
+    quantize_grouped_colwise(ExpertTable([Entry(x, q, sf, amax)]), fmt, SF_SWIZZLED, stream)
+    return q, sf, amax

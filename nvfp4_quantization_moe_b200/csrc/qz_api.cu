@@ -43,6 +43,25 @@ cudaError_t launch_split_fused(const qz_fused_split* table, int n, int fmt, int 
 int split_blocks_per_sm(int n);
 cudaError_t launch_attention_merge(const float* O, const float* lse, int S, int64_t T, int64_t H, uint16_t* y,
                                    uint8_t* q, uint8_t* sf, int layout, cudaStream_t s);
+cudaError_t launch_route(const void* logits, int type, int64_t T, int E, int64_t ld, const float* bias,
+                         const qz_router& r, int32_t* ids, float* weights, cudaStream_t s);
+cudaError_t launch_route_grad(const void* logits, int type, int64_t T, int E, int64_t ld, const qz_router& r,
+                              const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd, cudaStream_t s);
+size_t plan_bytes(int64_t n, int E);
+cudaError_t launch_plan(const int32_t* ids, int64_t T, int k, int E, int align, int64_t slots, int32_t* offsets,
+                        int32_t* counts, int32_t* rows, int32_t* pair_slots, void* ws, cudaStream_t s);
+cudaError_t launch_product(const qz_product& p, cudaStream_t s, unsigned* d_err);
+cudaError_t launch_weight_grad(const qz_weight_grad& p, cudaStream_t s, unsigned* d_err);
+cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p, int64_t slots,
+                            int64_t n, int act, bool gated, const int32_t* offsets, const int32_t* counts,
+                            int n_experts, uint16_t* dpre, int64_t ld_q, float* dbias, cudaStream_t s,
+                            unsigned* d_err);
+cudaError_t launch_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* slots, const int32_t* rows, int64_t T,
+                            int k, int64_t n_slots, int64_t H, const float* weights, uint16_t* y, int64_t ld_y,
+                            const uint16_t* other, int64_t ld_o, float* dots, cudaStream_t s);
+cudaError_t launch_combine(const uint16_t* y, int64_t ld_y, const int32_t* slots, int64_t T, int k, int64_t n_slots,
+                           int64_t H, const float* weights, const uint16_t* residual, int64_t ld_r, uint16_t* out,
+                           int64_t ld_o, cudaStream_t s);
 }  // namespace qz
 
 namespace {
@@ -141,6 +160,34 @@ int sized_grid(int kind, const qz_launch_opts* opts) {
     }
     if (opts && opts->max_ctas > 0 && opts->max_ctas < grid) grid = opts->max_ctas;
     return grid;
+}
+
+constexpr int64_t kMaxIndex = 0x7FFFFFFFLL;  // slots, rows and tokens are int32 on the device
+
+bool finite(float v) { return v - v == 0.0f; }
+
+// The router arguments that the forward and the gradient share.
+qz_status check_router(const void* logits, int type, int64_t T, int E, int64_t ld, const qz_router* r) {
+    if (!r || (type != QZ_TYPE_BF16 && type != QZ_TYPE_F32)) return QZ_ERR_INVALID_ARG;
+    if (T < 0 || T > kMaxIndex / QZ_MAX_TOP_K || E < 1 || E > QZ_MAX_ROUTE_EXPERTS || ld < E) return QZ_ERR_INVALID_ARG;
+    if (r->score != QZ_SCORE_SOFTMAX && r->score != QZ_SCORE_SIGMOID) return QZ_ERR_INVALID_ARG;
+    if (r->top_k < 1 || r->top_k > QZ_MAX_TOP_K || r->top_k > E || !finite(r->scale)) return QZ_ERR_INVALID_ARG;
+    if (T > 0 && !logits) return QZ_ERR_INVALID_ARG;
+    if (!aligned(logits, type == QZ_TYPE_BF16 ? 2 : 4)) return QZ_ERR_ALIGNMENT;
+    return QZ_OK;
+}
+
+// A row stride of a bf16 matrix of `cols` columns read 16 bytes at a time.
+bool valid_ld(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0 && ld <= QZ_MAX_LD; }
+
+bool valid_activation(int a) { return a >= QZ_ACT_NONE && a <= QZ_ACT_GELU; }
+
+qz_status check_rows(const void* a, const void* b, const int32_t* slots, int64_t T, int top_k, int64_t n_slots,
+                     int64_t H) {
+    if (T < 0 || T > kMaxIndex || n_slots < 0 || n_slots > kMaxIndex) return QZ_ERR_INVALID_ARG;
+    if (top_k < 1 || top_k > QZ_MAX_TOP_K || H < 8 || H % 8 != 0 || H > QZ_MAX_LD) return QZ_ERR_INVALID_ARG;
+    if ((T > 0 && !slots) || (T > 0 && !a) || (n_slots > 0 && !b)) return QZ_ERR_INVALID_ARG;
+    return QZ_OK;
 }
 
 }  // namespace
@@ -369,6 +416,169 @@ qz_status qz_ipc_import(const qz_ipc_handle* h, void** d_ptr_out) {
 qz_status qz_ipc_close(void* d_ptr, const qz_ipc_handle* h) {
     if (!d_ptr || !h) return QZ_ERR_INVALID_ARG;
     return from_cuda(cudaIpcCloseMemHandle(static_cast<char*>(d_ptr) - h->offset));
+}
+
+qz_status qz_route_experts(const void* d_logits, int type, int64_t T, int E, int64_t ld, const float* d_bias,
+                           const qz_router* router, int32_t* d_ids, float* d_weights, void* stream) {
+    qz_status st = check_router(d_logits, type, T, E, ld, router);
+    if (st != QZ_OK) return st;
+    if (router->n_groups < 1 || router->n_groups > QZ_MAX_GROUPS || E % router->n_groups != 0) return QZ_ERR_INVALID_ARG;
+    if (router->top_groups < 1 || router->top_groups > router->n_groups ||
+        router->top_k > router->top_groups * (E / router->n_groups))
+        return QZ_ERR_INVALID_ARG;
+    if (T == 0) return QZ_OK;
+    if (!d_ids || !d_weights) return QZ_ERR_INVALID_ARG;
+    if (!aligned(d_ids, 4) || !aligned(d_weights, 4) || !aligned(d_bias, 4)) return QZ_ERR_ALIGNMENT;
+    return from_cuda(qz::launch_route(d_logits, type, T, E, ld, d_bias, *router, d_ids, d_weights,
+                                      (cudaStream_t)stream));
+}
+
+qz_status qz_route_experts_grad(const void* d_logits, int type, int64_t T, int E, int64_t ld, const qz_router* router,
+                                const int32_t* d_ids, const float* d_dweights, void* d_dlogits, int64_t ldd,
+                                void* stream) {
+    qz_status st = check_router(d_logits, type, T, E, ld, router);
+    if (st != QZ_OK) return st;
+    if (ldd < E) return QZ_ERR_INVALID_ARG;
+    if (T == 0) return QZ_OK;
+    if (!d_ids || !d_dweights || !d_dlogits) return QZ_ERR_INVALID_ARG;
+    if (!aligned(d_ids, 4) || !aligned(d_dweights, 4) || !aligned(d_dlogits, type == QZ_TYPE_BF16 ? 2 : 4))
+        return QZ_ERR_ALIGNMENT;
+    return from_cuda(qz::launch_route_grad(d_logits, type, T, E, ld, *router, d_ids, d_dweights, d_dlogits, ldd,
+                                           (cudaStream_t)stream));
+}
+
+int64_t qz_plan_slots(int64_t T, int top_k, int E, int align) {
+    if (T < 0 || T > kMaxIndex / QZ_MAX_TOP_K || top_k < 1 || top_k > QZ_MAX_TOP_K) return 0;
+    if (E < 1 || E > QZ_MAX_ROUTE_EXPERTS || align < 1 || align > 1024 || (align & (align - 1)) != 0) return 0;
+    const int64_t n = T * top_k;
+    const int64_t s = (n + (E < n ? E : n) * (align - 1) + align - 1) / align * align;
+    return s <= kMaxIndex ? s : 0;
+}
+
+size_t qz_plan_bytes(int64_t T, int top_k, int E) {
+    if (T < 0 || T > kMaxIndex / QZ_MAX_TOP_K || top_k < 1 || top_k > QZ_MAX_TOP_K) return 0;
+    if (E < 1 || E > QZ_MAX_ROUTE_EXPERTS) return 0;
+    return qz::plan_bytes(T * top_k, E);
+}
+
+qz_status qz_plan_experts(const int32_t* d_ids, int64_t T, int top_k, int E, int align, int32_t* d_offsets,
+                          int32_t* d_counts, int32_t* d_rows, int32_t* d_slots, void* d_workspace,
+                          size_t workspace_bytes, void* stream) {
+    if (T < 0 || T > kMaxIndex / QZ_MAX_TOP_K || top_k < 1 || top_k > QZ_MAX_TOP_K) return QZ_ERR_INVALID_ARG;
+    if (E < 1 || E > QZ_MAX_ROUTE_EXPERTS || align < 1 || align > 1024 || (align & (align - 1)) != 0)
+        return QZ_ERR_INVALID_ARG;
+    const int64_t slots = qz_plan_slots(T, top_k, E, align);
+    if (!d_offsets || !d_counts || (T > 0 && (slots == 0 || !d_ids || !d_rows || !d_slots))) return QZ_ERR_INVALID_ARG;
+    const size_t need = qz::plan_bytes(T * top_k, E);
+    if (need > 0 && (!d_workspace || workspace_bytes < need)) return QZ_ERR_INVALID_ARG;
+    if (!aligned(d_ids, 4) || !aligned(d_offsets, 4) || !aligned(d_counts, 4) || !aligned(d_rows, 4) ||
+        !aligned(d_slots, 4) || !aligned(d_workspace, 4))
+        return QZ_ERR_ALIGNMENT;
+    return from_cuda(qz::launch_plan(d_ids, T, top_k, E, align, slots, d_offsets, d_counts, d_rows, d_slots,
+                                     d_workspace, (cudaStream_t)stream));
+}
+
+qz_status qz_expert_product(const qz_product* p, void* stream, const qz_launch_opts* opts) {
+    if (!p) return QZ_ERR_INVALID_ARG;
+    if (p->fmt != QZ_FMT_MXFP8 && p->fmt != QZ_FMT_NVFP4) return QZ_ERR_INVALID_ARG;
+    if (!valid_activation(p->activation)) return QZ_ERR_INVALID_ARG;
+    if (p->n_experts < 1 || p->n_experts > QZ_MAX_ROUTE_EXPERTS) return QZ_ERR_INVALID_ARG;
+    if (p->n < 8 || p->n % 8 != 0 || p->n > QZ_MAX_LD || p->k < 32 || p->k % 32 != 0 || p->k > QZ_MAX_LD)
+        return QZ_ERR_INVALID_ARG;
+    if (p->x_rows < 0 || p->x_rows > kMaxIndex || p->slots < 0 || p->slots > kMaxIndex) return QZ_ERR_INVALID_ARG;
+    const bool gated = p->up_q != nullptr, fp4 = p->fmt == QZ_FMT_NVFP4;
+    const int64_t row_bytes = fp4 ? p->k / 2 : p->k;
+    if (p->w_stride < p->n * row_bytes || p->w_stride % 16 != 0) return QZ_ERR_INVALID_ARG;
+    if (p->w_sf_stride < (int64_t)qz_sf_bytes(p->n, p->k, p->fmt, QZ_SF_SWIZZLED_128x4) || p->w_sf_stride % 16 != 0)
+        return QZ_ERR_INVALID_ARG;
+    if (!valid_ld(p->ld_out, p->n) || (p->residual && !valid_ld(p->ld_residual, p->n)) ||
+        (p->pre && !valid_ld(p->ld_pre, gated ? 2 * p->n : p->n)))
+        return QZ_ERR_INVALID_ARG;
+    if (!gated && (p->up_sf || p->up_amax || p->up_bias)) return QZ_ERR_INVALID_ARG;
+    if (p->q && (p->n % 32 != 0 || !p->sf)) return QZ_ERR_INVALID_ARG;
+    if (p->slots == 0) return QZ_OK;
+    if (!p->d_offsets || !p->d_counts || !p->w_q || !p->w_sf || !p->out) return QZ_ERR_INVALID_ARG;
+    if (p->x_rows > 0 && (!p->x_q || !p->x_sf || (fp4 && !p->x_amax))) return QZ_ERR_INVALID_ARG;
+    if (gated && (!p->up_sf || (fp4 && !p->up_amax))) return QZ_ERR_INVALID_ARG;
+    if (fp4 && !p->w_amax) return QZ_ERR_INVALID_ARG;
+    if (!aligned(p->x_q, 16) || !aligned(p->w_q, 16) || !aligned(p->up_q, 16) || !aligned(p->w_sf, 16) ||
+        !aligned(p->up_sf, 16) || !aligned(p->out, 16) || !aligned(p->residual, 16) || !aligned(p->pre, 16) ||
+        !aligned(p->q, 16) || !aligned(p->bias, 16) || !aligned(p->up_bias, 16))
+        return QZ_ERR_ALIGNMENT;
+    if (!aligned(p->x_sf, 4) || !aligned(p->x_amax, 4) || !aligned(p->w_amax, 4) || !aligned(p->up_amax, 4) ||
+        !aligned(p->d_rows, 4) || !aligned(p->d_offsets, 4) || !aligned(p->d_counts, 4))
+        return QZ_ERR_ALIGNMENT;
+    return from_cuda(qz::launch_product(*p, (cudaStream_t)stream, err_word(opts)));
+}
+
+qz_status qz_expert_weight_grad(const qz_weight_grad* p, void* stream, const qz_launch_opts* opts) {
+    if (!p) return QZ_ERR_INVALID_ARG;
+    if (p->fmt != QZ_FMT_MXFP8 && p->fmt != QZ_FMT_NVFP4) return QZ_ERR_INVALID_ARG;
+    if (p->out_type != QZ_TYPE_BF16 && p->out_type != QZ_TYPE_F32) return QZ_ERR_INVALID_ARG;
+    if (p->n_experts < 1 || p->n_experts > QZ_MAX_ROUTE_EXPERTS) return QZ_ERR_INVALID_ARG;
+    if (p->n < 8 || p->n % 8 != 0 || p->n > QZ_MAX_LD || p->k < 8 || p->k % 8 != 0 || p->k > QZ_MAX_LD)
+        return QZ_ERR_INVALID_ARG;
+    if (p->slots < 0 || p->slots % 32 != 0 || p->slots > kMaxIndex) return QZ_ERR_INVALID_ARG;
+    if (!p->d_offsets || !p->d_counts || !p->out) return QZ_ERR_INVALID_ARG;
+    if (p->slots > 0 && (!p->dz_q || !p->dz_sf || !p->x_q || !p->x_sf)) return QZ_ERR_INVALID_ARG;
+    if (p->slots > 0 && p->fmt == QZ_FMT_NVFP4 && (!p->dz_amax || !p->x_amax)) return QZ_ERR_INVALID_ARG;
+    if (!aligned(p->dz_q, 16) || !aligned(p->x_q, 16) || !aligned(p->dz_sf, 16) || !aligned(p->x_sf, 16) ||
+        !aligned(p->out, 16))
+        return QZ_ERR_ALIGNMENT;
+    if (!aligned(p->dz_amax, 4) || !aligned(p->x_amax, 4) || !aligned(p->d_offsets, 4) || !aligned(p->d_counts, 4))
+        return QZ_ERR_ALIGNMENT;
+    return from_cuda(qz::launch_weight_grad(*p, (cudaStream_t)stream, err_word(opts)));
+}
+
+qz_status qz_expert_activation_grad(const void* d_dout, int64_t ld_dout, const void* d_pre, int64_t ld_pre,
+                                    int64_t slots, int64_t n, int activation, int gated, const int32_t* d_offsets,
+                                    const int32_t* d_counts, int n_experts, void* d_dpre, int64_t ld_dpre,
+                                    float* d_dbias, void* stream, const qz_launch_opts* opts) {
+    const int64_t width = gated ? 2 * n : n;
+    if (!valid_activation(activation) || n_experts < 1 || n_experts > QZ_MAX_ROUTE_EXPERTS) return QZ_ERR_INVALID_ARG;
+    if (slots < 0 || slots > kMaxIndex || n < 8 || n % 8 != 0 || n > QZ_MAX_LD) return QZ_ERR_INVALID_ARG;
+    if (!valid_ld(ld_dout, n) || !valid_ld(ld_pre, width) || !valid_ld(ld_dpre, width)) return QZ_ERR_INVALID_ARG;
+    if (!d_offsets || !d_counts || (slots > 0 && (!d_dout || !d_pre || !d_dpre))) return QZ_ERR_INVALID_ARG;
+    if (!aligned(d_dout, 16) || !aligned(d_pre, 16) || !aligned(d_dpre, 16) || !aligned(d_dbias, 4) ||
+        !aligned(d_offsets, 4) || !aligned(d_counts, 4))
+        return QZ_ERR_ALIGNMENT;
+    return from_cuda(qz::launch_act_grad(static_cast<const uint16_t*>(d_dout), ld_dout,
+                                         static_cast<const uint16_t*>(d_pre), ld_pre, slots, n, activation, gated != 0,
+                                         d_offsets, d_counts, n_experts, static_cast<uint16_t*>(d_dpre), ld_dpre,
+                                         d_dbias, (cudaStream_t)stream, err_word(opts)));
+}
+
+qz_status qz_dispatch_experts(const void* d_x, int64_t ld_x, const int32_t* d_slots, const int32_t* d_rows, int64_t T,
+                              int top_k, int64_t slots, int64_t H, const float* d_weights, void* d_y, int64_t ld_y,
+                              const void* d_other, int64_t ld_other, float* d_dots, void* stream) {
+    qz_status st = check_rows(d_x, d_y, d_slots, T, top_k, slots, H);
+    if (st != QZ_OK) return st;
+    if (!valid_ld(ld_x, H) || !valid_ld(ld_y, H) || (d_other && !valid_ld(ld_other, H))) return QZ_ERR_INVALID_ARG;
+    if ((d_other != nullptr) != (d_dots != nullptr) || (slots > 0 && !d_rows)) return QZ_ERR_INVALID_ARG;
+    if (!aligned(d_x, 16) || !aligned(d_y, 16) || !aligned(d_other, 16) || !aligned(d_slots, 4) ||
+        !aligned(d_rows, 4) || !aligned(d_weights, 4) || !aligned(d_dots, 4))
+        return QZ_ERR_ALIGNMENT;
+    if (T == 0 && slots == 0) return QZ_OK;
+    return from_cuda(qz::launch_dispatch(static_cast<const uint16_t*>(d_x), ld_x, d_slots, d_rows, T, top_k, slots, H,
+                                         d_weights, static_cast<uint16_t*>(d_y), ld_y,
+                                         static_cast<const uint16_t*>(d_other), ld_other, d_dots,
+                                         (cudaStream_t)stream));
+}
+
+qz_status qz_combine_experts(const void* d_y, int64_t ld_y, const int32_t* d_slots, int64_t T, int top_k,
+                             int64_t slots, int64_t H, const float* d_weights, const void* d_residual,
+                             int64_t ld_residual, void* d_out, int64_t ld_out, void* stream) {
+    qz_status st = check_rows(d_out, d_y, d_slots, T, top_k, slots, H);
+    if (st != QZ_OK) return st;
+    if (!valid_ld(ld_y, H) || !valid_ld(ld_out, H) || (d_residual && !valid_ld(ld_residual, H)))
+        return QZ_ERR_INVALID_ARG;
+    if (!aligned(d_y, 16) || !aligned(d_out, 16) || !aligned(d_residual, 16) || !aligned(d_slots, 4) ||
+        !aligned(d_weights, 4))
+        return QZ_ERR_ALIGNMENT;
+    if (T == 0) return QZ_OK;
+    return from_cuda(qz::launch_combine(static_cast<const uint16_t*>(d_y), ld_y, d_slots, T, top_k, slots, H,
+                                        d_weights, static_cast<const uint16_t*>(d_residual), ld_residual,
+                                        static_cast<uint16_t*>(d_out), ld_out, (cudaStream_t)stream));
 }
 
 size_t qz_workspace_bytes(int n_experts) {

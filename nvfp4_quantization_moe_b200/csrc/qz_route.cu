@@ -1,0 +1,585 @@
+// qz_route.cu -- the router of a mixture-of-experts layer (sm_100a): scores,
+// group limit, top-k choice and weights; its gradient; and the expert order
+// (plan) of the choices.
+//
+// Router.  One warp owns one token: lane l holds the logits of experts
+// l, l + 32, ... in registers, so a row is read once and every reduction is a
+// warp reduction.  The choice is top_k rounds of a warp-wide argmax over
+// order-preserving integer keys (redux.sync on the key, then on the index,
+// which gives ties to the lower index).  Without a bias the key is the fp32
+// logit itself.  With a bias (and for group values) two experts may differ by
+// less than an fp32 rounding of the score, so the key is formed in binary64.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <float.h>
+
+#include <type_traits>
+
+#include "../../include/qz.h"
+#include "qz_device.cuh"
+
+namespace qz {
+
+constexpr int kRouteWarps = 4;  // tokens per CTA
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    int64_t T, ld;
+    int E, k, score, n_groups, top_groups, renorm;
+    float scale;
+    int32_t* ids;
+    float* weights;
+};
+
+// A logit as the router reads it: NaN masks like -inf, +inf counts as FLT_MAX.
+__device__ __forceinline__ float clean_logit(float x) { return x != x ? -INFINITY : fminf(x, FLT_MAX); }
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+    if (BF16) return clean_logit(__uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16));
+    return clean_logit(__ldg(static_cast<const float*>(p) + i));
+}
+
+// Order-preserving integers: a < b exactly when key(a) < key(b); 0 is below
+// the key of every number above -inf and stands for a masked expert.
+__device__ __forceinline__ uint32_t key32(float v) {
+    if (!(v > -INFINITY)) return 0u;
+    v = v + 0.0f;  // -0 and +0 are one value
+    const uint32_t b = __float_as_uint(v);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ unsigned long long key64(double v) {
+    if (!(v > -INFINITY)) return 0ull;
+    v = v + 0.0;
+    const unsigned long long b = (unsigned long long)__double_as_longlong(v);
+    return (b & 0x8000000000000000ull) ? ~b : (b | 0x8000000000000000ull);
+}
+
+// Largest value of a warp and the lowest index that has it.
+__device__ __forceinline__ uint32_t warp_best(uint32_t key, uint32_t& idx) {
+    const uint32_t top = __reduce_max_sync(kFull, key);
+    idx = __reduce_min_sync(kFull, key == top ? idx : 0xFFFFFFFFu);
+    return top;
+}
+
+__device__ __forceinline__ unsigned long long warp_best(unsigned long long key, uint32_t& idx) {
+    const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(key >> 32));
+    const bool in = (uint32_t)(key >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(kFull, in ? (uint32_t)key : 0u);
+    idx = __reduce_min_sync(kFull, in && (uint32_t)key == lo ? idx : 0xFFFFFFFFu);
+    return ((unsigned long long)hi << 32) | lo;
+}
+
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+__device__ __forceinline__ double sigmoid64(double x) {
+    const double e = exp(-fabs(x));  // at most 1: no overflow on either side
+    return (x >= 0 ? 1.0 : e) / (1.0 + e);
+}
+
+// x[i] for a warp-uniform register index i.
+template <int PER>
+__device__ __forceinline__ float pick(const float (&x)[PER], int i) {
+    float v = x[0];
+#pragma unroll
+    for (int j = 1; j < PER; ++j)
+        if (j == i) v = x[j];
+    return v;
+}
+
+// KEY: float when the logits themselves order the experts, double when biased
+// scores do.  GROUPS: the group limit applies (its values are binary64 too).
+template <int PER, bool BF16, typename KEY, bool GROUPS>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
+    extern __shared__ double s_values[];  // GROUPS: [warps][E]
+    typedef typename std::conditional<sizeof(KEY) == 8, unsigned long long, uint32_t>::type Key;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    float x[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = lane + 32 * j;
+        x[j] = i < a.E ? load_logit<BF16>(a.logits, t * a.ld + i) : -INFINITY;
+    }
+    float m = x[0];
+#pragma unroll
+    for (int j = 1; j < PER; ++j) m = fmaxf(m, x[j]);
+    m = warp_max(m);
+    const bool sigmoid = a.score == QZ_SCORE_SIGMOID;
+
+    Key key[PER];
+    double sum64 = 1.0;
+    if (sizeof(KEY) == 8 || GROUPS) {
+        // binary64 scores: the keys of a biased choice, the terms of a group's value
+        double s[PER];
+        double part = 0.0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            if (!(x[j] > -INFINITY)) s[j] = 0.0;
+            else s[j] = sigmoid ? sigmoid64((double)x[j]) : exp((double)x[j] - (double)m);
+            part += s[j];
+        }
+        if (!sigmoid) {
+            sum64 = warp_sum(part);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) s[j] = s[j] / sum64;
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = lane + 32 * j;
+            double v = s[j];
+            if (a.bias != nullptr && i < a.E) v += (double)__ldg(a.bias + i);
+            if (!(x[j] > -INFINITY) || v != v) v = -INFINITY;
+            if (sizeof(KEY) == 8) key[j] = (Key)key64(v);
+            else key[j] = (Key)key32(x[j]);
+            if (GROUPS && i < a.E) s_values[warp * a.E + i] = v;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) key[j] = (Key)key32(x[j]);
+    }
+    if (GROUPS) {
+        // lane g sums the two largest values of group g, then keeps it if
+        // fewer than top_groups groups come before it
+        __syncwarp();
+        const int size = a.E / a.n_groups;
+        double b1 = -INFINITY, b2 = -INFINITY;
+        if (lane < a.n_groups) {
+            const double* v = s_values + warp * a.E + lane * size;
+            for (int i = 0; i < size; ++i) {
+                const double u = v[i];
+                b2 = fmax(b2, fmin(b1, u));
+                b1 = fmax(b1, u);
+            }
+        }
+        const double value = b2 > -INFINITY ? b1 + b2 : b1;
+        int before = 0;
+        for (int g = 0; g < a.n_groups; ++g) {
+            const double other = __shfl_sync(kFull, value, g);
+            if (other > value || (other == value && g < lane)) ++before;
+        }
+        const unsigned kept = __ballot_sync(kFull, lane < a.n_groups && before < a.top_groups);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = lane + 32 * j;
+            if (i < a.E && !((kept >> (i / size)) & 1u)) key[j] = 0;
+        }
+    }
+
+    // lane j ends up with choice j
+    int id = -1;
+    float chosen = -INFINITY;
+    for (int c = 0; c < a.k; ++c) {
+        Key best = key[0];
+        uint32_t idx = lane;
+#pragma unroll
+        for (int j = 1; j < PER; ++j) {
+            if (key[j] > best) {
+                best = key[j];
+                idx = lane + 32 * j;
+            }
+        }
+        const Key top = warp_best(best, idx);
+        if (top == 0) break;  // no expert is left
+        const int at = (int)(idx >> 5), from = (int)(idx & 31);
+        const float v = __shfl_sync(kFull, pick<PER>(x, at), from);
+        if (lane == c) {
+            id = (int)idx;
+            chosen = v;
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (j == at && lane == from) key[j] = 0;
+    }
+
+    // weights: the chosen scores, in binary64 for a sigmoid (whose value may be
+    // far below 1 for every choice), relative to the largest chosen logit for
+    // a renormalized softmax
+    const bool live = id >= 0;
+    float w = 0.0f;
+    if (sigmoid) {
+        const double s = live ? sigmoid64((double)chosen) : 0.0;
+        const double total = a.renorm ? warp_sum(s) : 1.0;
+        w = total > 0.0 ? (float)(s / total) : 0.0f;
+    } else if (a.renorm) {
+        const float top = warp_max(chosen);
+        const float s = live ? expf(chosen - top) : 0.0f;
+        const float total = warp_sum(s);
+        w = live ? s / total : 0.0f;
+    } else if (sizeof(KEY) == 8 || GROUPS) {
+        w = live ? (float)(exp((double)chosen - (double)m) / sum64) : 0.0f;
+    } else {
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) part += x[j] > -INFINITY ? expf(x[j] - m) : 0.0f;
+        const float total = warp_sum(part);
+        w = live ? expf(chosen - m) / total : 0.0f;
+    }
+    if (lane < a.k) {
+        a.ids[t * a.k + lane] = id;
+        a.weights[t * a.k + lane] = w * a.scale;
+    }
+}
+
+struct RouteGradArgs {
+    const void* logits;
+    const int32_t* ids;
+    const float* dweights;
+    void* dlogits;
+    int64_t T, ld, ldd;
+    int E, k, score, renorm;
+    float scale;
+};
+
+// One warp per token again: lane j holds choice j and its incoming gradient,
+// the dense row of gradients is accumulated in the lanes' registers in choice
+// order (so a repeated id adds in a fixed order) and written once.
+template <int PER, bool BF16>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(RouteGradArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    const bool sigmoid = a.score == QZ_SCORE_SIGMOID;
+    int id = -1;
+    float g = 0.0f;
+    if (lane < a.k) {
+        id = __ldg(a.ids + t * a.k + lane);
+        g = __ldg(a.dweights + t * a.k + lane) * a.scale;
+        if (id < 0 || id >= a.E) id = -1;
+    }
+    float chosen = id >= 0 ? load_logit<BF16>(a.logits, t * a.ld + id) : -INFINITY;
+    const bool live = id >= 0 && chosen > -INFINITY;
+    if (!live) g = 0.0f;
+
+    float x[PER];
+    float d[PER];
+    float dot = 0.0f, m = 0.0f, total = 1.0f;
+    const bool dense = !sigmoid && !a.renorm;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) d[j] = 0.0f;
+    float v = 0.0f;  // what choice j adds to its expert's gradient
+    if (sigmoid) {
+        const float e = expf(-fabsf(chosen));
+        const float s = live ? (chosen >= 0 ? 1.0f : e) / (1.0f + e) : 0.0f;
+        const float rest = (chosen >= 0 ? e : 1.0f) / (1.0f + e);  // 1 - s without cancellation
+        if (a.renorm) {
+            // relative to the largest chosen score, so that a row of tiny scores keeps its ratios
+            const float top = warp_max(chosen);
+            const float et = expf(-fabsf(top));
+            const float lead = (top >= 0 ? 1.0f : et) / (1.0f + et);
+            const float r = live && lead > 0.0f ? s / lead : 0.0f;
+            const float S = warp_sum(r);
+            const float w = S > 0.0f ? r / S : 0.0f;
+            dot = warp_sum(g * w);
+            v = live ? w * (g - dot) * rest : 0.0f;
+        } else {
+            v = live ? g * s * rest : 0.0f;
+        }
+    } else if (a.renorm) {
+        const float top = warp_max(chosen);
+        const float s = live ? expf(chosen - top) : 0.0f;
+        const float S = warp_sum(s);
+        const float w = live ? s / S : 0.0f;
+        dot = warp_sum(g * w);
+        v = live ? w * (g - dot) : 0.0f;
+    } else {
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = lane + 32 * j;
+            x[j] = i < a.E ? load_logit<BF16>(a.logits, t * a.ld + i) : -INFINITY;
+        }
+        m = x[0];
+#pragma unroll
+        for (int j = 1; j < PER; ++j) m = fmaxf(m, x[j]);
+        m = warp_max(m);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            x[j] = x[j] > -INFINITY ? expf(x[j] - m) : 0.0f;
+            part += x[j];
+        }
+        total = warp_sum(part);
+        const float p = live ? expf(chosen - m) / total : 0.0f;
+        dot = warp_sum(g * p);
+        v = g * p;
+    }
+    for (int c = 0; c < a.k; ++c) {
+        const int i = __shfl_sync(kFull, id, c);
+        const float add = __shfl_sync(kFull, v, c);
+        if (i < 0) continue;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (i == lane + 32 * j) d[j] += add;
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = lane + 32 * j;
+        if (i >= a.E) continue;
+        if (dense && total > 0.0f) d[j] -= x[j] / total * dot;
+        if (BF16) {
+            uint16_t r;
+            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(d[j]));
+            static_cast<uint16_t*>(a.dlogits)[t * a.ldd + i] = r;
+        } else {
+            static_cast<float*>(a.dlogits)[t * a.ldd + i] = d[j];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the expert order
+// ---------------------------------------------------------------------------
+//
+// A stable counting sort.  The pairs are cut into one chunk per CTA, a chunk
+// into one contiguous piece per warp; a warp ranks its pairs 32 at a time with
+// match_any, on top of the counts of everything before it (other chunks, then
+// the warps before it in the chunk).  One launch when one chunk holds all
+// pairs; otherwise a launch that counts each chunk and one that places.
+
+constexpr int kPlanWarps = 16;
+constexpr int kPlanChunk = 4096;  // least pairs of a chunk when there are several
+constexpr int kPlanMost = 128;    // most chunks: each CTA of the second launch reads every chunk's counts
+constexpr int kPlanOne = 8192;    // pairs up to which one CTA sorts alone
+
+struct PlanArgs {
+    const int32_t* ids;
+    int64_t n;  // pairs
+    int64_t slots;
+    int k, E, align;
+    int chunks;
+    int64_t chunk;  // pairs per chunk
+    int32_t *offsets, *counts, *rows, *pair_slots;
+    int* hist;  // [chunks][E] counts of each chunk
+};
+
+// The CTA's counts per warp and expert, s_cnt[warp][E].
+__device__ __forceinline__ void plan_count(const PlanArgs& a, int64_t begin, int64_t end, int64_t piece, int* s_cnt) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += blockDim.x) s_cnt[i] = 0;
+    __syncthreads();
+    const int64_t lo = begin + warp * piece, hi = min(end, lo + piece);
+    for (int64_t p = lo; p < hi; p += 32) {
+        const int64_t i = p + lane;
+        const int id = i < hi ? __ldg(a.ids + i) : -1;
+        const int e = id >= 0 && id < a.E ? id : -1;
+        const unsigned same = __match_any_sync(kFull, e);
+        if (e >= 0 && lane == __ffs(same) - 1) s_cnt[warp * a.E + e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kPlanWarps * 32) plan_count_kernel(PlanArgs a) {
+    extern __shared__ int s_cnt[];
+    const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(a.n, begin + a.chunk);
+    plan_count(a, begin, end, (a.chunk + kPlanWarps - 1) / kPlanWarps, s_cnt);
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int c = 0;
+        for (int w = 0; w < kPlanWarps; ++w) c += s_cnt[w * a.E + e];
+        a.hist[(int64_t)blockIdx.x * a.E + e] = c;
+    }
+    // unused slots read as -1; the placing launch fills in the others
+    for (int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; s < a.slots; s += (int64_t)gridDim.x * blockDim.x)
+        a.rows[s] = -1;
+}
+
+__global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a) {
+    extern __shared__ int s_cnt[];  // [warps][E], then [E] first slots, then [warps] scan scratch
+    int* s_first = s_cnt + kPlanWarps * a.E;
+    int* s_scan = s_first + a.E;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(a.n, begin + a.chunk);
+    const int64_t piece = (a.chunk + kPlanWarps - 1) / kPlanWarps;
+    plan_count(a, begin, end, piece, s_cnt);
+    if (a.chunks == 1) {
+        for (int64_t s = threadIdx.x; s < a.slots; s += blockDim.x) a.rows[s] = -1;
+    }
+    // per expert: all pairs (its count), and the pairs of the chunks before this one.
+    // E <= 1024 = 2 * threads, so a thread owns the experts 2i and 2i + 1.
+    int total[2] = {0, 0}, before[2] = {0, 0}, padded = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = 2 * threadIdx.x + h;
+        if (e >= a.E) continue;
+        if (a.chunks == 1) {
+            for (int w = 0; w < kPlanWarps; ++w) total[h] += s_cnt[w * a.E + e];
+        } else {
+            for (int c = 0; c < a.chunks; ++c) {
+                const int v = a.hist[(int64_t)c * a.E + e];
+                total[h] += v;
+                if (c < (int)blockIdx.x) before[h] += v;
+            }
+        }
+        padded += (total[h] + a.align - 1) & ~(a.align - 1);
+    }
+    int incl = padded;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int first = incl - padded;
+    for (int w = 0; w < warp; ++w) first += s_scan[w];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = 2 * threadIdx.x + h;
+        if (e >= a.E) continue;
+        s_first[e] = first + before[h];
+        if (blockIdx.x == 0) {
+            a.offsets[e] = first;
+            a.counts[e] = total[h];
+        }
+        first += (total[h] + a.align - 1) & ~(a.align - 1);
+        if (blockIdx.x == 0 && e == a.E - 1) a.offsets[a.E] = first;
+    }
+    __syncthreads();
+    // each warp's counter of an expert starts at the slot of its first pair there
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int at = s_first[e];
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int c = s_cnt[w * a.E + e];
+            s_cnt[w * a.E + e] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    const int64_t lo = begin + warp * piece, hi = min(end, lo + piece);
+    for (int64_t p = lo; p < hi; p += 32) {
+        const int64_t i = p + lane;
+        const int id = i < hi ? __ldg(a.ids + i) : -1;
+        const int e = id >= 0 && id < a.E ? id : -1;
+        const unsigned same = __match_any_sync(kFull, e);
+        int slot = -1;
+        if (e >= 0) slot = s_cnt[warp * a.E + e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) s_cnt[warp * a.E + e] += __popc(same);
+        __syncwarp();
+        if (i < hi) {
+            a.pair_slots[i] = slot;
+            if (slot >= 0) a.rows[slot] = (int)(i / a.k);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+template <int PER, bool BF16>
+static cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
+    const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
+    const int threads = kRouteWarps * 32;
+    const size_t smem = (size_t)kRouteWarps * a.E * sizeof(double);  // at most 32 KB
+    const bool groups = a.top_groups < a.n_groups;
+    if (a.bias && groups) route_kernel<PER, BF16, double, true><<<grid, threads, smem, s>>>(a);
+    else if (a.bias) route_kernel<PER, BF16, double, false><<<grid, threads, 0, s>>>(a);
+    else if (groups) route_kernel<PER, BF16, float, true><<<grid, threads, smem, s>>>(a);
+    else route_kernel<PER, BF16, float, false><<<grid, threads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool BF16>
+static cudaError_t route_sized(const RouteArgs& a, cudaStream_t s) {
+    const int per = (a.E + 31) / 32;
+    if (per <= 1) return route_launch<1, BF16>(a, s);
+    if (per <= 2) return route_launch<2, BF16>(a, s);
+    if (per <= 4) return route_launch<4, BF16>(a, s);
+    if (per <= 8) return route_launch<8, BF16>(a, s);
+    if (per <= 16) return route_launch<16, BF16>(a, s);
+    return route_launch<32, BF16>(a, s);
+}
+
+cudaError_t launch_route(const void* logits, int type, int64_t T, int E, int64_t ld, const float* bias,
+                         const qz_router& r, int32_t* ids, float* weights, cudaStream_t s) {
+    const RouteArgs a = {logits,       bias,          T,             ld,      E,  r.top_k, r.score, r.n_groups,
+                         r.top_groups, r.renormalize, r.scale, ids, weights};
+    return type == QZ_TYPE_BF16 ? route_sized<true>(a, s) : route_sized<false>(a, s);
+}
+
+template <bool BF16>
+static cudaError_t route_grad_sized(const RouteGradArgs& a, cudaStream_t s) {
+    const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
+    const int threads = kRouteWarps * 32, per = (a.E + 31) / 32;
+    if (per <= 1) route_grad_kernel<1, BF16><<<grid, threads, 0, s>>>(a);
+    else if (per <= 2) route_grad_kernel<2, BF16><<<grid, threads, 0, s>>>(a);
+    else if (per <= 4) route_grad_kernel<4, BF16><<<grid, threads, 0, s>>>(a);
+    else if (per <= 8) route_grad_kernel<8, BF16><<<grid, threads, 0, s>>>(a);
+    else if (per <= 16) route_grad_kernel<16, BF16><<<grid, threads, 0, s>>>(a);
+    else route_grad_kernel<32, BF16><<<grid, threads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_route_grad(const void* logits, int type, int64_t T, int E, int64_t ld, const qz_router& r,
+                              const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd, cudaStream_t s) {
+    const RouteGradArgs a = {logits, ids, dweights, dlogits, T, ld, ldd, E, r.top_k, r.score, r.renormalize, r.scale};
+    return type == QZ_TYPE_BF16 ? route_grad_sized<true>(a, s) : route_grad_sized<false>(a, s);
+}
+
+static int64_t plan_chunk(int64_t n) {
+    if (n <= kPlanOne) return n > 0 ? n : 1;
+    const int64_t c = (n + kPlanMost - 1) / kPlanMost;
+    return c > kPlanChunk ? c : kPlanChunk;
+}
+
+static int64_t plan_chunks(int64_t n) { return n > 0 ? (n + plan_chunk(n) - 1) / plan_chunk(n) : 1; }
+
+size_t plan_bytes(int64_t n, int E) {
+    const int64_t c = plan_chunks(n);
+    return c == 1 ? 0 : (size_t)c * (size_t)E * sizeof(int);
+}
+
+cudaError_t launch_plan(const int32_t* ids, int64_t T, int k, int E, int align, int64_t slots, int32_t* offsets,
+                        int32_t* counts, int32_t* rows, int32_t* pair_slots, void* ws, cudaStream_t s) {
+    PlanArgs a;
+    a.ids = ids;
+    a.n = T * k;
+    a.slots = slots;
+    a.k = k;
+    a.E = E;
+    a.align = align;
+    a.chunks = (int)plan_chunks(a.n);
+    a.chunk = plan_chunk(a.n);
+    a.offsets = offsets;
+    a.counts = counts;
+    a.rows = rows;
+    a.pair_slots = pair_slots;
+    a.hist = static_cast<int*>(ws);
+    const int threads = kPlanWarps * 32;
+    const size_t smem_count = (size_t)kPlanWarps * E * sizeof(int);
+    const size_t smem_place = smem_count + (size_t)(E + kPlanWarps) * sizeof(int);  // at most 68 KB
+    // asked for at its largest every time: the attribute is one value per device and
+    // a smaller value of another call must not take it back
+    const int most = (kPlanWarps * QZ_MAX_ROUTE_EXPERTS + QZ_MAX_ROUTE_EXPERTS + kPlanWarps) * (int)sizeof(int);
+    if (smem_place > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e != cudaSuccess) return e;
+    }
+    if (a.chunks > 1) {
+        plan_count_kernel<<<a.chunks, threads, smem_count, s>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    plan_place_kernel<<<a.chunks, threads, smem_place, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace qz

@@ -1,0 +1,509 @@
+"""The experts' products, their gradients and the moves between token order and
+expert order, against binary64."""
+import numpy as np
+import pytest
+import torch
+
+import moe_ref as ref
+import nvfp4_quantization_moe_b200 as qz
+
+pytestmark = pytest.mark.gpu
+MX, NV = qz.FMT_MXFP8, qz.FMT_NVFP4
+
+
+def stacked(g, E, N, K, fmt, std=0.1):
+    w = (ref.randn(g, E, N, K) * std).to(torch.bfloat16).cuda()
+    part = qz.quantize_expert_weights(w, fmt)
+    return part
+
+
+def weight64(part, e, K, fmt):
+    q, sf, amax = part
+    return ref.decode(q[e], sf[e], K, fmt == NV, True, None if amax is None else ref.decode_scale(amax[e].cpu()))
+
+
+def tokens64(part, K, fmt):
+    q, sf, amax = part
+    return ref.decode(q, sf, K, fmt == NV, False, None if amax is None else ref.decode_scale(amax.cpu()).reshape(-1, 1))
+
+
+def offsets_of(counts, align=1, gap=0):
+    padded = (counts + align - 1) // align * align + gap
+    return torch.cat([torch.zeros(1, dtype=torch.long), padded.cumsum(0)]).to(torch.int32)
+
+
+def run_product(fmt, counts, N, K, *, seed=0, gather=True, gated=False, act=qz.ACT_NONE, bias=False, residual=False,
+                pre=False, q=False, R=None, gap=0, pad=0, std=0.1, extra=0, max_ctas=0):
+    """One call against binary64; buffers carry a canary in every row that is not live and in the columns past N."""
+    g = ref.gen(seed + N + K)
+    E = len(counts)
+    counts = torch.tensor(counts)
+    offsets = offsets_of(counts, gap=gap)
+    S = int(offsets[-1]) + extra
+    R = (max(S // 2, 1) if gather else S) if R is None else R
+    x = qz.quantize_tokens((ref.randn(g, R, K)).to(torch.bfloat16).cuda(), fmt)
+    w = stacked(g, E, N, K, fmt, std)
+    up = stacked(g, E, N, K, fmt, std) if gated else None
+    rows = torch.randint(0, R, (S,), generator=g, dtype=torch.int32) if gather else None
+    if gather and S > 3:
+        rows[1] = -1
+        rows[2] = R
+    b = (ref.randn(g, E, N)).to(torch.bfloat16) if bias else None
+    ub = (ref.randn(g, E, N)).to(torch.bfloat16) if bias and gated else None
+    r = ref.randn(g, S, N + pad).to(torch.bfloat16) if residual else None
+    width = 2 * N if gated else N
+    out = torch.full((S, N + pad), 7.5, dtype=torch.bfloat16).cuda()
+    z = torch.full((S, width + pad), 7.5, dtype=torch.bfloat16).cuda() if pre else None
+    oq = torch.full((S, N), 0x5A, dtype=torch.uint8).cuda() if q else None
+    osf = torch.full((S, N // 32), 0x5A, dtype=torch.uint8).cuda() if q else None
+    err = torch.zeros(1, dtype=torch.int32).cuda()
+    cuda = lambda t: None if t is None else t.cuda()  # noqa: E731
+    qz.expert_product(fmt, x, w, offsets.cuda(), counts.to(torch.int32).cuda(), out[:, :N], rows=cuda(rows), up=up,
+                      bias=cuda(b), up_bias=cuda(ub), activation=act,
+                      residual=None if r is None else r.cuda()[:, :N], pre=None if z is None else z[:, :width], q=oq,
+                      sf=osf, err=err, max_ctas=max_ctas)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    A = tokens64(x, K, fmt)
+    A = torch.cat([A, torch.zeros(1, K, dtype=torch.float64)])
+    live = torch.zeros(S, dtype=torch.bool)
+    step = (K // 32 + 8) * 2.0 ** -22  # fp32 accumulation of one block of 32 products at a time, and the scales
+    for e in range(E):
+        at = torch.arange(int(offsets[e]), int(offsets[e]) + int(counts[e]))
+        if not len(at):
+            continue
+        live[at] = True
+        idx = rows[at].long() if gather else at
+        a = A[torch.where((idx < 0) | (idx >= R), R, idx)]
+        W = weight64(w, e, K, fmt)
+        zz, dz = a @ W.T, (a.abs() @ W.abs().T) * step
+        if b is not None:
+            zz = zz + b[e].double()
+            dz = dz + HALF32(zz)
+        h, dh = ref.act(act, zz), 1.2 * dz
+        if act in (qz.ACT_SILU, qz.ACT_GELU):
+            # expf within 2 + 1.17 |argument| ulp (|argument| < 90 matters), a quotient of 2 ulp
+            dh = dh + 112 * 2 * ref.HALF_F32 * h.abs()
+        parts = [(zz, dz)]
+        if gated:
+            U = weight64(up, e, K, fmt)
+            u, du = a @ U.T, (a.abs() @ U.abs().T) * step
+            if ub is not None:
+                u = u + ub[e].double()
+                du = du + HALF32(u)
+            parts.append((u, du))
+            dh = dh * (u.abs() + du) + h.abs() * du
+            h = h * u
+        if r is not None:
+            h = h + r[at, :N].double()
+        # two fp32 roundings, then one to bf16 (of a value that may be off by dh)
+        dh = dh + 2 * HALF32(h)
+        ref.close(out[at.cuda(), :N], h, ref.HALF_BF16 * (h.abs() + dh) + dh + 1e-38, f"out of expert {e}")
+        if z is not None:
+            for i, (v, dv) in enumerate(parts):
+                dv = dv + HALF32(v)
+                ref.close(z[at.cuda(), i * N:(i + 1) * N], v, ref.HALF_BF16 * (v.abs() + dv) + dv + 1e-38, "pre")
+    dead = (~live).cuda()
+    assert (out[dead] == 7.5).all() and (out[:, N:] == 7.5).all()
+    if z is not None:
+        assert (z[dead] == 7.5).all() and (z[:, width:] == 7.5).all()
+    if q:
+        assert (oq[dead] == 0x5A).all() and (osf[dead] == 0x5A).all()
+        lv = live.cuda()
+        if live.any():
+            want = qz.quantize_experts([out[:, :N][lv].contiguous()], MX, qz.SF_LINEAR)[0]
+            assert torch.equal(oq[lv], want.q) and torch.equal(osf[lv].reshape(-1), want.sf.reshape(-1))
+    return out, z, oq, osf
+
+
+def HALF32(v):
+    return ref.HALF_F32 * v.abs()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("counts", [[1], [0, 1, 0], [3, 0, 130, 1], [128, 129, 127], [300, 0, 0, 5]])
+@pytest.mark.parametrize("N,K", [(8, 32), (136, 96), (264, 352), (128, 128), (512, 544)])
+def test_product(fmt, counts, N, K):
+    run_product(fmt, counts, N, K)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", [qz.ACT_NONE, qz.ACT_RELU, qz.ACT_SILU, qz.ACT_GELU])
+def test_product_epilogues(fmt, gated, act):
+    for gather in (True, False):
+        run_product(fmt, [70, 0, 33, 131], 160, 288, gather=gather, gated=gated, act=act, bias=True, residual=True,
+                    pre=True, q=True, gap=3, pad=8, extra=5)
+    run_product(fmt, [2, 9], 96, 64, gated=gated, act=act, q=True)
+    run_product(fmt, [40], 72, 64, gated=gated, act=act, pre=True, gather=False)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("gated", [False, True])
+def test_product_single_tokens(fmt, gated):
+    """Decode: a token or a few per expert, many experts."""
+    run_product(fmt, [1] * 8 + [0] * 24, 384, 1024, gated=gated, act=qz.ACT_SILU, q=True)
+    run_product(fmt, [0] * 5 + [2, 0, 1, 4, 0, 16, 7], 256, 2048, gated=gated)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_product_many_tiles(fmt):
+    """More tiles than CTAs, and any number of CTAs gives the same bits."""
+    first = run_product(fmt, [700, 3, 0, 1025, 256], 776, 256, gated=True, act=qz.ACT_SILU, max_ctas=0)
+    for ctas in (1, 7):
+        again = run_product(fmt, [700, 3, 0, 1025, 256], 776, 256, gated=True, act=qz.ACT_SILU, max_ctas=ctas)
+        assert torch.equal(first[0], again[0])
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_product_long_contraction(fmt):
+    run_product(fmt, [5, 150], 136, 4128, std=0.02)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_product_of_fused_weights(fmt):
+    """Gate and up as views of one fused weight [E, 2N, K]."""
+    g = ref.gen(4)
+    E, N, K, S = 3, 256, 160, 90
+    q, sf, amax = stacked(g, E, 2 * N, K, fmt)
+    x = qz.quantize_tokens(ref.randn(g, S, K).to(torch.bfloat16).cuda(), fmt)
+    half = qz.sf_bytes(N, K, fmt, qz.SF_SWIZZLED)
+    offsets, counts = torch.tensor([0, 30, 60, 90], dtype=torch.int32).cuda(), torch.full((3,), 30, dtype=torch.int32).cuda()
+    out = torch.zeros(S, N, dtype=torch.bfloat16).cuda()
+    qz.expert_product(fmt, x, (q[:, :N], sf[:, :half], amax), offsets, counts, out, up=(q[:, N:], sf[:, half:], amax),
+                      activation=qz.ACT_SILU)
+    parts = []
+    for lo in (0, N):
+        p = (q[:, lo:lo + N].contiguous(), sf[:, lo // N * half:lo // N * half + half].contiguous(), amax)
+        parts.append(p)
+    want = torch.zeros_like(out)
+    qz.expert_product(fmt, x, parts[0], offsets, counts, want, up=parts[1], activation=qz.ACT_SILU)
+    assert torch.equal(out, want) and out.abs().sum() > 0
+
+
+def test_product_skips_bad_experts():
+    g = ref.gen(6)
+    x = qz.quantize_tokens(ref.randn(g, 40, 64).to(torch.bfloat16).cuda(), MX)
+    w = stacked(g, 4, 64, 64, MX)
+    out = torch.full((40, 64), 3.0, dtype=torch.bfloat16).cuda()
+    err = torch.zeros(1, dtype=torch.int32).cuda()
+    offsets = torch.tensor([0, 10, -5, 35], dtype=torch.int32).cuda()
+    counts = torch.tensor([10, -1, 3, 6], dtype=torch.int32).cuda()  # negative count, negative offset, past the end
+    qz.expert_product(MX, x, w, offsets, counts, out, err=err)
+    assert err.item() == qz.DERR_SHAPE
+    assert (out[10:] == 3.0).all() and not (out[:10] == 3.0).all()
+
+
+def test_product_writes_nothing_without_rows():
+    g = ref.gen(8)
+    x = qz.quantize_tokens(ref.randn(g, 4, 64).to(torch.bfloat16).cuda(), MX)
+    w = stacked(g, 2, 64, 64, MX)
+    out = torch.full((4, 64), 3.0, dtype=torch.bfloat16).cuda()
+    zero = torch.zeros(2, dtype=torch.int32).cuda()
+    qz.expert_product(MX, x, w, zero, zero, out)
+    assert (out == 3.0).all()
+    qz.expert_product(MX, x, w, zero, zero, out[:0])
+
+
+def test_product_on_a_stream_and_in_a_graph():
+    g = ref.gen(10)
+    x = qz.quantize_tokens(ref.randn(g, 64, 256).to(torch.bfloat16).cuda(), MX)
+    w = stacked(g, 4, 256, 256, MX)
+    offsets = torch.tensor([0, 16, 32, 48, 64], dtype=torch.int32).cuda()
+    counts = torch.full((4,), 16, dtype=torch.int32).cuda()
+    outs = [torch.zeros(64, 256, dtype=torch.bfloat16).cuda() for _ in range(4)]
+    qz.expert_product(MX, x, w, offsets, counts, outs[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s, o in zip(streams, outs[1:3]):
+        s.wait_stream(torch.cuda.current_stream())
+        qz.expert_product(MX, x, w, offsets, counts, o, stream=s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qz.expert_product(MX, x, w, offsets, counts, outs[3])
+    graph.replay()
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    counts.copy_(torch.tensor([1, 16, 0, 3], dtype=torch.int32))  # read on the device at each replay
+    outs[3].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[3][16:32], outs[0][16:32]) and (outs[3][32:48] == 0).all() and (outs[3][1:16] == 0).all()
+
+
+# --- weight gradient --------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts,N,K", [([1], 8, 8), ([0, 200, 3], 136, 264), ([128, 0, 129, 31], 264, 128),
+                                        ([700, 64], 96, 520)])
+def test_weight_grad(fmt, dtype, counts, N, K):
+    g = ref.gen(N + K)
+    E = len(counts)
+    counts = torch.tensor(counts)
+    offsets = offsets_of(counts, 128)
+    S = int(offsets[-1]) + 128
+    live = torch.zeros(S, 1)
+    for e in range(E):
+        live[int(offsets[e]):int(offsets[e]) + int(counts[e])] = 1
+    dz = qz.quantize_slots_colwise((ref.randn(g, S, N) * live).to(torch.bfloat16).cuda(), fmt)
+    x = qz.quantize_slots_colwise((ref.randn(g, S, K) * live).to(torch.bfloat16).cuda(), fmt)
+    start = ref.randn(g, E, N, K).to(dtype)
+    Z, X = (ref.decode(p[0], p[1], S, fmt == NV, True, None if p[2] is None else ref.decode_scale(p[2].cpu()))
+            for p in (dz, x))
+    for accumulate in (False, True):
+        out = start.clone().cuda()
+        qz.expert_weight_grad(fmt, dz, x, offsets.cuda(), counts.to(torch.int32).cuda(), out, accumulate=accumulate)
+        for e in range(E):
+            at = slice(int(offsets[e]), int(offsets[e]) + int(counts[e]))
+            want, size = Z[:, at] @ X[:, at].T, Z[:, at].abs() @ X[:, at].abs().T
+            tol = size * (int(counts[e]) // 32 + 8) * 2.0 ** -22
+            if accumulate:
+                want = want + start[e].double()
+            tol = tol + (ref.HALF_F32 if dtype == torch.float32 else ref.HALF_BF16) * (want.abs() + tol) + 1e-38
+            ref.close(out[e], want, tol, f"dW of expert {e}")
+
+
+def test_weight_grad_refuses_unaligned_experts():
+    g = ref.gen(2)
+    S = 256
+    dz = qz.quantize_slots_colwise(ref.randn(g, S, 32).to(torch.bfloat16).cuda(), MX)
+    x = qz.quantize_slots_colwise(ref.randn(g, S, 32).to(torch.bfloat16).cuda(), MX)
+    out = torch.full((3, 32, 32), 5.0).cuda()
+    err = torch.zeros(1, dtype=torch.int32).cuda()
+    offsets = torch.tensor([0, 64, 128], dtype=torch.int32).cuda()
+    counts = torch.tensor([64, 64, 129], dtype=torch.int32).cuda()
+    qz.expert_weight_grad(MX, dz, x, offsets, counts, out, err=err)
+    assert err.item() == qz.DERR_ALIGN | qz.DERR_SHAPE
+    assert (out[1:] == 5.0).all() and not (out[0] == 5.0).any()
+
+
+# --- activation gradient ----------------------------------------------------
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", [qz.ACT_NONE, qz.ACT_RELU, qz.ACT_SILU, qz.ACT_GELU])
+@pytest.mark.parametrize("counts,N", [([1], 8), ([0, 200, 3], 136), ([64, 0, 0, 700], 520)])
+def test_activation_grad(gated, act, counts, N):
+    g = ref.gen(N + act)
+    E = len(counts)
+    counts = torch.tensor(counts)
+    offsets = offsets_of(counts, 16)
+    S, width = int(offsets[-1]) + 9, 2 * N if gated else N
+    pre = (ref.randn(g, S, width) * 3).to(torch.bfloat16)
+    dout = ref.randn(g, S, N).to(torch.bfloat16)
+    wide = torch.full((S, width + 8), 7.5, dtype=torch.bfloat16).cuda()
+    dbias = torch.full((E, width), 7.5).cuda()
+    qz.expert_activation_grad(dout.cuda(), pre.cuda(), offsets.cuda(), counts.to(torch.int32).cuda(), wide[:, :width],
+                              activation=act, gated=gated, dbias=dbias)
+    z, d = pre[:, :N].double(), dout.double()
+    want = d * ref.act_grad(act, z)
+    if gated:
+        want = torch.cat([want * pre[:, N:].double(), d * ref.act(act, z)], -1)
+    live = torch.zeros(S, 1, dtype=torch.float64)
+    for e in range(E):
+        live[int(offsets[e]):int(offsets[e]) + int(counts[e])] = 1
+    want = want * live
+    # below 16 fp32 roundings of |d| (|u|) (1 + |z|) before the one to bf16; act' itself cancels
+    size = d.abs() * 1.2 * (1 + z.abs())
+    size = torch.cat([size * pre[:, N:].double().abs(), size], -1) if gated else size
+    each = 16 * ref.HALF_F32 * size
+    ref.close(wide[:, :width], want, each + ref.HALF_BF16 * (want.abs() + each) + 1e-38, "dpre")
+    assert (wide[:, width:] == 7.5).all()
+    for e in range(E):
+        at = slice(int(offsets[e]), int(offsets[e]) + int(counts[e]))
+        tol = each[at].sum(0) + (int(counts[e]) + 16) * ref.HALF_F32 * want[at].abs().sum(0) + 1e-38
+        ref.close(dbias[e], want[at].sum(0), tol, "dbias")
+    first = dbias.clone()
+    qz.expert_activation_grad(dout.cuda(), pre.cuda(), offsets.cuda(), counts.to(torch.int32).cuda(), wide[:, :width],
+                              activation=act, gated=gated, dbias=dbias)
+    assert torch.equal(first, dbias)
+
+
+@pytest.mark.parametrize("act", [qz.ACT_SILU, qz.ACT_GELU])
+def test_activation_grad_against_differences(act):
+    """dpre against central differences of the forward epilogue: x = 1 row of the identity, so pre = bias."""
+    z = torch.linspace(-6, 6, 256).to(torch.bfloat16)
+    n = z.numel()
+    one = torch.zeros(1, n, dtype=torch.bfloat16)
+    count, off = torch.ones(1, dtype=torch.int32).cuda(), torch.zeros(2, dtype=torch.int32).cuda()
+    d = torch.zeros(1, n, dtype=torch.bfloat16).cuda()
+    qz.expert_activation_grad(torch.ones_like(one).cuda(), z.reshape(1, n).cuda(), off, count, d, activation=act)
+    h = 2.0 ** -4
+    diff = (ref.act(act, z.double() + h) - ref.act(act, z.double() - h)) / (2 * h)
+    ref.close(d[0], diff, ref.HALF_BF16 * diff.abs() + h * h / 6 * 1.5 + 1e-6, "dpre")
+
+
+# --- dispatch and combine ---------------------------------------------------
+
+@pytest.mark.parametrize("T,E,k,H,align", [(1, 4, 2, 8, 1), (1, 1, 1, 8, 128), (5, 7, 3, 72, 16), (64, 16, 8, 1032, 1),
+                                           (37, 128, 8, 2048, 128), (300, 3, 1, 264, 32), (9, 60, 32, 520, 4)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_and_combine(T, E, k, H, align, weighted):
+    g = ref.gen(T + H)
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    if T > 4:
+        ids[1] = -1
+        ids[2, 0] = -1
+    plan = qz.plan_experts(ids.cuda(), E, align=align)
+    slots, rows = plan.slots.cpu().long(), plan.rows.cpu()
+    S, pad = plan.rows.numel(), 16
+    x, y = ref.randn(g, T, H + pad).to(torch.bfloat16), ref.randn(g, S, H).to(torch.bfloat16)
+    w = ref.randn(g, T, k) if weighted else None
+    r = ref.randn(g, T, H).to(torch.bfloat16) if weighted else None
+    live = slots >= 0
+    at = slots.clamp(min=0)
+    ww = (w.double() if weighted else torch.ones(T, k, dtype=torch.float64)) * live
+    cw = w.cuda() if weighted else None
+    out = torch.full((T, H + pad), 7.5, dtype=torch.bfloat16).cuda()
+    qz.combine_experts(y.cuda(), plan.slots, out[:, :H], weights=cw, residual=None if r is None else r.cuda())
+    terms = ww.unsqueeze(-1) * y[at].double()
+    want, size = terms.sum(1), terms.abs().sum(1)
+    if r is not None:
+        want, size = want + r.double(), size + r.double().abs()
+    tol = (k + 1) * ref.HALF_F32 * size
+    ref.close(out[:, :H], want, tol + ref.HALF_BF16 * (want.abs() + tol) + 1e-38, "combine")
+    assert (out[:, H:] == 7.5).all()
+
+    back = torch.full((S, H + pad), 7.5, dtype=torch.bfloat16).cuda()
+    dots = torch.full((T, k), 7.5).cuda()
+    qz.dispatch_experts(x.cuda()[:, :H], plan.slots, plan.rows, back[:, :H], weights=cw,
+                        other=y.cuda() if weighted else None, dots=dots if weighted else None)
+    want = torch.zeros(S, H, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            if live[t, j]:
+                want[slots[t, j]] = ww[t, j] * x[t, :H].double()
+    ref.close(back[:, :H], want, ref.HALF_BF16 * want.abs() * (1 + 2.0 ** -15) + 1e-38, "dispatch")
+    assert (back[rows < 0][:, :H] == 0).all() and (back[:, H:] == 7.5).all()
+    if weighted:
+        prod = x[:, :H].double().unsqueeze(1) * y[at].double() * live.unsqueeze(-1)
+        # 8 products in a chain, 5 + 3 levels of a tree and ceil(H / 2048) passes
+        ref.close(dots, prod.sum(-1), (20 + H // 2048) * ref.HALF_F32 * prod.abs().sum(-1) + 1e-38, "dots")
+
+
+def test_combine_in_place_of_the_residual_and_empty_calls():
+    g = ref.gen(1)
+    r = ref.randn(g, 6, 64).to(torch.bfloat16).cuda()
+    y = ref.randn(g, 12, 64).to(torch.bfloat16).cuda()
+    slots = torch.arange(12, dtype=torch.int32).reshape(6, 2).cuda()
+    want = torch.empty_like(r)
+    qz.combine_experts(y, slots, want, residual=r)
+    qz.combine_experts(y, slots, r, residual=r)
+    assert torch.equal(r, want)
+    qz.combine_experts(y, slots[:0], r[:0])
+    empty = torch.full((12, 64), 3.0, dtype=torch.bfloat16).cuda()
+    qz.dispatch_experts(r[:0], slots[:0], torch.full((12,), -1, dtype=torch.int32).cuda(), empty)
+    assert (empty == 0).all()
+    none = torch.full((6, 2), -1, dtype=torch.int32).cuda()
+    qz.combine_experts(y, none, want)
+    assert (want == 0).all()
+
+
+# --- the layer --------------------------------------------------------------
+
+def test_serving_layer():
+    """Norm + quantize, route, plan, gated product, down product, combine: as a decode or prefill step runs."""
+    T, E, k, H, I = 45, 8, 3, 256, 160
+    g = ref.gen(21)
+    x = ref.randn(g, T, H).to(torch.bfloat16).cuda()
+    gate, up, down = (stacked(g, E, *s, MX) for s in ((I, H), (I, H), (H, I)))
+    logits = ref.randn(g, T, E).to(torch.bfloat16).cuda()
+    logits[7] = -torch.inf  # a padded token
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    q = torch.empty(T, H, dtype=torch.uint8).cuda()
+    sf = torch.empty(T, H // 32, dtype=torch.uint8).cuda()
+    qz.rmsnorm_quantize(x, torch.zeros_like(x), torch.ones(H, dtype=torch.bfloat16).cuda(), 1e-6, y, h, MX, q, sf,
+                        qz.SF_LINEAR)
+    ids, w = qz.route_experts(logits, k)
+    plan = qz.plan_experts(ids, E)
+    S = plan.rows.numel()
+    mid = torch.zeros(S, I, dtype=torch.bfloat16).cuda()
+    mq = torch.zeros(S, I, dtype=torch.uint8).cuda()
+    msf = torch.zeros(S, I // 32, dtype=torch.uint8).cuda()
+    qz.expert_product(MX, (q, sf), gate[:2], plan.offsets, plan.counts, mid, rows=plan.rows, up=up[:2],
+                      activation=qz.ACT_SILU, q=mq, sf=msf)
+    o = torch.zeros(S, H, dtype=torch.bfloat16).cuda()
+    qz.expert_product(MX, (mq, msf), down[:2], plan.offsets, plan.counts, o)
+    out = torch.empty_like(x)
+    qz.combine_experts(o, plan.slots, out, weights=w, residual=h)
+    A = ref.decode(q, sf, H, False, False)
+    M = ref.decode(mq, msf, I, False, False)
+    want, size = h.double().cpu(), h.double().cpu().abs()
+    ids, w, slots = ids.cpu(), w.double().cpu(), plan.slots.cpu()
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            if e < 0:
+                assert t == 7
+                continue
+            z = A[t] @ weight64(gate, e, H, MX).T
+            m = ref.act(qz.ACT_SILU, z) * (A[t] @ weight64(up, e, H, MX).T)
+            # the quantized hidden row: half a bf16 step, then half an e4m3 step (or of the block's smallest one)
+            block = m.abs().reshape(-1, 32).amax(-1).repeat_interleave(32)
+            ref.close(M[slots[t, j]], m, (ref.HALF_E4M3 + 2 * ref.HALF_BF16) * m.abs() + block * 2.0 ** -16 * 1.01
+                      + 1e-4 * block, "hidden")
+            term = w[t, j] * (M[slots[t, j]] @ weight64(down, e, I, MX).T)
+            want[t] += term
+            size[t] += term.abs()
+    ref.close(out, want, 2 * ref.HALF_BF16 * size + 1e-4 * size, "layer")
+    assert torch.equal(out[7], h[7])
+
+
+def test_training_layer():
+    """Forward with saved pre-activations, then every gradient, against autograd in binary64 on the quantized operands'
+    values: the straight-through gradients of the quantizers."""
+    T, E, k, H, I = 60, 4, 2, 128, 96
+    g = ref.gen(33)
+    x = ref.randn(g, T, H).to(torch.bfloat16).cuda()
+    gate, up, down = ((ref.randn(g, E, *s) * 0.1).to(torch.bfloat16).cuda() for s in ((I, H), (I, H), (H, I)))
+    logits = ref.randn(g, T, E).cuda()
+    dy = ref.randn(g, T, H).to(torch.bfloat16).cuda()
+    ids, w = qz.route_experts(logits, k)
+    plan = qz.plan_experts(ids, E, align=128)
+    S = plan.rows.numel()
+    off, cnt, rows, slots = plan
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16).cuda()  # noqa: E731
+    xs = qz.dispatch_experts(x, slots, rows, bf(S, H))
+    pre, mid, o = bf(S, 2 * I), bf(S, I), bf(S, H)
+    qg, qu, qd = (qz.quantize_expert_weights(v, MX) for v in (gate, up, down))
+    qx = qz.quantize_tokens(x, MX)
+    qz.expert_product(MX, qx, qg, off, cnt, mid, rows=rows, up=qu, activation=qz.ACT_SILU, pre=pre)
+    qz.expert_product(MX, qz.quantize_tokens(mid, MX), qd, off, cnt, o)
+    # backward
+    do, dots = bf(S, H), torch.empty(T, k).cuda()
+    qz.dispatch_experts(dy, slots, rows, do, weights=w, other=o, dots=dots)
+    dlogits = qz.route_experts_grad(logits, ids, dots)
+    dmid = bf(S, I)
+    qdo = qz.quantize_tokens(do, MX)
+    qz.expert_product(MX, qdo, qz.quantize_expert_weights(down.transpose(1, 2).contiguous(), MX), off, cnt, dmid)
+    ddown = torch.zeros(E, H, I).cuda()
+    cdo, cmid = qz.quantize_slots_colwise(do, MX), qz.quantize_slots_colwise(mid, MX)
+    qz.expert_weight_grad(MX, cdo, cmid, off, cnt, ddown)
+    dpre, dbias = bf(S, 2 * I), torch.zeros(E, 2 * I).cuda()
+    qz.expert_activation_grad(dmid, pre, off, cnt, dpre, activation=qz.ACT_SILU, gated=True, dbias=dbias)
+    dgate = torch.zeros(E, 2 * I, H).cuda()
+    qz.expert_weight_grad(MX, qz.quantize_slots_colwise(dpre, MX), qz.quantize_slots_colwise(xs, MX), off, cnt, dgate)
+    fused = torch.cat([gate, up], 1).transpose(1, 2).contiguous()
+    dxs, dx = bf(S, H), bf(T, H)
+    qz.expert_product(MX, qz.quantize_tokens(dpre, MX), qz.quantize_expert_weights(fused, MX), off, cnt, dxs)
+    qz.combine_experts(dxs, slots, dx)
+
+    X, G, U, D, L = (v.double().cpu().requires_grad_() for v in (x, gate, up, down, logits))
+    p = torch.softmax(torch.gather(torch.softmax(L, -1).log(), 1, ids.cpu().long()), -1)
+    ic = ids.cpu()
+    bg = torch.zeros(E, 2 * I, dtype=torch.float64, requires_grad=True)
+    out = torch.zeros(T, H, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            e = int(ic[t, j])
+            z = torch.cat([G[e], U[e]]) @ X[t] + bg[e]
+            out[t] = out[t] + p[t, j] * (D[e] @ (ref.act(2, z[:I]) * z[I:]))
+    grads = torch.autograd.grad((out * dy.double().cpu()).sum(), [X, G, U, D, L, bg])
+    # each operand of a product is off by at most half an e4m3 step (2^-4 of a value); the products behind one another
+    # leave less than 3 of these, and their errors are independent: compared by norms
+    got = [dx, dgate[:, :I], dgate[:, I:], ddown, dlogits, dbias]
+    for name, a, b in zip(("dx", "dgate", "dup", "ddown", "dlogits", "dbias"), got, grads):
+        rel = (a.double().cpu() - b).norm() / b.norm()
+        assert rel < 3 * ref.HALF_E4M3, (name, float(rel))
