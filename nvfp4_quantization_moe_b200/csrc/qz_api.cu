@@ -50,8 +50,8 @@ cudaError_t launch_route_grad(const void* logits, int type, int64_t T, int E, in
 size_t plan_bytes(int64_t n, int E);
 cudaError_t launch_plan(const int32_t* ids, int64_t T, int k, int E, int align, int64_t slots, int32_t* offsets,
                         int32_t* counts, int32_t* rows, int32_t* pair_slots, void* ws, cudaStream_t s);
-cudaError_t launch_product(const qz_product& p, cudaStream_t s, unsigned* d_err);
-cudaError_t launch_weight_grad(const qz_weight_grad& p, cudaStream_t s, unsigned* d_err);
+cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsigned* d_err);
+cudaError_t launch_weight_grad(const qz_weight_grad& p, int ctas, cudaStream_t s, unsigned* d_err);
 cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p, int64_t slots,
                             int64_t n, int act, bool gated, const int32_t* offsets, const int32_t* counts,
                             int n_experts, uint16_t* dpre, int64_t ld_q, float* dbias, cudaStream_t s,
@@ -179,6 +179,12 @@ qz_status check_router(const void* logits, int type, int64_t T, int E, int64_t l
 
 // A row stride of a bf16 matrix of `cols` columns read 16 bytes at a time.
 bool valid_ld(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0 && ld <= QZ_MAX_LD; }
+
+// CTAs of the product kernels: one per SM, or the call's cap.
+int one_per_sm(const qz_launch_opts* opts) {
+    const int sms = device_sms();
+    return opts && opts->max_ctas > 0 && opts->max_ctas < sms ? opts->max_ctas : sms;
+}
 
 bool valid_activation(int a) { return a >= QZ_ACT_NONE && a <= QZ_ACT_GELU; }
 
@@ -508,7 +514,7 @@ qz_status qz_expert_product(const qz_product* p, void* stream, const qz_launch_o
     if (!aligned(p->x_sf, 4) || !aligned(p->x_amax, 4) || !aligned(p->w_amax, 4) || !aligned(p->up_amax, 4) ||
         !aligned(p->d_rows, 4) || !aligned(p->d_offsets, 4) || !aligned(p->d_counts, 4))
         return QZ_ERR_ALIGNMENT;
-    return from_cuda(qz::launch_product(*p, (cudaStream_t)stream, err_word(opts)));
+    return from_cuda(qz::launch_product(*p, one_per_sm(opts), (cudaStream_t)stream, err_word(opts)));
 }
 
 qz_status qz_expert_weight_grad(const qz_weight_grad* p, void* stream, const qz_launch_opts* opts) {
@@ -527,7 +533,7 @@ qz_status qz_expert_weight_grad(const qz_weight_grad* p, void* stream, const qz_
         return QZ_ERR_ALIGNMENT;
     if (!aligned(p->dz_amax, 4) || !aligned(p->x_amax, 4) || !aligned(p->d_offsets, 4) || !aligned(p->d_counts, 4))
         return QZ_ERR_ALIGNMENT;
-    return from_cuda(qz::launch_weight_grad(*p, (cudaStream_t)stream, err_word(opts)));
+    return from_cuda(qz::launch_weight_grad(*p, one_per_sm(opts), (cudaStream_t)stream, err_word(opts)));
 }
 
 qz_status qz_expert_activation_grad(const void* d_dout, int64_t ld_dout, const void* d_pre, int64_t ld_pre,

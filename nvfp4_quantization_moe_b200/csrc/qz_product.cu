@@ -1,7 +1,33 @@
-// qz_product.cu -- the experts' block-scaled matrix products (sm_100a).
+// qz_product.cu -- the experts' block-scaled matrix products on the tensor
+// cores (sm_100a): rows of x times every expert's weight, with the layer's
+// epilogue, and the experts' weight gradients.
 //
-// A tile of 64 slots x 64 columns per CTA: each step decodes 32 elements of
-// every row to fp32 in shared memory and multiplies on the CUDA cores.
+// Mathematics.  out[s, :] = epilogue(sum_k x[row(s), k] w_e[:, k]), both
+// operands coded with one scale per 32 (MXFP8) or 16 (NVFP4) elements.
+// tcgen05.mma with block scaling multiplies the codes and applies both scales
+// inside the fp32 accumulation, so the dequantized operands never exist.
+//
+// Bound.  With few rows per expert the weights' bytes from HBM; with many, the
+// tensor cores.  A CTA therefore computes 128 slots x 256 accumulator columns
+// (gated: 128 of the gate and 128 of the up projection, so that the gate is
+// applied in registers): per 128 bytes of contraction it reads 16 KB of x and
+// 32 KB of weights, and four such stages (192 KB, almost the whole shared
+// memory) keep enough bytes in flight for HBM when the tile has few live rows.
+//
+// Roles of the 12 warps of the one CTA per SM (persistent over its tiles):
+//   0      TMA: weights (tiled, 128-byte swizzle), their scales (a swizzled
+//          512-byte tile is exactly what tcgen05.cp wants: one bulk copy), and
+//          x -- rows gathered four at a time by index, or tiled without an index
+//   1      one thread copies scales to tensor memory and issues the products
+//   2, 3   gather the rows' scales (linear) into the 512-byte tile form; two
+//          warps take alternate stages so that their loads are in flight early
+//   4..11  epilogue: warp w % 4 owns the lanes (rows) 32 (w % 4) .. + 31
+//
+// Tensor memory (512 columns): two accumulators of 256 columns and the scales
+// do not fit side by side, so the accumulators overlap, [0, 256) and
+// [256 - V, 512 - V), with the scales in the last V columns.  The epilogue
+// drains the shared V columns first; from then on the next tile's products run
+// under the rest of the epilogue.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -9,230 +35,709 @@
 #include "../../include/qz_quant.cuh"
 #include "qz_act.cuh"
 #include "qz_device.cuh"
+#include "qz_tc.cuh"
 
 namespace qz {
 
-constexpr int kPT = 64;   // tile rows and columns
-constexpr int kPK = 32;   // contraction elements per step
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kTileM = 128;
+constexpr int kStages = 4;
+constexpr int kProductThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr uint32_t kRowBytes = 128;               // contraction bytes of a stage
+constexpr uint32_t kBytesA = kTileM * kRowBytes;  // 16 KB; each half of B the same
+constexpr uint32_t kBytesData = 3 * kBytesA;
 
-// Value of element i of a row of block-scaled codes without its second-level scale.
+// Per format: elements of a stage, elements of one MMA, 512-byte scale tiles of
+// 128 rows per stage, tensor-memory columns of a stage's scales (A, then B's
+// two halves), buffers of them, and the accumulators' overlap V.
 template <int FMT>
-__device__ __forceinline__ float coded_value(const uint8_t* q, const uint8_t* sf, int64_t i, uint32_t scale) {
-    if (FMT == QZ_FMT_MXFP8) {
-        const uint32_t c = q[i];
-        const float v = e4m3_value(c & 0x7Fu);
-        const float p = scale == 0 ? 0x1p-127f : __uint_as_float(scale << 23);
-        return ((c & 0x80u) ? -v : v) * p;
-    }
-    const uint32_t c = (q[i >> 1] >> ((i & 1) * 4)) & 15u;
-    const uint32_t m = c & 7u;
-    const float v = m < 2 ? 0.5f * (float)m : (float)((2u | (m & 1u)) << (m >> 1)) * 0.25f;
-    return ((c & 8u) ? -v : v) * e4m3_value(scale);
-}
+struct Shape;
+template <>
+struct Shape<QZ_FMT_MXFP8> {
+    static constexpr int kElems = 128, kMma = 32, kBlock = 32, kScaleTiles = 1;
+    static constexpr int kScaleCols = 12, kScaleBufs = kStages, kShared = 64;
+};
+template <>
+struct Shape<QZ_FMT_NVFP4> {
+    static constexpr int kElems = 256, kMma = 64, kBlock = 16, kScaleTiles = 4;
+    static constexpr int kScaleCols = 48, kScaleBufs = 2, kShared = 96;
+};
 
-__device__ __forceinline__ float activate(int act, float z) {
-    if (act == QZ_ACT_RELU) return act_value<QZ_ACT_RELU>(z);
-    if (act == QZ_ACT_SILU) return act_value<QZ_ACT_SILU>(z);
-    if (act == QZ_ACT_GELU) return act_value<QZ_ACT_GELU>(z);
-    return z;
-}
-
-__device__ __forceinline__ float decode_scale(const float* amax, int64_t i) {
-    return amax ? __fdiv_rn(__ldg(amax + i), 2688.0f) : 1.0f;
-}
-
-// Which expert and which of its row tiles work item u is; false past the end.
-__device__ __forceinline__ bool find_tile(const qz_product& p, int u, int& e, int64_t& first, int64_t& live) {
-    for (e = 0; e < p.n_experts; ++e) {
-        const int64_t off = __ldg(p.d_offsets + e), cnt = __ldg(p.d_counts + e);
-        if (off < 0 || cnt <= 0 || off + cnt > p.slots) continue;
-        const int64_t tiles = (cnt + kPT - 1) / kPT;
-        if (u < tiles) {
-            first = off + (int64_t)u * kPT;
-            live = min((int64_t)kPT, cnt - (int64_t)u * kPT);
-            return true;
-        }
-        u -= (int)tiles;
-    }
-    return false;
-}
-
+// Shared memory of the stages: all data first (each stage on a 1024-byte
+// boundary, the swizzle's period), then all scales.
 template <int FMT>
-__global__ void __launch_bounds__(256) product_kernel(qz_product p, unsigned* d_err) {
-    constexpr int BLOCK = FMT == QZ_FMT_MXFP8 ? 32 : 16;
-    constexpr int EB = FMT == QZ_FMT_MXFP8 ? 1 : 2;  // elements per byte
-    __shared__ float s_a[kPK][kPT + 1], s_b[2][kPK][kPT + 1];
-    __shared__ int s_row[kPT];
-    if (blockIdx.x == 0 && blockIdx.y == 0 && d_err) {
-        for (int e = threadIdx.x; e < p.n_experts; e += blockDim.x) {
-            const int64_t off = p.d_offsets[e], cnt = p.d_counts[e];
-            if (off < 0 || cnt < 0 || off + cnt > p.slots) atomicOr(d_err, QZ_DERR_SHAPE);
-        }
-    }
-    int e;
-    int64_t first, live;
-    if (!find_tile(p, blockIdx.y, e, first, live)) return;
-    const int64_t n0 = (int64_t)blockIdx.x * kPT, kv = p.k / BLOCK;
-    const bool gated = p.up_q != nullptr;
-    if (threadIdx.x < kPT) {
-        int r = -1;
-        if (threadIdx.x < live) {
-            r = p.d_rows ? __ldg(p.d_rows + first + threadIdx.x) : (int)(first + threadIdx.x);
-            if (r < 0 || r >= p.x_rows) r = -1;
-        }
-        s_row[threadIdx.x] = r;
-    }
-    __syncthreads();
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[2][4][4] = {};
-    for (int64_t k0 = 0; k0 < p.k; k0 += kPK) {
-        for (int i = threadIdx.x; i < kPT * kPK; i += blockDim.x) {
-            const int r = i / kPK, c = i % kPK;
-            const int64_t kk = k0 + c, row = s_row[r];
-            float v = 0.0f;
-            if (row >= 0)
-                v = coded_value<FMT>(static_cast<const uint8_t*>(p.x_q) + row * (p.k / EB), nullptr, kk,
-                                     p.x_sf[row * kv + kk / BLOCK]);
-            s_a[c][r] = v;
-            for (int h = 0; h < (gated ? 2 : 1); ++h) {
-                const uint8_t* q = static_cast<const uint8_t*>(h ? p.up_q : p.w_q) + e * p.w_stride;
-                const uint8_t* sf = (h ? p.up_sf : p.w_sf) + e * p.w_sf_stride;
-                float w = 0.0f;
-                if (n0 + r < p.n)
-                    w = coded_value<FMT>(q + (n0 + r) * (p.k / EB), nullptr, kk, sf[swz_offset(n0 + r, kk / BLOCK, kv)]);
-                s_b[h][c][r] = w;
-            }
-        }
-        __syncthreads();
-        for (int c = 0; c < kPK; ++c) {
+constexpr uint32_t kScaleStage = 3u * 512u * Shape<FMT>::kScaleTiles;
+template <int FMT>
+constexpr uint32_t kStagesBytes = kStages * (kBytesData + kScaleStage<FMT>);
+
+struct ProductArgs {
+    int act, n_experts, gated, x_per_row, gather, n_blocks;
+    int64_t n, k, x_rows, slots, w_sf_stride;
+    const uint8_t *x_sf, *w_sf, *up_sf;
+    const float *x_amax, *w_amax, *up_amax;
+    const int32_t *rows, *offsets, *counts;
+    const uint16_t *bias, *up_bias, *residual;
+    uint16_t *out, *pre;
+    int64_t ld_residual, ld_out, ld_pre;
+    uint8_t *q, *sf;
+    unsigned* d_err;
+};
+
+struct GradArgs {
+    int n_experts, f32, accumulate, m_blocks, n_blocks;
+    int64_t n, k, slots;
+    const uint8_t *dz_sf, *x_sf;
+    const float *dz_amax, *x_amax;
+    const int32_t *offsets, *counts;
+    void* out;
+    unsigned* d_err;
+};
+
+// One tile of work.
+struct Tile {
+    int e, m, n;      // expert, row tile and column block within it
+    int64_t first;    // product: first slot; gradient: first slot of the contraction
+    int live;         // product: rows of this tile that exist
+    int64_t depth;    // contraction elements
+};
+
+// The shared-memory words of the roles, in front of the stages.
+struct Control {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_free;
+    uint32_t tmem;
+    int abort;
+    long long scratch[33];
+};
+
+// ---------------------------------------------------------------------------
+// work list
+// ---------------------------------------------------------------------------
+
+struct Range {
+    int64_t off, cnt;
+    unsigned bad;
+};
+
+__device__ __forceinline__ Range expert_range(const int32_t* offsets, const int32_t* counts, int e, int64_t slots) {
+    Range r;
+    r.off = __ldg(offsets + e);
+    r.cnt = __ldg(counts + e);
+    r.bad = (r.off < 0 || r.cnt < 0 || r.off + r.cnt > slots) ? QZ_DERR_SHAPE : 0u;
+    return r;
+}
+
+// Product: s_prefix holds the experts' row tiles; an expert's tiles are ordered
+// by column block, row tiles innermost, so that CTAs working side by side read
+// the same weights.
+__device__ __forceinline__ Tile product_tile(const ProductArgs& a, const int* s_prefix, int u) {
+    Tile t;
+    t.e = find_owner(s_prefix, a.n_experts, u / a.n_blocks);
+    const int tiles = s_prefix[t.e + 1] - s_prefix[t.e];
+    const int v = u - s_prefix[t.e] * a.n_blocks;
+    t.n = v / tiles;
+    t.m = v - t.n * tiles;
+    const Range r = expert_range(a.offsets, a.counts, t.e, a.slots);
+    t.first = r.off + (int64_t)t.m * kTileM;
+    t.live = (int)min((int64_t)kTileM, r.cnt - (int64_t)t.m * kTileM);
+    t.depth = a.k;
+    return t;
+}
+
+__device__ __forceinline__ bool grad_tile(const GradArgs& a, int u, Tile& t) {
+    const int per = a.m_blocks * a.n_blocks;
+    t.e = u / per;
+    const int v = u - t.e * per;
+    t.n = v / a.m_blocks;
+    t.m = v - t.n * a.m_blocks;
+    const Range r = expert_range(a.offsets, a.counts, t.e, a.slots);
+    t.first = r.off;
+    t.live = kTileM;
+    t.depth = r.cnt;
+    return r.bad == 0 && (r.off & 127) == 0;
+}
+
+// ---------------------------------------------------------------------------
+// x's scales: linear rows to 512-byte tiles
+// ---------------------------------------------------------------------------
+
+// `take` (1..4) bytes at p as a little-endian word, the others 0.
+__device__ __forceinline__ uint32_t load_word(const uint8_t* p, int64_t take, bool word_aligned) {
+    if (take >= 4 && word_aligned) return __ldg(reinterpret_cast<const uint32_t*>(p));
+    uint32_t v = 0;
+    for (int i = 0; i < 4; ++i)
+        if (i < take) v |= (uint32_t)__ldg(p + i) << (8 * i);
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// epilogue pieces
+// ---------------------------------------------------------------------------
+
+// 32 fp32 columns as bf16 words.
+__device__ __forceinline__ void to_words(const float (&v)[32], uint32_t (&w)[16]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float av = s_a[c][ty * 4 + i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[0][i][j] = fmaf(av, s_b[0][c][tx * 4 + j], acc[0][i][j]);
-                    if (gated) acc[1][i][j] = fmaf(av, s_b[1][c][tx * 4 + j], acc[1][i][j]);
-                }
-            }
-        }
-        __syncthreads();
-    }
-    // epilogue: out in place of s_a / s_b is not needed for bf16; the MXFP8 form
-    // is made from the bf16 values once the tile is in shared memory
-    __shared__ uint16_t s_o[kPT][kPT];
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
-        const int64_t s = first + r;
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx * 4 + j;
-            float h = 0.0f;
-            if (r < live && n < p.n) {
-                const int row = s_row[r];
-                const float ga = row >= 0 ? decode_scale(p.x_amax, p.x_amax_per_row ? row : 0) : 1.0f;
-                float z = acc[0][i][j] * (ga * decode_scale(p.w_amax, e));
-                if (p.bias) z += bf16_lo(static_cast<const uint16_t*>(p.bias)[e * p.n + n]);
-                if (p.pre) static_cast<uint16_t*>(p.pre)[s * p.ld_pre + n] = (uint16_t)bf16x2_of(z, 0.0f);
-                h = activate(p.activation, z);
-                if (gated) {
-                    float u = acc[1][i][j] * (ga * decode_scale(p.up_amax, e));
-                    if (p.up_bias) u += bf16_lo(static_cast<const uint16_t*>(p.up_bias)[e * p.n + n]);
-                    if (p.pre) static_cast<uint16_t*>(p.pre)[s * p.ld_pre + p.n + n] = (uint16_t)bf16x2_of(u, 0.0f);
-                    h *= u;
-                }
-                if (p.residual) h += bf16_lo(static_cast<const uint16_t*>(p.residual)[s * p.ld_residual + n]);
-                static_cast<uint16_t*>(p.out)[s * p.ld_out + n] = (uint16_t)bf16x2_of(h, 0.0f);
-            }
-            s_o[r][tx * 4 + j] = (uint16_t)bf16x2_of(h, 0.0f);
-        }
-    }
-    if (!p.q) return;
-    __syncthreads();
-    if (threadIdx.x < 2 * kPT) {
-        const int r = threadIdx.x >> 1, b = threadIdx.x & 1;
-        const int64_t n = n0 + 32 * b;
-        if (r < live && n < p.n) {
-            uint32_t x[16], q[8];
-            for (int i = 0; i < 16; ++i) x[i] = (uint32_t)s_o[r][32 * b + 2 * i] | ((uint32_t)s_o[r][32 * b + 2 * i + 1] << 16);
-            const uint32_t sc = qzq::mxfp8_block(x, q);
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.q) + (first + r) * p.n + n);
-            dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
-            dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
-            p.sf[(first + r) * (p.n / 32) + n / 32] = (uint8_t)sc;
-        }
-    }
+    for (int i = 0; i < 16; ++i) w[i] = bf16x2_of(v[2 * i], v[2 * i + 1]);
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(256) weight_grad_kernel(qz_weight_grad p, unsigned* d_err) {
-    constexpr int BLOCK = FMT == QZ_FMT_MXFP8 ? 32 : 16;
-    constexpr int EB = FMT == QZ_FMT_MXFP8 ? 1 : 2;
-    __shared__ float s_a[kPK][kPT + 1], s_b[kPK][kPT + 1];
-    const int e = blockIdx.z;
-    const int64_t off = __ldg(p.d_offsets + e), cnt = __ldg(p.d_counts + e);
-    const bool shape = off < 0 || cnt < 0 || off + cnt > p.slots, align = (off & 127) != 0;
-    if (shape || align) {
-        if (d_err && threadIdx.x == 0) atomicOr(d_err, (shape ? QZ_DERR_SHAPE : 0u) | (align ? QZ_DERR_ALIGN : 0u));
+// The first `cols` (a multiple of 8) of 32 columns of a row; `wide`: p is 32-byte aligned.
+__device__ __forceinline__ void store_words(uint16_t* p, const uint32_t (&w)[16], int cols, bool wide) {
+    if (wide && cols >= 32) {
+        st_v8(p, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+        st_v8(p + 16, make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
         return;
     }
-    const int64_t r0 = (int64_t)blockIdx.y * kPT, c0 = (int64_t)blockIdx.x * kPT, kv = p.slots / BLOCK;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < cnt; k0 += kPK) {
-        for (int i = threadIdx.x; i < kPT * kPK; i += blockDim.x) {
-            const int r = i / kPK, c = i % kPK;
-            const int64_t s = off + k0 + c;
-            float a = 0.0f, b = 0.0f;
-            if (k0 + c < cnt) {
-                if (r0 + r < p.n)
-                    a = coded_value<FMT>(static_cast<const uint8_t*>(p.dz_q) + (r0 + r) * (p.slots / EB), nullptr, s,
-                                         p.dz_sf[swz_offset(r0 + r, s / BLOCK, kv)]);
-                if (c0 + r < p.k)
-                    b = coded_value<FMT>(static_cast<const uint8_t*>(p.x_q) + (c0 + r) * (p.slots / EB), nullptr, s,
-                                         p.x_sf[swz_offset(c0 + r, s / BLOCK, kv)]);
-            }
-            s_a[c][r] = a;
-            s_b[c][r] = b;
-        }
-        __syncthreads();
-        for (int c = 0; c < kPK; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
+        if (8 * i < cols) st_v4(p + 8 * i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+}
+
+// v += the first `cols` of 32 bf16 columns at p.
+__device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[32]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s_a[c][ty * 4 + i], s_b[c][tx * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
-    const float g = decode_scale(p.dz_amax, 0) * decode_scale(p.x_amax, 0);
     for (int i = 0; i < 4; ++i) {
+        if (8 * i >= cols) continue;
+        const uint4 r = *reinterpret_cast<const uint4*>(p + 8 * i);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + ty * 4 + i, c = c0 + tx * 4 + j;
-            if (r >= p.n || c >= p.k) continue;
-            const int64_t at = (e * p.n + r) * p.k + c;
-            float v = acc[i][j] * g;
-            if (p.out_type == QZ_TYPE_F32) {
-                float* o = static_cast<float*>(p.out) + at;
-                *o = p.accumulate ? *o + v : v;
-            } else {
-                uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-                if (p.accumulate) v += bf16_lo(*o);
-                *o = (uint16_t)bf16x2_of(v, 0.0f);
-            }
+            v[8 * i + 2 * j] += bf16_lo(w[j]);
+            v[8 * i + 2 * j + 1] += bf16_hi(w[j]);
         }
     }
 }
 
-cudaError_t launch_product(const qz_product& p, cudaStream_t s, unsigned* d_err) {
-    const int64_t most = (p.slots + kPT - 1) / kPT + p.n_experts;
-    const dim3 grid((unsigned)((p.n + kPT - 1) / kPT), (unsigned)(most < 65535 ? most : 65535));
-    if (p.fmt == QZ_FMT_MXFP8) product_kernel<QZ_FMT_MXFP8><<<grid, 256, 0, s>>>(p, d_err);
-    else product_kernel<QZ_FMT_NVFP4><<<grid, 256, 0, s>>>(p, d_err);
+template <int ACT>
+__device__ __forceinline__ void act32(float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
+}
+
+__device__ __forceinline__ void activate32(int act, float (&v)[32]) {
+    if (act == QZ_ACT_SILU) act32<QZ_ACT_SILU>(v);
+    else if (act == QZ_ACT_GELU) act32<QZ_ACT_GELU>(v);
+    else if (act == QZ_ACT_RELU) act32<QZ_ACT_RELU>(v);
+}
+
+__device__ __forceinline__ float amax_scale(const float* amax, int64_t i) {
+    return amax != nullptr ? __fdiv_rn(__ldg(amax + i), 2688.0f) : 1.0f;
+}
+
+// Accumulator columns of one 32-column piece, times g (NVFP4), 0 for a row that does not exist.
+__device__ __forceinline__ void scaled(const uint32_t (&raw)[32], float g, bool exists, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = exists ? __uint_as_float(raw[i]) * g : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+
+// GRAD: the weight gradient (args.g), otherwise the product (args.p).
+union Args {
+    ProductArgs p;
+    GradArgs g;
+};
+
+template <int FMT, bool GRAD>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    experts_kernel(const __grid_constant__ Args args, const __grid_constant__ CUtensorMap map_a,
+                   const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_up) {
+    typedef Shape<FMT> S;
+    constexpr uint32_t kSfBase = kStages * kBytesData, kSfStage = kScaleStage<FMT>;
+    constexpr uint32_t kScaleBytes = 512u * S::kScaleTiles;  // of 128 rows
+    constexpr int kAcc1 = 256 - S::kShared;
+    constexpr int kScaleCol = 512 - S::kShared;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    // the stages start at the next 1024-byte boundary (the swizzle's period)
+    const uint32_t base = (smem_addr(smem) + 1023u) & ~1023u;
+    uint8_t* const stages = smem + (base - smem_addr(smem));
+    Control* const ctl = reinterpret_cast<Control*>(stages + kStagesBytes<FMT>);
+    int* const s_prefix = reinterpret_cast<int*>(ctl + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const ProductArgs& p = args.p;
+    const GradArgs& g = args.g;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_addr(&ctl->full[i]), GRAD ? 1 : 2);  // TMA, and the scale-gathering warp
+            mbar_init(smem_addr(&ctl->empty[i]), 1);
+        }
+        mbar_init(smem_addr(&ctl->acc_full[0]), 1);
+        mbar_init(smem_addr(&ctl->acc_full[1]), 1);
+        mbar_init(smem_addr(&ctl->acc_free), kEpilogueWarps);
+        ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+    }
+    if (warp == 1) tmem_alloc(smem_addr(&ctl->tmem), 512);
+    int total;
+    if (GRAD) {
+        total = g.n_experts * g.m_blocks * g.n_blocks;
+        if (blockIdx.x == 0 && g.d_err) {
+            for (int e = threadIdx.x; e < g.n_experts; e += blockDim.x) {
+                const Range r = expert_range(g.offsets, g.counts, e, g.slots);
+                const unsigned bad = r.bad | ((r.off & 127) ? QZ_DERR_ALIGN : 0u);
+                if (bad) atomicOr(g.d_err, bad);
+            }
+        }
+        __syncthreads();
+    } else {
+        unsigned bad = 0;
+        total = p.n_blocks * block_prefix(p.n_experts, s_prefix, ctl->scratch,
+                                          [&](int e) -> long long {
+                                              const Range r = expert_range(p.offsets, p.counts, e, p.slots);
+                                              bad |= r.bad;
+                                              return r.bad ? 0 : (r.cnt + kTileM - 1) / kTileM;
+                                          },
+                                          p.d_err);  // ends with a barrier
+        if (bad && blockIdx.x == 0 && p.d_err) atomicOr(p.d_err, bad);
+    }
+    tc_fence_after();
+    const uint32_t tmem = *const_cast<volatile uint32_t*>(&ctl->tmem);
+    volatile int* const abort = &ctl->abort;
+    const int64_t kv = (GRAD ? g.slots : p.k) / S::kBlock;  // scale columns of the operands
+    const int64_t scale_tiles = (kv + 3) / 4;               // 512-byte tiles of a 128-row block of scales
+
+    // what each role needs to know of tile u; false: nothing is to be done
+    auto tile_of = [&](int u, Tile& t) -> bool {
+        if (GRAD) return grad_tile(g, u, t);
+        t = product_tile(p, s_prefix, u);
+        return true;
+    };
+    // 128-column halves of B that tile t multiplies with
+    auto halves_of = [&](const Tile& t) -> int {
+        if (GRAD) return (int64_t)t.n * 256 + 128 < g.k ? 2 : 1;
+        return p.gated || (int64_t)t.n * 256 + 128 < p.n ? 2 : 1;
+    };
+    auto stages_of = [&](const Tile& t) -> int { return (int)((t.depth + S::kElems - 1) / S::kElems); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA
+        int it = 0;
+        for (int u = blockIdx.x; u < total; u += gridDim.x) {
+            Tile t;
+            if (!tile_of(u, t)) continue;
+            const int halves = halves_of(t), steps = stages_of(t);
+            int4 rows = make_int4(0, 0, 0, 0);
+            if (!GRAD && p.gather) {
+                // lane l fetches rows 4l .. 4l + 3; an index that is no row of x
+                // reads row 0 and is zeroed by the epilogue
+                int r[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 4 * lane + i;
+                    r[i] = at < t.live ? __ldg(p.rows + t.first + at) : 0;
+                    if (r[i] < 0 || r[i] >= p.x_rows) r[i] = 0;
+                }
+                rows = make_int4(r[0], r[1], r[2], r[3]);
+            }
+            const int quads = (t.live + 3) / 4, boxes = (t.live + 31) / 32;
+            const uint32_t bytes_a = GRAD ? kBytesA : p.gather ? quads * 4 * kRowBytes : boxes * 32 * kRowBytes;
+            for (int s = 0; s < steps; ++s, ++it) {
+                const int st = it % kStages;
+                if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
+                const uint32_t bar = smem_addr(&ctl->full[st]), dst = base + st * kBytesData;
+                const uint32_t dst_sf = base + kSfBase + st * kSfStage;
+                const int64_t tile0 = (GRAD ? t.first / (4 * S::kBlock) : 0) + (int64_t)s * S::kScaleTiles;
+                const uint32_t sf_bytes = 512u * (uint32_t)min((int64_t)S::kScaleTiles, scale_tiles - tile0);
+                if (lane == 0) {
+                    mbar_arrive_tx(bar, bytes_a + halves * (kBytesA + sf_bytes) + (GRAD ? sf_bytes : 0u));
+                    for (int h = 0; h < halves; ++h) {
+                        const uint32_t db = dst + kBytesA * (1 + h), ds = dst_sf + kScaleBytes * (1 + h);
+                        if (GRAD) {
+                            const int r = t.n * 256 + 128 * h;
+                            tma_load_2d(db, &map_b, bar, (int)(t.first * 128 / S::kElems) + s * (int)kRowBytes, r);
+                            bulk_load(ds, g.x_sf + (((int64_t)(r / 128)) * scale_tiles + tile0) * 512, sf_bytes, bar);
+                        } else {
+                            const bool up = p.gated && h;
+                            const int r = p.gated ? t.n * 128 : t.n * 256 + 128 * h;
+                            tma_load_3d(db, up ? &map_up : &map_b, bar, s * (int)kRowBytes, r, t.e);
+                            bulk_load(ds, (up ? p.up_sf : p.w_sf) + t.e * p.w_sf_stride +
+                                              ((int64_t)(r / 128) * scale_tiles + tile0) * 512,
+                                      sf_bytes, bar);
+                        }
+                    }
+                    if (GRAD) {
+                        tma_load_2d(dst, &map_a, bar, (int)(t.first * 128 / S::kElems) + s * (int)kRowBytes, t.m * kTileM);
+                        bulk_load(dst_sf, g.dz_sf + ((int64_t)t.m * scale_tiles + tile0) * 512, sf_bytes, bar);
+                    } else if (!p.gather) {
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(dst + b * 32 * kRowBytes, &map_a, bar, s * (int)kRowBytes, (int)t.first + 32 * b);
+                    }
+                }
+                __syncwarp();
+                if (!GRAD && p.gather && lane < quads)
+                    tma_gather4(dst + lane * 4 * kRowBytes, &map_a, bar, s * (int)kRowBytes, rows);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        if (lane == 0) {
+            int it = 0, done_tiles = 0;
+            for (int u = blockIdx.x; u < total; u += gridDim.x) {
+                Tile t;
+                if (!tile_of(u, t)) continue;
+                const int halves = halves_of(t), steps = stages_of(t);
+                if (steps == 0) continue;
+                // the epilogue of the tile before has drained the columns both accumulators share
+                if (done_tiles > 0 && !mbar_wait(smem_addr(&ctl->acc_free), (done_tiles - 1) & 1, abort)) goto done;
+                tc_fence_after();
+                const uint32_t acc = tmem + ((done_tiles & 1) ? kAcc1 : 0);
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int st = it % kStages;
+                    // scale buffers are fewer than stages: the products that read this one two steps ago are done
+                    if (S::kScaleBufs < kStages && it >= S::kScaleBufs) {
+                        const int b = it - S::kScaleBufs;
+                        if (!mbar_wait(smem_addr(&ctl->empty[b % kStages]), (b / kStages) & 1, abort)) goto done;
+                    }
+                    if (!mbar_wait(smem_addr(&ctl->full[st]), (it / kStages) & 1, abort)) goto done;
+                    tc_fence_after();
+                    const uint32_t data = base + st * kBytesData, sfs = base + kSfBase + st * kSfStage;
+                    const uint32_t col = tmem + kScaleCol + (it % S::kScaleBufs) * S::kScaleCols;
+                    // A's tiles, then each half's: 4 columns per tile; for NVFP4 tile j of both
+                    // halves lie side by side, as one product of 256 columns reads them
+#pragma unroll
+                    for (int j = 0; j < S::kScaleTiles; ++j) {
+                        tc_copy_scales(col + 4 * j, scale_desc(sfs + 512 * j));
+                        for (int h = 0; h < halves; ++h)
+                            tc_copy_scales(col + 4 * S::kScaleTiles + 8 * j + 4 * h,
+                                           scale_desc(sfs + kScaleBytes * (1 + h) + 512 * j));
+                    }
+                    const int64_t left = t.depth - (int64_t)s * S::kElems;
+                    const int products = (int)min((int64_t)(S::kElems / S::kMma), (left + S::kMma - 1) / S::kMma);
+                    for (int k = 0; k < products; ++k) {
+                        const int j = S::kScaleTiles == 1 ? 0 : k;
+                        tc_mma<FMT>(acc, operand_desc(data + 32 * k), operand_desc(data + kBytesA + 32 * k),
+                                    mma_idesc<FMT>(128 * halves, k), col + 4 * j, col + 4 * S::kScaleTiles + 8 * j,
+                                    (s | k) != 0);
+                    }
+                    tc_commit(smem_addr(&ctl->empty[st]));
+                }
+                tc_commit(smem_addr(&ctl->acc_full[done_tiles & 1]));
+                ++done_tiles;
+            }
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ scales of x
+        if (!GRAD) {
+            int it = 0;
+            const bool words = (kv & 3) == 0;  // a row's scales start on a word
+            for (int u = blockIdx.x; u < total; u += gridDim.x) {
+                Tile t;
+                if (!tile_of(u, t)) continue;
+                const int steps = stages_of(t);
+                const uint8_t* row[4];  // rows lane, lane + 32, ...
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = lane + 32 * i;
+                    int64_t r = -1;
+                    if (at < t.live) r = p.gather ? (int64_t)__ldg(p.rows + t.first + at) : t.first + at;
+                    row[i] = r >= 0 && r < p.x_rows ? p.x_sf + r * kv : nullptr;
+                }
+                for (int s = 0; s < steps; ++s, ++it) {
+                    if ((it & 1) != warp - 2) continue;
+                    uint32_t w[S::kScaleTiles][4];
+#pragma unroll
+                    for (int j = 0; j < S::kScaleTiles; ++j) {
+                        const int64_t at = ((int64_t)s * S::kScaleTiles + j) * 4;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[j][i] = row[i] && at < kv ? load_word(row[i] + at, kv - at, words) : 0u;
+                    }
+                    const int st = it % kStages;
+                    if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
+                    uint8_t* dst = stages + kSfBase + st * kSfStage + 16 * lane;
+#pragma unroll
+                    for (int j = 0; j < S::kScaleTiles; ++j)
+                        *reinterpret_cast<uint4*>(dst + 512 * j) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ctl->full[st]));
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int quarter = warp & 3, group = (warp - 4) >> 2;
+        const int r = 32 * quarter + lane;  // row of the tile
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        int done_tiles = 0;
+        for (int u = blockIdx.x; u < total; u += gridDim.x) {
+            Tile t;
+            if (!tile_of(u, t)) continue;
+            const int halves = halves_of(t);
+            const bool any = stages_of(t) > 0;
+            if (GRAD && !any && g.accumulate) continue;
+            // per-row and per-expert facts, while the products still run
+            bool exists = true;
+            float scale0 = 1.0f, scale1 = 1.0f;
+            const int64_t slot = t.first + r;
+            if (GRAD) {
+                if (FMT == QZ_FMT_NVFP4) scale0 = scale1 = amax_scale(g.dz_amax, 0) * amax_scale(g.x_amax, 0);
+            } else if (r < t.live) {
+                int64_t row = slot;
+                if (p.gather) row = __ldg(p.rows + slot);
+                exists = row >= 0 && row < p.x_rows;
+                if (FMT == QZ_FMT_NVFP4 && exists) {
+                    const float ga = amax_scale(p.x_amax, p.x_per_row ? row : 0);
+                    scale0 = ga * amax_scale(p.w_amax, t.e);
+                    scale1 = p.gated ? ga * amax_scale(p.up_amax, t.e) : scale0;
+                }
+            }
+            const int buf = done_tiles & 1;
+            const uint32_t acc = tmem + (buf ? kAcc1 : 0) + lanes;
+            if (any) {
+                if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->acc_full[buf]), (done_tiles >> 1) & 1, abort))) goto done;
+                tc_fence_after();
+                ++done_tiles;
+            }
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                // 32 columns of each half; those shared with the other accumulator first: the upper
+                // columns of the second half (buffer 0), the lower ones of the first (buffer 1)
+                const int c = 32 * (group + 2 * (buf ? i : 1 - i));
+                float v[32], w[32];
+                __syncwarp();  // rows that do not exist have skipped ahead
+                {
+                    uint32_t raw0[32], raw1[32];
+                    if (any) {
+                        tc_load32(acc + c, raw0);
+                        if (halves == 2) tc_load32(acc + 128 + c, raw1);
+                        tc_wait_load();
+                        if (i == (S::kShared <= 64 ? 0 : 1)) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_addr(&ctl->acc_free));
+                        }
+                    }
+                    scaled(raw0, scale0, exists && any, v);
+                    if (halves == 2) scaled(raw1, scale1, exists && any, w);
+                }
+                if (GRAD) {
+                    const int64_t row = (int64_t)t.m * kTileM + r;
+                    if (row >= g.n) continue;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int64_t col = (int64_t)t.n * 256 + 128 * h + c;
+                        const int cols = (int)min((int64_t)32, g.k - col);
+                        if (h >= halves || cols <= 0) continue;
+                        float(&x)[32] = h ? w : v;
+                        const int64_t at = (t.e * g.n + row) * g.k + col;
+                        if (g.f32) {
+                            float* o = static_cast<float*>(g.out) + at;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                if (4 * q >= cols) continue;
+                                float4 y = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                                float4* to = reinterpret_cast<float4*>(o) + q;
+                                if (g.accumulate) {
+                                    const float4 b = *to;
+                                    y = make_float4(y.x + b.x, y.y + b.y, y.z + b.z, y.w + b.w);
+                                }
+                                *to = y;
+                            }
+                        } else {
+                            uint16_t* o = static_cast<uint16_t*>(g.out) + at;
+                            if (g.accumulate) add_row(o, cols, x);
+                            uint32_t words[16];
+                            to_words(x, words);
+                            store_words(o, words, cols, ((uintptr_t)o & 31) == 0);
+                        }
+                    }
+                    continue;
+                }
+                if (r >= t.live) continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && (p.gated || halves == 1)) continue;
+                    const int64_t col = p.gated ? (int64_t)t.n * 128 + c : (int64_t)t.n * 256 + 128 * h + c;
+                    const int cols = (int)min((int64_t)32, p.n - col);
+                    if (cols <= 0) continue;
+                    float(&x)[32] = h ? w : v;
+                    uint32_t words[16];
+                    if (p.bias) add_row(p.bias + t.e * p.n + col, cols, x);
+                    if (p.gated && p.up_bias) add_row(p.up_bias + t.e * p.n + col, cols, w);
+                    if (p.pre) {
+                        uint16_t* o = p.pre + slot * p.ld_pre + col;
+                        to_words(x, words);
+                        store_words(o, words, cols, ((uintptr_t)o & 31) == 0);
+                        if (p.gated) {
+                            o += p.n;
+                            to_words(w, words);
+                            store_words(o, words, cols, ((uintptr_t)o & 31) == 0);
+                        }
+                    }
+                    activate32(p.act, x);
+                    if (p.gated) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] *= w[j];
+                    }
+                    if (p.residual) add_row(p.residual + slot * p.ld_residual + col, cols, x);
+                    to_words(x, words);
+                    uint16_t* o = p.out + slot * p.ld_out + col;
+                    store_words(o, words, cols, ((uintptr_t)o & 31) == 0);
+                    if (p.q) {  // n is a multiple of 32: a whole block in this thread
+                        uint32_t codes[8];
+                        const uint32_t sc = qzq::mxfp8_block(words, codes);
+                        uint8_t* to = p.q + slot * p.n + col;
+                        st_v4(to, make_uint4(codes[0], codes[1], codes[2], codes[3]));
+                        st_v4(to + 16, make_uint4(codes[4], codes[5], codes[6], codes[7]));
+                        p.sf[slot * (p.n / 32) + col / 32] = (uint8_t)sc;
+                    }
+                }
+            }
+        }
+    }
+done:
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (ctl->abort) {
+        // a wait ran out: report it, and give copies in flight time to land before the memory goes
+        unsigned* d_err = GRAD ? g.d_err : p.d_err;
+        if (threadIdx.x == 0 && d_err) atomicOr(d_err, QZ_DERR_TIMEOUT);
+        const uint64_t start = global_ns();
+        while (global_ns() - start < 20000000ull) __nanosleep(1000);
+    }
+    tc_fence_after();
+    if (warp == 1) tmem_free(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, reached through the runtime (no link to the driver).
+static EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// Map of `experts` matrices [rows, row_bytes] of bytes, `stride` bytes apart, read in boxes of 128 bytes x box_rows.
+static bool make_map(CUtensorMap* m, const void* p, int64_t row_bytes, int64_t rows, int64_t experts, int64_t stride,
+                     int box_rows) {
+    const EncodeTiled fn = encoder();
+    if (!fn) return false;
+    const cuuint32_t rank = experts > 0 ? 3 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)rows, (cuuint64_t)experts};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)stride};
+    const cuuint32_t box[3] = {kRowBytes, (cuuint32_t)box_rows, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(p), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, bool GRAD>
+static cudaError_t launch_experts(const Args& a, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mu,
+                                  int n_experts, int grid, cudaStream_t s) {
+    const size_t smem = 1024 + kStagesBytes<FMT> + sizeof(Control) + (n_experts + 1) * sizeof(int);
+    // asked for at its largest: the attribute is one value per device
+    const size_t most = 1024 + kStagesBytes<FMT> + sizeof(Control) + (QZ_MAX_ROUTE_EXPERTS + 1) * sizeof(int);
+    static_assert(1024 + kStagesBytes<FMT> + sizeof(Control) + (QZ_MAX_ROUTE_EXPERTS + 1) * sizeof(int) <= 232448,
+                  "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(experts_kernel<FMT, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e != cudaSuccess) return e;
+    experts_kernel<FMT, GRAD><<<grid, kProductThreads, smem, s>>>(a, ma, mb, mu);
     return cudaGetLastError();
 }
 
-cudaError_t launch_weight_grad(const qz_weight_grad& p, cudaStream_t s, unsigned* d_err) {
-    const dim3 grid((unsigned)((p.k + kPT - 1) / kPT), (unsigned)((p.n + kPT - 1) / kPT), (unsigned)p.n_experts);
-    if (p.fmt == QZ_FMT_MXFP8) weight_grad_kernel<QZ_FMT_MXFP8><<<grid, 256, 0, s>>>(p, d_err);
-    else weight_grad_kernel<QZ_FMT_NVFP4><<<grid, 256, 0, s>>>(p, d_err);
-    return cudaGetLastError();
+cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsigned* d_err) {
+    Args a = {};
+    ProductArgs& q = a.p;
+    q.act = p.activation;
+    q.n_experts = p.n_experts;
+    q.gated = p.up_q != nullptr;
+    q.x_per_row = p.x_amax_per_row;
+    q.gather = p.d_rows != nullptr;
+    q.n_blocks = (int)(q.gated ? (p.n + 127) / 128 : (p.n + 255) / 256);
+    q.n = p.n;
+    q.k = p.k;
+    q.x_rows = p.x_rows;
+    q.slots = p.slots;
+    q.w_sf_stride = p.w_sf_stride;
+    q.x_sf = p.x_sf;
+    q.w_sf = p.w_sf;
+    q.up_sf = p.up_sf;
+    const bool fp4 = p.fmt == QZ_FMT_NVFP4;
+    q.x_amax = fp4 ? p.x_amax : nullptr;
+    q.w_amax = fp4 ? p.w_amax : nullptr;
+    q.up_amax = fp4 ? p.up_amax : nullptr;
+    q.rows = p.d_rows;
+    q.offsets = p.d_offsets;
+    q.counts = p.d_counts;
+    q.bias = static_cast<const uint16_t*>(p.bias);
+    q.up_bias = static_cast<const uint16_t*>(p.up_bias);
+    q.residual = static_cast<const uint16_t*>(p.residual);
+    q.out = static_cast<uint16_t*>(p.out);
+    q.pre = static_cast<uint16_t*>(p.pre);
+    q.ld_residual = p.ld_residual;
+    q.ld_out = p.ld_out;
+    q.ld_pre = p.ld_pre;
+    q.q = static_cast<uint8_t*>(p.q);
+    q.sf = p.sf;
+    q.d_err = d_err;
+    const int64_t row_bytes = fp4 ? p.k / 2 : p.k;
+    // an x without rows: every slot reads a row of zeros, so any mapped memory does for the map
+    const void* x = p.x_rows > 0 ? p.x_q : p.w_q;
+    CUtensorMap ma, mb, mu;
+    if (!make_map(&ma, x, row_bytes, p.x_rows > 0 ? p.x_rows : 1, 0, 0, q.gather ? 1 : 32)) return cudaErrorInvalidValue;
+    if (!make_map(&mb, p.w_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
+    mu = mb;
+    if (q.gated && !make_map(&mu, p.up_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
+    // no more CTAs than the slots can make tiles
+    const int64_t most = ((p.slots + kTileM - 1) / kTileM + p.n_experts) * q.n_blocks;
+    const int64_t rows = p.slots < p.n_experts ? p.slots * q.n_blocks : most;
+    const int grid = (int)(rows < ctas ? rows : ctas);
+    return fp4 ? launch_experts<QZ_FMT_NVFP4, false>(a, ma, mb, mu, p.n_experts, grid, s)
+               : launch_experts<QZ_FMT_MXFP8, false>(a, ma, mb, mu, p.n_experts, grid, s);
+}
+
+cudaError_t launch_weight_grad(const qz_weight_grad& p, int ctas, cudaStream_t s, unsigned* d_err) {
+    Args a = {};
+    GradArgs& q = a.g;
+    const bool fp4 = p.fmt == QZ_FMT_NVFP4;
+    q.n_experts = p.n_experts;
+    q.f32 = p.out_type == QZ_TYPE_F32;
+    q.accumulate = p.accumulate;
+    q.m_blocks = (int)((p.n + kTileM - 1) / kTileM);
+    q.n_blocks = (int)((p.k + 255) / 256);
+    q.n = p.n;
+    q.k = p.k;
+    q.slots = p.slots;
+    q.dz_sf = p.dz_sf;
+    q.x_sf = p.x_sf;
+    q.dz_amax = p.dz_amax;
+    q.x_amax = p.x_amax;
+    q.offsets = p.d_offsets;
+    q.counts = p.d_counts;
+    q.out = p.out;
+    q.d_err = d_err;
+    const int64_t row_bytes = fp4 ? p.slots / 2 : p.slots;
+    CUtensorMap ma, mb;
+    // without slots no tile reads an operand: any mapped memory does for the maps
+    const bool none = p.slots == 0;
+    if (!make_map(&ma, none ? p.out : p.dz_q, none ? 16 : row_bytes, none ? 1 : p.n, 0, 0, 128)) return cudaErrorInvalidValue;
+    if (!make_map(&mb, none ? p.out : p.x_q, none ? 16 : row_bytes, none ? 1 : p.k, 0, 0, 128)) return cudaErrorInvalidValue;
+    const int64_t tiles = (int64_t)p.n_experts * q.m_blocks * q.n_blocks;
+    if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const int grid = (int)(tiles < ctas ? tiles : ctas);
+    return fp4 ? launch_experts<QZ_FMT_NVFP4, true>(a, ma, mb, mb, p.n_experts, grid, s)
+               : launch_experts<QZ_FMT_MXFP8, true>(a, ma, mb, mb, p.n_experts, grid, s);
 }
 
 }  // namespace qz
