@@ -149,6 +149,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load libqz.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -575,53 +577,73 @@ def swizzle_scales(table: SfPairTable, stream=None, err=None, max_ctas: int = 0)
 # between token order and expert order
 # ---------------------------------------------------------------------------
 
+# A decode step makes these calls once per layer and is bound by the host, so
+# the checks below read each property once and format a message only to raise it.
+
 def _require(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
 
 
-def _tensor(t, name: str, dtype, shape=None, optional: bool = False) -> int:
+def _raw_stream(stream, dev: int) -> int:
+    """The stream to launch on; refuses a call whose tensors (all on device
+    ``dev``) are not on the current CUDA device, where the launch goes."""
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device, not " + (f"cuda:{dev}" if dev >= 0 else "cpu"))
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _tensor(t, name: str, dtype, dev: int, shape=None, optional: bool = False) -> int:
     """Address of a contiguous CUDA tensor of the given type (and shape), 0 for an absent optional one."""
     if t is None:
-        _require(optional, f"{name} is required")
+        if not optional:
+            raise ValueError(f"{name} is required")
         return 0
-    _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _require(t.is_contiguous(), f"{name} must be contiguous")
-    _require(shape is None or tuple(t.shape) == shape, f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    _on_device(t, name)
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device: {t.device}")
     return t.data_ptr()
 
 
-def _on_device(t, name: str):
-    """Every tensor must be on the current CUDA device, where the kernels are launched."""
-    _require(t.is_cuda and t.device.index == torch.cuda.current_device(),
-             f"{name} must be on the current CUDA device, not {t.device}")
-
-
-def _matrix(t, name: str, dtype, shape, optional: bool = False):
+def _matrix(t, name: str, dtype, dev: int, shape, optional: bool = False):
     """(address, row stride) of a CUDA matrix whose rows are contiguous; (0, 0) for an absent optional one."""
     if t is None:
-        _require(optional, f"{name} is required")
+        if not optional:
+            raise ValueError(f"{name} is required")
         return 0, 0
-    _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _require(tuple(t.shape) == shape, f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    _require(shape[1] == 1 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
-    _on_device(t, name)
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device: {t.device}")
+    return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
 
 
-def _codes(t, name: str, cols: int, fmt: int):
+def _codes(t, name: str, cols: int, fmt: int, dev: int) -> int:
     """Payloads come as uint8 bytes (or, for MXFP8, as torch.float8_e4m3fn): [..., cols] or [..., cols / 2]."""
-    _require(t.dtype == torch.uint8 or (fmt == FMT_MXFP8 and t.dtype == torch.float8_e4m3fn),
-             f"{name} must be a quantized payload, not {t.dtype}")
-    _require(t.shape[-1] == (cols if fmt == FMT_MXFP8 else cols // 2), f"the last axis of {name} does not match")
-    _on_device(t, name)
+    if t.dtype is not torch.uint8 and (fmt != FMT_MXFP8 or t.dtype is not torch.float8_e4m3fn):
+        raise ValueError(f"{name} must be a quantized payload, not {t.dtype}")
+    if t.shape[-1] != (cols if fmt == FMT_MXFP8 else cols // 2):
+        raise ValueError(f"the last axis of {name} does not match")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device: {t.device}")
     return t.data_ptr()
 
 
 def _parts(x, name: str):
-    _require(isinstance(x, (tuple, list)) and len(x) in (2, 3), f"{name} must be (payload, scales) or "
-             "(payload, scales, amax)")
+    if not isinstance(x, (tuple, list)) or len(x) not in (2, 3):
+        raise ValueError(f"{name} must be (payload, scales) or (payload, scales, amax)")
     return x[0], x[1], (x[2] if len(x) == 3 else None)
 
 
@@ -631,8 +653,11 @@ def _router(top_k, score, n_groups, top_groups, renormalize, scale):
 
 
 def _float_type(t, name: str) -> int:
-    _require(t.dtype in (torch.bfloat16, torch.float32), f"{name} must be bfloat16 or float32, not {t.dtype}")
-    return TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32
+    if t.dtype is torch.bfloat16:
+        return TYPE_BF16
+    if t.dtype is not torch.float32:
+        raise ValueError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+    return TYPE_F32
 
 
 def route_experts(logits: torch.Tensor, top_k: int, *, score: int = SCORE_SOFTMAX, bias=None, n_groups: int = 1,
@@ -645,18 +670,20 @@ def route_experts(logits: torch.Tensor, top_k: int, *, score: int = SCORE_SOFTMA
     consecutive experts stay in the choice."""
     _require(logits.dim() == 2, "logits must be [T, E]")
     kind = _float_type(logits, "logits")
+    dev = logits.get_device()
     T, E = logits.shape
-    x, ld = _matrix(logits, "logits", logits.dtype, (T, E))
-    b = _tensor(bias, "bias", torch.float32, (E,), optional=True)
+    x, ld = _matrix(logits, "logits", logits.dtype, dev, (T, E))
+    b = _tensor(bias, "bias", torch.float32, dev, (E,), optional=True)
+    _require(top_k >= 1, "top_k must be at least 1")
     if ids is None:
-        ids = torch.empty((T, max(int(top_k), 0)), dtype=torch.int32, device=logits.device)
+        ids = logits.new_empty((T, top_k), dtype=torch.int32)
     if weights is None:
-        weights = torch.empty((T, max(int(top_k), 0)), dtype=torch.float32, device=logits.device)
-    i = _tensor(ids, "ids", torch.int32, (T, top_k))
-    w = _tensor(weights, "weights", torch.float32, (T, top_k))
+        weights = logits.new_empty((T, top_k), dtype=torch.float32)
+    i = _tensor(ids, "ids", torch.int32, dev, (T, top_k))
+    w = _tensor(weights, "weights", torch.float32, dev, (T, top_k))
     _check(load().qz_route_experts(x, kind, T, E, ld, b,
                                    _router(top_k, score, n_groups, n_groups if top_groups is None else top_groups,
-                                           renormalize, scale), i, w, _stream_ptr(stream)), "qz_route_experts")
+                                           renormalize, scale), i, w, _raw_stream(stream, dev)), "qz_route_experts")
     return ids, weights
 
 
@@ -667,16 +694,17 @@ def route_experts_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
     logits' type."""
     _require(logits.dim() == 2 and ids.dim() == 2, "logits must be [T, E] and ids [T, top_k]")
     kind = _float_type(logits, "logits")
+    dev = logits.get_device()
     T, E = logits.shape
     k = ids.shape[1]
-    x, ld = _matrix(logits, "logits", logits.dtype, (T, E))
-    i = _tensor(ids, "ids", torch.int32, (T, k))
-    g = _tensor(dweights, "dweights", torch.float32, (T, k))
+    x, ld = _matrix(logits, "logits", logits.dtype, dev, (T, E))
+    i = _tensor(ids, "ids", torch.int32, dev, (T, k))
+    g = _tensor(dweights, "dweights", torch.float32, dev, (T, k))
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    d, ldd = _matrix(dlogits, "dlogits", logits.dtype, (T, E))
+        dlogits = logits.new_empty((T, E))
+    d, ldd = _matrix(dlogits, "dlogits", logits.dtype, dev, (T, E))
     _check(load().qz_route_experts_grad(x, kind, T, E, ld, _router(k, score, 1, 1, renormalize, scale), i, g, d, ldd,
-                                        _stream_ptr(stream)), "qz_route_experts_grad")
+                                        _raw_stream(stream, dev)), "qz_route_experts_grad")
     return dlogits
 
 
@@ -702,31 +730,32 @@ def plan_experts(ids: torch.Tensor, n_experts: int, *, align: int = 1, plan: Opt
     many pairs, the scratch) are allocated unless given."""
     _require(ids.dim() == 2, "ids must be [T, top_k]")
     T, k = ids.shape
-    i = _tensor(ids, "ids", torch.int32)
+    dev = ids.get_device()
+    i = _tensor(ids, "ids", torch.int32, dev)
     lib = load()
     n = lib.qz_plan_slots(T, k, int(n_experts), int(align))
     need = lib.qz_plan_bytes(T, k, int(n_experts))
     if plan is None:
-        E = max(int(n_experts), 0)
-        buf = torch.empty(2 * E + 1 + n + T * k, dtype=torch.int32, device=ids.device)
-        plan = ExpertPlan(buf[:E + 1], buf[E + 1:2 * E + 1], buf[2 * E + 1:2 * E + 1 + n],
-                          buf[2 * E + 1 + n:].view(T, k))
+        _require(n_experts >= 1, "n_experts must be at least 1")
+        offsets, counts, rows, slots = ids.new_empty(2 * n_experts + 1 + n + T * k).split(
+            (n_experts + 1, n_experts, n, T * k))
+        plan = ExpertPlan(offsets, counts, rows, slots.view(T, k))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
-    ws = 0 if workspace is None else _tensor(workspace, "workspace", torch.uint8)
+        workspace = ids.new_empty(need, dtype=torch.uint8)
+    ws = 0 if workspace is None else _tensor(workspace, "workspace", torch.uint8, dev)
     _check(lib.qz_plan_experts(i, T, k, int(n_experts), int(align),
-                               _tensor(plan.offsets, "offsets", torch.int32, (n_experts + 1,)),
-                               _tensor(plan.counts, "counts", torch.int32, (n_experts,)),
-                               _tensor(plan.rows, "rows", torch.int32, (n,)),
-                               _tensor(plan.slots, "slots", torch.int32, (T, k)), ws,
-                               0 if workspace is None else workspace.numel(), _stream_ptr(stream)), "qz_plan_experts")
+                               _tensor(plan.offsets, "offsets", torch.int32, dev, (n_experts + 1,)),
+                               _tensor(plan.counts, "counts", torch.int32, dev, (n_experts,)),
+                               _tensor(plan.rows, "rows", torch.int32, dev, (n,)),
+                               _tensor(plan.slots, "slots", torch.int32, dev, (T, k)), ws,
+                               0 if workspace is None else workspace.numel(), _raw_stream(stream, dev)), "qz_plan_experts")
     return plan
 
 
-def _expert_lists(offsets, counts, n_experts: int):
+def _expert_lists(offsets, counts, n_experts: int, dev: int):
     """Addresses of offsets ([n_experts] or [n_experts + 1]) and counts."""
     _require(offsets.dim() == 1 and offsets.numel() in (n_experts, n_experts + 1), "offsets must be [n_experts + 1]")
-    return _tensor(offsets, "offsets", torch.int32), _tensor(counts, "counts", torch.int32, (n_experts,))
+    return _tensor(offsets, "offsets", torch.int32, dev), _tensor(counts, "counts", torch.int32, dev, (n_experts,))
 
 
 def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, out: torch.Tensor, *, rows=None,
@@ -749,7 +778,8 @@ def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, 
     _require(xq.dim() == 2 and wq.dim() == 3 and out.dim() == 2, "x must be [R, K], w [E, N, K], out [slots, N]")
     _require(fmt in (FMT_MXFP8, FMT_NVFP4), "fmt must be FMT_MXFP8 or FMT_NVFP4")
     fp4 = fmt == FMT_NVFP4
-    E, N = wq.shape[:2]
+    dev = out.get_device()
+    E, N, _ = wq.shape
     K = xq.shape[1] * (2 if fp4 else 1)
     R, S = xq.shape[0], out.shape[0]
     _require(xq.is_contiguous(), "x must be contiguous")
@@ -757,40 +787,45 @@ def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, 
 
     def weight(part, name):
         pq, psf, pa = part
-        _require(pq.dim() == 3 and pq.shape[:2] == (E, N), f"{name} must be [E, N, K]")
-        _require(pq.stride(2) == 1 and (N == 1 or pq.stride(1) == pq.shape[2]), f"{name}: an expert's rows must be dense")
-        _require(psf.dim() == 2 and psf.shape[0] == E and psf.dtype == torch.uint8 and psf.stride(1) == 1
-                 and psf.shape[1] >= sf_bytes(N, K, fmt, SF_SWIZZLED), f"{name}: scales must be [E, region] bytes")
-        _on_device(psf, f"{name}'s scales")
-        return (_codes(pq, name, K, fmt), psf.data_ptr(),
-                _tensor(pa, f"{name}'s amax", torch.float32, (E,)) if fp4 else 0,
-                pq.stride(0) if E > 1 else N * pq.shape[2], psf.stride(0) if E > 1 else (psf.shape[1] + 15) // 16 * 16)
+        if pq.dim() != 3 or pq.shape[0] != E or pq.shape[1] != N:
+            raise ValueError(f"{name} must be [E, N, K]")
+        apart, row, one = pq.stride()
+        if one != 1 or (N > 1 and row != pq.shape[2]):
+            raise ValueError(f"{name}: an expert's rows must be dense")
+        if (psf.dim() != 2 or psf.shape[0] != E or psf.dtype is not torch.uint8 or psf.stride(1) != 1
+                or psf.shape[1] < region or psf.get_device() != dev):
+            raise ValueError(f"{name}: scales must be [E, region] bytes on the current CUDA device")
+        return (_codes(pq, name, K, fmt, dev), psf.data_ptr(),
+                _tensor(pa, "a weight's amax", torch.float32, dev, (E,)) if fp4 else 0,
+                apart if E > 1 else N * pq.shape[2], psf.stride(0) if E > 1 else (psf.shape[1] + 15) // 16 * 16)
+
+    region = load().qz_sf_bytes(N, K, fmt, SF_SWIZZLED)
 
     wp = weight((wq, wsf, wa), "w")
     upp = (0, 0, 0)
     if up is not None:
         upp = weight(_parts(up, "up"), "up")
         _require(upp[3:] == wp[3:], "w and up must have the same strides")
-    offs, cnts = _expert_lists(offsets, counts, E)
-    o, ldo = _matrix(out, "out", torch.bfloat16, (S, N))
-    r, ldr = _matrix(residual, "residual", torch.bfloat16, (S, N), optional=True)
-    z, ldz = _matrix(pre, "pre", torch.bfloat16, (S, N if up is None else 2 * N), optional=True)
+    offs, cnts = _expert_lists(offsets, counts, E, dev)
+    o, ldo = _matrix(out, "out", torch.bfloat16, dev, (S, N))
+    r, ldr = _matrix(residual, "residual", torch.bfloat16, dev, (S, N), optional=True)
+    z, ldz = _matrix(pre, "pre", torch.bfloat16, dev, (S, N if up is None else 2 * N), optional=True)
     _require((q is None) == (sf is None), "q and sf come together")
     if q is not None:
         _require(q.is_contiguous() and q.shape == (S, N), "q must be a contiguous [slots, N]")
         _require(sf.is_contiguous() and sf.dtype == torch.uint8 and sf.shape == (S, N // 32), "sf must be [slots, N/32] bytes")
-        _on_device(sf, "sf")
+        _require(sf.get_device() == dev, "sf must be on the current CUDA device")
     amax = 0
     if fp4:
         _require(xa is not None and xa.numel() in (1, R), "x's amax must be [R] or [1]")
-        amax = _tensor(xa, "x's amax", torch.float32)
+        amax = _tensor(xa, "x's amax", torch.float32, dev)
     p = _Product(fmt, int(activation), E, 1 if fp4 and xa.numel() == R and R > 1 else 0, N, K, R, S,
-                 _codes(xq, "x", K, fmt), _tensor(xsf, "x's scales", torch.uint8, (R, kv)), amax,
-                 _tensor(rows, "rows", torch.int32, (S,), optional=True), offs, cnts, wp[0], wp[1], wp[2], upp[0],
-                 upp[1], upp[2], wp[3], wp[4], _tensor(bias, "bias", torch.bfloat16, (E, N), optional=True),
-                 _tensor(up_bias, "up_bias", torch.bfloat16, (E, N), optional=True), r, ldr, o, ldo, z, ldz,
-                 0 if q is None else _codes(q, "q", N, FMT_MXFP8), 0 if sf is None else sf.data_ptr())
-    _check(load().qz_expert_product(ctypes.byref(p), _stream_ptr(stream), _opts(err, max_ctas)), "qz_expert_product")
+                 _codes(xq, "x", K, fmt, dev), _tensor(xsf, "x's scales", torch.uint8, dev, (R, kv)), amax,
+                 _tensor(rows, "rows", torch.int32, dev, (S,), optional=True), offs, cnts, wp[0], wp[1], wp[2], upp[0],
+                 upp[1], upp[2], wp[3], wp[4], _tensor(bias, "bias", torch.bfloat16, dev, (E, N), optional=True),
+                 _tensor(up_bias, "up_bias", torch.bfloat16, dev, (E, N), optional=True), r, ldr, o, ldo, z, ldz,
+                 0 if q is None else _codes(q, "q", N, FMT_MXFP8, dev), 0 if sf is None else sf.data_ptr())
+    _check(load().qz_expert_product(ctypes.byref(p), _raw_stream(stream, dev), _opts(err, max_ctas)), "qz_expert_product")
     return out
 
 
@@ -807,20 +842,21 @@ def expert_weight_grad(fmt: int, dz, x, offsets: torch.Tensor, counts: torch.Ten
     _require(zq.dim() == 2 and xq.dim() == 2 and out.dim() == 3, "dz must be [N, slots], x [K, slots], out [E, N, K]")
     _require(fmt in (FMT_MXFP8, FMT_NVFP4), "fmt must be FMT_MXFP8 or FMT_NVFP4")
     fp4 = fmt == FMT_NVFP4
+    dev = out.get_device()
     E, N, K = out.shape
     S = zq.shape[1] * (2 if fp4 else 1)
     _require(zq.shape[0] == N and xq.shape[0] == K, "dz, x and out do not match")
     _require(zq.is_contiguous() and xq.is_contiguous(), "dz and x must be contiguous")
     _require(zsf.numel() >= sf_bytes(N, S, fmt, SF_SWIZZLED) and xsf.numel() >= sf_bytes(K, S, fmt, SF_SWIZZLED),
              "the scales are smaller than the swizzled region")
-    offs, cnts = _expert_lists(offsets, counts, E)
-    p = _WeightGrad(fmt, E, _float_type(out, "out"), 1 if accumulate else 0, N, K, S, _codes(zq, "dz", S, fmt),
-                    _tensor(zsf, "dz's scales", torch.uint8),
-                    _tensor(za, "dz's amax", torch.float32, (1,)) if fp4 else 0, _codes(xq, "x", S, fmt),
-                    _tensor(xsf, "x's scales", torch.uint8),
-                    _tensor(xa, "x's amax", torch.float32, (1,)) if fp4 else 0, offs, cnts,
-                    _tensor(out, "out", out.dtype))
-    _check(load().qz_expert_weight_grad(ctypes.byref(p), _stream_ptr(stream), _opts(err, max_ctas)),
+    offs, cnts = _expert_lists(offsets, counts, E, dev)
+    p = _WeightGrad(fmt, E, _float_type(out, "out"), 1 if accumulate else 0, N, K, S, _codes(zq, "dz", S, fmt, dev),
+                    _tensor(zsf, "dz's scales", torch.uint8, dev),
+                    _tensor(za, "dz's amax", torch.float32, dev, (1,)) if fp4 else 0, _codes(xq, "x", S, fmt, dev),
+                    _tensor(xsf, "x's scales", torch.uint8, dev),
+                    _tensor(xa, "x's amax", torch.float32, dev, (1,)) if fp4 else 0, offs, cnts,
+                    _tensor(out, "out", out.dtype, dev))
+    _check(load().qz_expert_weight_grad(ctypes.byref(p), _raw_stream(stream, dev), _opts(err, max_ctas)),
            "qz_expert_weight_grad")
     return out
 
@@ -833,16 +869,18 @@ def expert_activation_grad(dout: torch.Tensor, pre: torch.Tensor, offsets: torch
     and dpre bf16 [slots, N or 2N], dbias fp32 [E, N or 2N] or None.  offsets
     must be [E + 1] or [E], as the plan writes them; rows of dpre that are no
     live slot become zeros."""
+    _require(dout.dim() == 2, "dout must be [slots, N]")
+    dev = dout.get_device()
     S, N = dout.shape
     width = 2 * N if gated else N
     E = counts.numel()
-    offs, cnts = _expert_lists(offsets, counts, E)
-    d, ldd = _matrix(dout, "dout", torch.bfloat16, (S, N))
-    z, ldz = _matrix(pre, "pre", torch.bfloat16, (S, width))
-    g, ldg = _matrix(dpre, "dpre", torch.bfloat16, (S, width))
+    offs, cnts = _expert_lists(offsets, counts, E, dev)
+    d, ldd = _matrix(dout, "dout", torch.bfloat16, dev, (S, N))
+    z, ldz = _matrix(pre, "pre", torch.bfloat16, dev, (S, width))
+    g, ldg = _matrix(dpre, "dpre", torch.bfloat16, dev, (S, width))
     _check(load().qz_expert_activation_grad(d, ldd, z, ldz, S, N, int(activation), 1 if gated else 0, offs, cnts, E,
-                                            g, ldg, _tensor(dbias, "dbias", torch.float32, (E, width), optional=True),
-                                            _stream_ptr(stream), _opts(err, 0)), "qz_expert_activation_grad")
+                                            g, ldg, _tensor(dbias, "dbias", torch.float32, dev, (E, width), optional=True),
+                                            _raw_stream(stream, dev), _opts(err, 0)), "qz_expert_activation_grad")
     return dpre
 
 
@@ -852,16 +890,17 @@ def dispatch_experts(x: torch.Tensor, slots: torch.Tensor, rows: torch.Tensor, y
     weights[t, j] * x[t], zeros in unused slots; with ``other`` [slots, H] also
     dots[t, j] = <x[t], other[slots[t, j]]>.  The gradient of combine_experts."""
     _require(x.dim() == 2 and slots.dim() == 2 and y.dim() == 2, "x must be [T, H], slots [T, top_k], y [slots, H]")
+    dev = x.get_device()
     T, H = x.shape
     k, S = slots.shape[1], y.shape[0]
-    a, lda = _matrix(x, "x", torch.bfloat16, (T, H))
-    b, ldb = _matrix(y, "y", torch.bfloat16, (S, H))
-    o, ldo = _matrix(other, "other", torch.bfloat16, (S, H), optional=True)
-    _check(load().qz_dispatch_experts(a, lda, _tensor(slots, "slots", torch.int32, (T, k)),
-                                      _tensor(rows, "rows", torch.int32, (S,)), T, k, S, H,
-                                      _tensor(weights, "weights", torch.float32, (T, k), optional=True), b, ldb, o,
-                                      ldo, _tensor(dots, "dots", torch.float32, (T, k), optional=True),
-                                      _stream_ptr(stream)), "qz_dispatch_experts")
+    a, lda = _matrix(x, "x", torch.bfloat16, dev, (T, H))
+    b, ldb = _matrix(y, "y", torch.bfloat16, dev, (S, H))
+    o, ldo = _matrix(other, "other", torch.bfloat16, dev, (S, H), optional=True)
+    _check(load().qz_dispatch_experts(a, lda, _tensor(slots, "slots", torch.int32, dev, (T, k)),
+                                      _tensor(rows, "rows", torch.int32, dev, (S,)), T, k, S, H,
+                                      _tensor(weights, "weights", torch.float32, dev, (T, k), optional=True), b, ldb, o,
+                                      ldo, _tensor(dots, "dots", torch.float32, dev, (T, k), optional=True),
+                                      _raw_stream(stream, dev)), "qz_dispatch_experts")
     return y
 
 
@@ -871,14 +910,15 @@ def combine_experts(y: torch.Tensor, slots: torch.Tensor, out: torch.Tensor, *, 
     sum_j weights[t, j] * y[slots[t, j]] (a missing weight counts 1).  The
     gradient of dispatch_experts."""
     _require(y.dim() == 2 and slots.dim() == 2 and out.dim() == 2, "y must be [slots, H], slots [T, top_k], out [T, H]")
+    dev = out.get_device()
     T, H = out.shape
     S, k = y.shape[0], slots.shape[1]
-    a, lda = _matrix(y, "y", torch.bfloat16, (S, H))
-    o, ldo = _matrix(out, "out", torch.bfloat16, (T, H))
-    r, ldr = _matrix(residual, "residual", torch.bfloat16, (T, H), optional=True)
-    _check(load().qz_combine_experts(a, lda, _tensor(slots, "slots", torch.int32, (T, k)), T, k, S, H,
-                                     _tensor(weights, "weights", torch.float32, (T, k), optional=True), r, ldr, o, ldo,
-                                     _stream_ptr(stream)), "qz_combine_experts")
+    a, lda = _matrix(y, "y", torch.bfloat16, dev, (S, H))
+    o, ldo = _matrix(out, "out", torch.bfloat16, dev, (T, H))
+    r, ldr = _matrix(residual, "residual", torch.bfloat16, dev, (T, H), optional=True)
+    _check(load().qz_combine_experts(a, lda, _tensor(slots, "slots", torch.int32, dev, (T, k)), T, k, S, H,
+                                     _tensor(weights, "weights", torch.float32, dev, (T, k), optional=True), r, ldr, o, ldo,
+                                     _raw_stream(stream, dev)), "qz_combine_experts")
     return out
 
 

@@ -14,14 +14,18 @@
 // 32 KB of weights, and four such stages (192 KB, almost the whole shared
 // memory) keep enough bytes in flight for HBM when the tile has few live rows.
 //
-// Roles of the 12 warps of the one CTA per SM (persistent over its tiles):
-//   0      TMA: weights (tiled, 128-byte swizzle), their scales (a swizzled
-//          512-byte tile is exactly what tcgen05.cp wants: one bulk copy), and
-//          x -- rows gathered four at a time by index, or tiled without an index
-//   1      one thread copies scales to tensor memory and issues the products
-//   2, 3   gather the rows' scales (linear) into the 512-byte tile form; two
-//          warps take alternate stages so that their loads are in flight early
+// Roles of the 14 warps of the one CTA per SM (persistent over its tiles):
+//   0..3   x: each lane owns one row's scales (linear; 16 bytes at a time, three
+//          such pieces ahead, written into the 512-byte tile form), and with a
+//          row index the warps also gather the rows themselves by 16-byte
+//          cp.async in the 128-byte swizzle.  (TMA's gather of four rows was
+//          measured first: about 55 ns per 512 bytes, 352 us against 181 us
+//          without an index on 4096 tokens x 8 experts, 2 x 768 x 2048.)
 //   4..11  epilogue: warp w % 4 owns the lanes (rows) 32 (w % 4) .. + 31
+//   12     TMA: weights (tiled, 128-byte swizzle), their scales (a swizzled
+//          512-byte tile is exactly what tcgen05.cp wants: one bulk copy), and
+//          x when it has no index
+//   13     one thread copies scales to tensor memory and issues the products
 //
 // Tensor memory (512 columns): two accumulators of 256 columns and the scales
 // do not fit side by side, so the accumulators overlap, [0, 256) and
@@ -42,7 +46,8 @@ namespace qz {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kTileM = 128;
 constexpr int kStages = 4;
-constexpr int kProductThreads = 384;
+constexpr int kProductThreads = 448;
+constexpr int kRowWarps = 4;
 constexpr int kEpilogueWarps = 8;
 constexpr uint32_t kRowBytes = 128;               // contraction bytes of a stage
 constexpr uint32_t kBytesA = kTileM * kRowBytes;  // 16 KB; each half of B the same
@@ -74,7 +79,7 @@ constexpr uint32_t kStagesBytes = kStages * (kBytesData + kScaleStage<FMT>);
 struct ProductArgs {
     int act, n_experts, gated, x_per_row, gather, n_blocks;
     int64_t n, k, x_rows, slots, w_sf_stride;
-    const uint8_t *x_sf, *w_sf, *up_sf;
+    const uint8_t *x_q, *x_sf, *w_sf, *up_sf;
     const float *x_amax, *w_amax, *up_amax;
     const int32_t *rows, *offsets, *counts;
     const uint16_t *bias, *up_bias, *residual;
@@ -175,28 +180,30 @@ __device__ __forceinline__ uint32_t load_word(const uint8_t* p, int64_t take, bo
 // epilogue pieces
 // ---------------------------------------------------------------------------
 
-// 32 fp32 columns as bf16 words.
-__device__ __forceinline__ void to_words(const float (&v)[32], uint32_t (&w)[16]) {
+// A lane handles 16 columns of its row at a time (the register budget of 14
+// warps), two such pieces making one MXFP8 block.
+
+// 16 fp32 columns as 8 bf16 words.
+__device__ __forceinline__ void to_words(const float (&v)[16], uint32_t* w) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = bf16x2_of(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) w[i] = bf16x2_of(v[2 * i], v[2 * i + 1]);
 }
 
-// The first `cols` (a multiple of 8) of 32 columns of a row; `wide`: p is 32-byte aligned.
-__device__ __forceinline__ void store_words(uint16_t* p, const uint32_t (&w)[16], int cols, bool wide) {
-    if (wide && cols >= 32) {
-        st_v8(p, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
-        st_v8(p + 16, make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
+// The first `cols` (a multiple of 8) of 16 columns of a row.
+__device__ __forceinline__ void store_words(uint16_t* p, const uint32_t* w, int cols) {
+    const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
+    if (cols >= 16 && ((uintptr_t)p & 31) == 0) {
+        st_v8(p, a, b);
         return;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (8 * i < cols) st_v4(p + 8 * i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+    if (cols > 0) st_v4(p, a);
+    if (cols > 8) st_v4(p + 8, b);
 }
 
-// v += the first `cols` of 32 bf16 columns at p.
-__device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[32]) {
+// v += the first `cols` of 16 bf16 columns at p.
+__device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         if (8 * i >= cols) continue;
         const uint4 r = *reinterpret_cast<const uint4*>(p + 8 * i);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -208,26 +215,51 @@ __device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[
     }
 }
 
-template <int ACT>
-__device__ __forceinline__ void act32(float (&v)[32]) {
+// The first n (a multiple of 8) of 16 fp32 columns at p, added to what is there if `add`.
+__device__ __forceinline__ void store_f32(float* p, float (&v)[16], int n, bool add) {
+    const bool wide = ((uintptr_t)p & 31) == 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
+    for (int q = 0; q < 2; ++q) {
+        if (8 * q >= n) continue;
+        uint4 y[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float4 f = make_float4(v[8 * q + 4 * j], v[8 * q + 4 * j + 1], v[8 * q + 4 * j + 2], v[8 * q + 4 * j + 3]);
+            if (add) {
+                const float4 b = *(reinterpret_cast<const float4*>(p) + 2 * q + j);
+                f = make_float4(f.x + b.x, f.y + b.y, f.z + b.z, f.w + b.w);
+            }
+            y[j] = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
+        }
+        if (wide) {
+            st_v8(p + 8 * q, y[0], y[1]);
+        } else {
+            st_v4(p + 8 * q, y[0]);
+            st_v4(p + 8 * q + 4, y[1]);
+        }
+    }
 }
 
-__device__ __forceinline__ void activate32(int act, float (&v)[32]) {
-    if (act == QZ_ACT_SILU) act32<QZ_ACT_SILU>(v);
-    else if (act == QZ_ACT_GELU) act32<QZ_ACT_GELU>(v);
-    else if (act == QZ_ACT_RELU) act32<QZ_ACT_RELU>(v);
+template <int ACT>
+__device__ __forceinline__ void act16(float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_value<ACT>(v[i]);
+}
+
+__device__ __forceinline__ void activate(int act, float (&v)[16]) {
+    if (act == QZ_ACT_SILU) act16<QZ_ACT_SILU>(v);
+    else if (act == QZ_ACT_GELU) act16<QZ_ACT_GELU>(v);
+    else if (act == QZ_ACT_RELU) act16<QZ_ACT_RELU>(v);
 }
 
 __device__ __forceinline__ float amax_scale(const float* amax, int64_t i) {
     return amax != nullptr ? __fdiv_rn(__ldg(amax + i), 2688.0f) : 1.0f;
 }
 
-// Accumulator columns of one 32-column piece, times g (NVFP4), 0 for a row that does not exist.
-__device__ __forceinline__ void scaled(const uint32_t (&raw)[32], float g, bool exists, float (&v)[32]) {
+// Accumulator columns times g (NVFP4's second-level scales), 0 for a row that does not exist.
+__device__ __forceinline__ void scaled(const uint32_t (&raw)[16], float g, bool exists, float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = exists ? __uint_as_float(raw[i]) * g : 0.0f;
+    for (int i = 0; i < 16; ++i) v[i] = exists ? __uint_as_float(raw[i]) * g : 0.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -262,7 +294,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_addr(&ctl->full[i]), GRAD ? 1 : 2);  // TMA, and the scale-gathering warp
+            // TMA; the warps of x's scales; every lane of them when it gathers rows
+            mbar_init(smem_addr(&ctl->full[i]), GRAD ? 1 : 1 + kRowWarps + (p.gather ? 32 * kRowWarps : 0));
             mbar_init(smem_addr(&ctl->empty[i]), 1);
         }
         mbar_init(smem_addr(&ctl->acc_full[0]), 1);
@@ -273,7 +306,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_b);
     }
-    if (warp == 1) tmem_alloc(smem_addr(&ctl->tmem), 512);
+    if (warp == 13) tmem_alloc(smem_addr(&ctl->tmem), 512);
     int total;
     if (GRAD) {
         total = g.n_experts * g.m_blocks * g.n_blocks;
@@ -315,28 +348,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     };
     auto stages_of = [&](const Tile& t) -> int { return (int)((t.depth + S::kElems - 1) / S::kElems); };
 
-    if (warp == 0) {
+    if (warp == 12) {
         // ------------------------------------------------------------ TMA
         int it = 0;
         for (int u = blockIdx.x; u < total; u += gridDim.x) {
             Tile t;
             if (!tile_of(u, t)) continue;
             const int halves = halves_of(t), steps = stages_of(t);
-            int4 rows = make_int4(0, 0, 0, 0);
-            if (!GRAD && p.gather) {
-                // lane l fetches rows 4l .. 4l + 3; an index that is no row of x
-                // reads row 0 and is zeroed by the epilogue
-                int r[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = 4 * lane + i;
-                    r[i] = at < t.live ? __ldg(p.rows + t.first + at) : 0;
-                    if (r[i] < 0 || r[i] >= p.x_rows) r[i] = 0;
-                }
-                rows = make_int4(r[0], r[1], r[2], r[3]);
-            }
-            const int quads = (t.live + 3) / 4, boxes = (t.live + 31) / 32;
-            const uint32_t bytes_a = GRAD ? kBytesA : p.gather ? quads * 4 * kRowBytes : boxes * 32 * kRowBytes;
+            const int boxes = (t.live + 31) / 32;
+            const uint32_t bytes_a = GRAD ? kBytesA : p.gather ? 0u : boxes * 32 * kRowBytes;
             for (int s = 0; s < steps; ++s, ++it) {
                 const int st = it % kStages;
                 if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
@@ -370,11 +390,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (!GRAD && p.gather && lane < quads)
-                    tma_gather4(dst + lane * 4 * kRowBytes, &map_a, bar, s * (int)kRowBytes, rows);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 13) {
         // ------------------------------------------------------------ MMA
         if (lane == 0) {
             int it = 0, done_tiles = 0;
@@ -395,6 +413,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         if (!mbar_wait(smem_addr(&ctl->empty[b % kStages]), (b / kStages) & 1, abort)) goto done;
                     }
                     if (!mbar_wait(smem_addr(&ctl->full[st]), (it / kStages) & 1, abort)) goto done;
+                    if (!GRAD && p.gather) fence_async();  // the gathered rows were written by cp.async
                     tc_fence_after();
                     const uint32_t data = base + st * kBytesData, sfs = base + kSfBase + st * kSfStage;
                     const uint32_t col = tmem + kScaleCol + (it % S::kScaleBufs) * S::kScaleCols;
@@ -421,41 +440,109 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 ++done_tiles;
             }
         }
-    } else if (warp < 4) {
-        // ------------------------------------------------------------ scales of x
+    } else if (warp < kRowWarps) {
+        // ------------------------------------------------------------ rows of x
         if (!GRAD) {
+            // a piece: 16 bytes of the lane's row's scales, for kPiece stages
+            constexpr int kPiece = 4 / S::kScaleTiles;
+            const bool words = (kv & 3) == 0, quads = (kv & 15) == 0 && aligned(p.x_sf, 16);
+            // the scales run ahead of the stages over their own walk of the tiles
+            int su = (int)blockIdx.x - (int)gridDim.x, ssteps = 0, ss = 0;
+            const uint8_t* srow = nullptr;
+            auto next_piece = [&]() -> uint4 {
+                ss += kPiece;
+                if (ss >= ssteps) {
+                    su += gridDim.x;
+                    ss = 0;
+                    ssteps = 0;
+                    srow = nullptr;
+                    if (su < total) {
+                        Tile t;
+                        tile_of(su, t);
+                        ssteps = stages_of(t);
+                        const int at = 32 * warp + lane;
+                        int64_t r = -1;
+                        if (at < t.live) r = p.gather ? (int64_t)__ldg(p.rows + t.first + at) : t.first + at;
+                        if (r >= 0 && r < p.x_rows) srow = p.x_sf + r * kv;
+                    }
+                }
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (srow != nullptr) {
+                    const int64_t at = (int64_t)ss * S::kScaleTiles * 4;
+                    if (quads) {
+                        v = __ldg(reinterpret_cast<const uint4*>(srow + at));
+                    } else {
+                        v.x = load_word(srow + at, kv - at, words);
+                        v.y = load_word(srow + at + 4, kv - at - 4, words);
+                        v.z = load_word(srow + at + 8, kv - at - 8, words);
+                        v.w = load_word(srow + at + 12, kv - at - 12, words);
+                    }
+                }
+                return v;
+            };
+            uint4 p0 = next_piece(), p1 = next_piece(), p2 = next_piece();
+            // rows that this lane helps to gather: 32 warp + lane / 8 + 4 i, 16-byte chunk lane % 8
+            const int chunk = lane & 7, sub = lane >> 3;
+            auto index_of = [&](int u) -> int {
+                if (!p.gather || u >= total) return 0;
+                Tile t;
+                tile_of(u, t);
+                const int at = 32 * warp + lane;
+                return at < t.live ? __ldg(p.rows + t.first + at) : -1;
+            };
+            const int64_t row_bytes = p.k * kRowBytes / S::kElems;
             int it = 0;
-            const bool words = (kv & 3) == 0;  // a row's scales start on a word
+            int next_index = index_of(blockIdx.x);
             for (int u = blockIdx.x; u < total; u += gridDim.x) {
                 Tile t;
-                if (!tile_of(u, t)) continue;
+                tile_of(u, t);
                 const int steps = stages_of(t);
-                const uint8_t* row[4];  // rows lane, lane + 32, ...
+                const uint8_t* from[8];
+                if (p.gather) {
+                    // an index that is no row of x reads row 0; the epilogue zeroes the result
+                    const int index = next_index;
+                    next_index = index_of(u + gridDim.x);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = lane + 32 * i;
-                    int64_t r = -1;
-                    if (at < t.live) r = p.gather ? (int64_t)__ldg(p.rows + t.first + at) : t.first + at;
-                    row[i] = r >= 0 && r < p.x_rows ? p.x_sf + r * kv : nullptr;
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = __shfl_sync(kFull, index, sub + 4 * i);
+                        from[i] = p.x_q + (r > 0 && r < p.x_rows ? r : 0) * row_bytes + 16 * chunk;
+                    }
                 }
                 for (int s = 0; s < steps; ++s, ++it) {
-                    if ((it & 1) != warp - 2) continue;
-                    uint32_t w[S::kScaleTiles][4];
-#pragma unroll
-                    for (int j = 0; j < S::kScaleTiles; ++j) {
-                        const int64_t at = ((int64_t)s * S::kScaleTiles + j) * 4;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w[j][i] = row[i] && at < kv ? load_word(row[i] + at, kv - at, words) : 0u;
-                    }
                     const int st = it % kStages;
                     if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
-                    uint8_t* dst = stages + kSfBase + st * kSfStage + 16 * lane;
+                    const uint32_t bar = smem_addr(&ctl->full[st]);
+                    if (p.gather) {
+                        const int64_t at = (int64_t)s * kRowBytes;
+                        const bool in = at + 16 * chunk < row_bytes;  // past the row's end: zeros
 #pragma unroll
-                    for (int j = 0; j < S::kScaleTiles; ++j)
-                        *reinterpret_cast<uint4*>(dst + 512 * j) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 32 * warp + sub + 4 * i;
+                            if (r >= t.live) continue;  // such a row is multiplied but never stored
+                            const uint32_t to = base + st * kBytesData + r * kRowBytes + ((chunk ^ (r & 7)) << 4);
+                            asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(to),
+                                         "l"(in ? from[i] + at : p.x_q), "r"(in ? 16 : 0)
+                                         : "memory");
+                        }
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+                    }
+                    uint8_t* dst = stages + kSfBase + st * kSfStage + 16 * lane + 4 * warp;
+                    if (S::kScaleTiles == 4) {
+                        *reinterpret_cast<uint32_t*>(dst) = p0.x;
+                        *reinterpret_cast<uint32_t*>(dst + 512) = p0.y;
+                        *reinterpret_cast<uint32_t*>(dst + 1024) = p0.z;
+                        *reinterpret_cast<uint32_t*>(dst + 1536) = p0.w;
+                    } else {
+                        *reinterpret_cast<uint32_t*>(dst) = (s & 2) ? ((s & 1) ? p0.w : p0.z) : ((s & 1) ? p0.y : p0.x);
+                    }
                     fence_async();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&ctl->full[st]));
+                    if (lane == 0) mbar_arrive(bar);
+                    if (kPiece == 1 || (s & (kPiece - 1)) == kPiece - 1 || s + 1 == steps) {
+                        p0 = p1;
+                        p1 = p2;
+                        p2 = next_piece();
+                    }
                 }
             }
         }
@@ -499,93 +586,74 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 // 32 columns of each half; those shared with the other accumulator first: the upper
                 // columns of the second half (buffer 0), the lower ones of the first (buffer 1)
                 const int c = 32 * (group + 2 * (buf ? i : 1 - i));
-                float v[32], w[32];
-                __syncwarp();  // rows that do not exist have skipped ahead
-                {
-                    uint32_t raw0[32], raw1[32];
-                    if (any) {
-                        tc_load32(acc + c, raw0);
-                        if (halves == 2) tc_load32(acc + 128 + c, raw1);
-                        tc_wait_load();
-                        if (i == (S::kShared <= 64 ? 0 : 1)) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(smem_addr(&ctl->acc_free));
-                        }
-                    }
-                    scaled(raw0, scale0, exists && any, v);
-                    if (halves == 2) scaled(raw1, scale1, exists && any, w);
-                }
-                if (GRAD) {
-                    const int64_t row = (int64_t)t.m * kTileM + r;
-                    if (row >= g.n) continue;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int64_t col = (int64_t)t.n * 256 + 128 * h + c;
-                        const int cols = (int)min((int64_t)32, g.k - col);
-                        if (h >= halves || cols <= 0) continue;
-                        float(&x)[32] = h ? w : v;
-                        const int64_t at = (t.e * g.n + row) * g.k + col;
-                        if (g.f32) {
-                            float* o = static_cast<float*>(g.out) + at;
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                if (4 * q >= cols) continue;
-                                float4 y = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-                                float4* to = reinterpret_cast<float4*>(o) + q;
-                                if (g.accumulate) {
-                                    const float4 b = *to;
-                                    y = make_float4(y.x + b.x, y.y + b.y, y.z + b.z, y.w + b.w);
-                                }
-                                *to = y;
-                            }
-                        } else {
-                            uint16_t* o = static_cast<uint16_t*>(g.out) + at;
-                            if (g.accumulate) add_row(o, cols, x);
-                            uint32_t words[16];
-                            to_words(x, words);
-                            store_words(o, words, cols, ((uintptr_t)o & 31) == 0);
-                        }
-                    }
-                    continue;
-                }
-                if (r >= t.live) continue;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && (p.gated || halves == 1)) continue;
-                    const int64_t col = p.gated ? (int64_t)t.n * 128 + c : (int64_t)t.n * 256 + 128 * h + c;
-                    const int cols = (int)min((int64_t)32, p.n - col);
-                    if (cols <= 0) continue;
-                    float(&x)[32] = h ? w : v;
+                const int passes = !GRAD && p.gated ? 1 : halves;
+#pragma unroll 1
+                for (int h = 0; h < passes; ++h) {
                     uint32_t words[16];
-                    if (p.bias) add_row(p.bias + t.e * p.n + col, cols, x);
-                    if (p.gated && p.up_bias) add_row(p.up_bias + t.e * p.n + col, cols, w);
-                    if (p.pre) {
-                        uint16_t* o = p.pre + slot * p.ld_pre + col;
-                        to_words(x, words);
-                        store_words(o, words, cols, ((uintptr_t)o & 31) == 0);
-                        if (p.gated) {
-                            o += p.n;
-                            to_words(w, words);
-                            store_words(o, words, cols, ((uintptr_t)o & 31) == 0);
-                        }
-                    }
-                    activate32(p.act, x);
-                    if (p.gated) {
+                    const int64_t col = !GRAD && p.gated ? (int64_t)t.n * 128 + c : (int64_t)t.n * 256 + 128 * h + c;
+                    const int cols = (int)min((int64_t)32, (GRAD ? g.k : p.n) - col);
+                    const bool store = cols > 0 && (GRAD ? (int64_t)t.m * kTileM + r < g.n : r < t.live);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] *= w[j];
-                    }
-                    if (p.residual) add_row(p.residual + slot * p.ld_residual + col, cols, x);
-                    to_words(x, words);
-                    uint16_t* o = p.out + slot * p.ld_out + col;
-                    store_words(o, words, cols, ((uintptr_t)o & 31) == 0);
-                    if (p.q) {  // n is a multiple of 32: a whole block in this thread
-                        uint32_t codes[8];
-                        const uint32_t sc = qzq::mxfp8_block(words, codes);
-                        uint8_t* to = p.q + slot * p.n + col;
-                        st_v4(to, make_uint4(codes[0], codes[1], codes[2], codes[3]));
-                        st_v4(to + 16, make_uint4(codes[4], codes[5], codes[6], codes[7]));
-                        p.sf[slot * (p.n / 32) + col / 32] = (uint8_t)sc;
+                    for (int b = 0; b < 2; ++b) {
+                        float x[16], y[16];
+                        __syncwarp();  // rows that are not stored have skipped ahead
+                        {
+                            uint32_t raw[16], raw_up[16];
+                            if (any) {
+                                tc_load16(acc + 128 * h + c + 16 * b, raw);
+                                if (!GRAD && p.gated) tc_load16(acc + 128 + c + 16 * b, raw_up);
+                                tc_wait_load();
+                                if (b == 1 && h == passes - 1 && i == (S::kShared <= 64 ? 0 : 1)) {
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) mbar_arrive(smem_addr(&ctl->acc_free));
+                                }
+                            }
+                            scaled(raw, scale0, exists && any, x);
+                            if (!GRAD && p.gated) scaled(raw_up, scale1, exists && any, y);
+                        }
+                        const int n = cols - 16 * b;  // columns of this piece
+                        if (!store || n <= 0) continue;
+                        const int64_t at = col + 16 * b;
+                        if (GRAD) {
+                            const int64_t to = (t.e * g.n + (int64_t)t.m * kTileM + r) * g.k + at;
+                            if (g.f32) {
+                                store_f32(static_cast<float*>(g.out) + to, x, n, g.accumulate);
+                            } else {
+                                uint16_t* o = static_cast<uint16_t*>(g.out) + to;
+                                if (g.accumulate) add_row(o, n, x);
+                                to_words(x, words);
+                                store_words(o, words, n);
+                            }
+                            continue;
+                        }
+                        if (p.bias) add_row(p.bias + t.e * p.n + at, n, x);
+                        if (p.gated && p.up_bias) add_row(p.up_bias + t.e * p.n + at, n, y);
+                        if (p.pre) {
+                            uint16_t* o = p.pre + slot * p.ld_pre + at;
+                            to_words(x, words + 8 * b);
+                            store_words(o, words + 8 * b, n);
+                            if (p.gated) {
+                                to_words(y, words + 8 * b);
+                                store_words(o + p.n, words + 8 * b, n);
+                            }
+                        }
+                        activate(p.act, x);
+                        if (p.gated) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) x[j] *= y[j];
+                        }
+                        if (p.residual) add_row(p.residual + slot * p.ld_residual + at, n, x);
+                        to_words(x, words + 8 * b);
+                        store_words(p.out + slot * p.ld_out + at, words + 8 * b, n);
+                        if (p.q && b == 1) {  // n is a multiple of 32: a whole block in this lane
+                            uint32_t codes[8];
+                            const uint32_t sc = qzq::mxfp8_block(words, codes);
+                            uint8_t* to = p.q + slot * p.n + col;
+                            st_v4(to, make_uint4(codes[0], codes[1], codes[2], codes[3]));
+                            st_v4(to + 16, make_uint4(codes[4], codes[5], codes[6], codes[7]));
+                            p.sf[slot * (p.n / 32) + col / 32] = (uint8_t)sc;
+                        }
                     }
                 }
             }
@@ -603,7 +671,7 @@ done:
         while (global_ns() - start < 20000000ull) __nanosleep(1000);
     }
     tc_fence_after();
-    if (warp == 1) tmem_free(tmem, 512);
+    if (warp == 13) tmem_free(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -670,6 +738,9 @@ cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsign
     q.x_rows = p.x_rows;
     q.slots = p.slots;
     q.w_sf_stride = p.w_sf_stride;
+    // an x without rows: every slot reads a row of zeros, so any mapped memory does
+    const void* x = p.x_rows > 0 ? p.x_q : p.w_q;
+    q.x_q = static_cast<const uint8_t*>(x);
     q.x_sf = p.x_sf;
     q.w_sf = p.w_sf;
     q.up_sf = p.up_sf;
@@ -692,10 +763,8 @@ cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsign
     q.sf = p.sf;
     q.d_err = d_err;
     const int64_t row_bytes = fp4 ? p.k / 2 : p.k;
-    // an x without rows: every slot reads a row of zeros, so any mapped memory does for the map
-    const void* x = p.x_rows > 0 ? p.x_q : p.w_q;
     CUtensorMap ma, mb, mu;
-    if (!make_map(&ma, x, row_bytes, p.x_rows > 0 ? p.x_rows : 1, 0, 0, q.gather ? 1 : 32)) return cudaErrorInvalidValue;
+    if (!make_map(&ma, x, row_bytes, p.x_rows > 0 ? p.x_rows : 1, 0, 0, 32)) return cudaErrorInvalidValue;
     if (!make_map(&mb, p.w_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
     mu = mb;
     if (q.gated && !make_map(&mu, p.up_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
