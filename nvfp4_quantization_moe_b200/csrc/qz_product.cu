@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const uint32_t dst_sf = base + kSfBase + st * kSfStage;
                 const int64_t tile0 = (GRAD ? t.first / (4 * S::kBlock) : 0) + (int64_t)s * S::kScaleTiles;
                 const uint32_t sf_bytes = 512u * (uint32_t)min((int64_t)S::kScaleTiles, scale_tiles - tile0);
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_arrive_tx(bar, bytes_a + halves * (kBytesA + sf_bytes) + (GRAD ? sf_bytes : 0u));
                     for (int h = 0; h < halves; ++h) {
                         const uint32_t db = dst + kBytesA * (1 + h), ds = dst_sf + kScaleBytes * (1 + h);
@@ -394,51 +394,56 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
     } else if (warp == 13) {
         // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            int it = 0, done_tiles = 0;
-            for (int u = blockIdx.x; u < total; u += gridDim.x) {
-                Tile t;
-                if (!tile_of(u, t)) continue;
-                const int halves = halves_of(t), steps = stages_of(t);
-                if (steps == 0) continue;
-                // the epilogue of the tile before has drained the columns both accumulators share
-                if (done_tiles > 0 && !mbar_wait(smem_addr(&ctl->acc_free), (done_tiles - 1) & 1, abort)) goto done;
+        int it = 0, done_tiles = 0;
+        for (int u = blockIdx.x; u < total; u += gridDim.x) {
+            Tile t;
+            if (!tile_of(u, t)) continue;
+            const int halves = halves_of(t), steps = stages_of(t);
+            if (steps == 0) continue;
+            // the epilogue of the tile before has drained the columns both accumulators share
+            if (done_tiles > 0 && !__all_sync(kFull, mbar_wait(smem_addr(&ctl->acc_free), (done_tiles - 1) & 1, abort))) goto done;
+            tc_fence_after();
+            const uint32_t acc = tmem + ((done_tiles & 1) ? kAcc1 : 0);
+            const int last = (int)((t.depth - (int64_t)(steps - 1) * S::kElems + S::kMma - 1) / S::kMma);
+            for (int s = 0; s < steps; ++s, ++it) {
+                const int st = it % kStages;
+                // scale buffers are fewer than stages: the products that read this one two steps ago are done
+                if (S::kScaleBufs < kStages && it >= S::kScaleBufs) {
+                    const int b = it - S::kScaleBufs;
+                    if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[b % kStages]), (b / kStages) & 1, abort))) goto done;
+                }
+                if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->full[st]), (it / kStages) & 1, abort))) goto done;
+                if (!GRAD && p.gather) fence_async();  // the gathered rows were written by cp.async
                 tc_fence_after();
-                const uint32_t acc = tmem + ((done_tiles & 1) ? kAcc1 : 0);
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const int st = it % kStages;
-                    // scale buffers are fewer than stages: the products that read this one two steps ago are done
-                    if (S::kScaleBufs < kStages && it >= S::kScaleBufs) {
-                        const int b = it - S::kScaleBufs;
-                        if (!mbar_wait(smem_addr(&ctl->empty[b % kStages]), (b / kStages) & 1, abort)) goto done;
-                    }
-                    if (!mbar_wait(smem_addr(&ctl->full[st]), (it / kStages) & 1, abort)) goto done;
-                    if (!GRAD && p.gather) fence_async();  // the gathered rows were written by cp.async
-                    tc_fence_after();
+                const int products = s + 1 < steps ? S::kElems / S::kMma : last;
+                if (elect_one()) {
                     const uint32_t data = base + st * kBytesData, sfs = base + kSfBase + st * kSfStage;
                     const uint32_t col = tmem + kScaleCol + (it % S::kScaleBufs) * S::kScaleCols;
+                    const uint64_t da = operand_desc(data), db = operand_desc(data + kBytesA), ds = scale_desc(sfs);
+                    const uint32_t idesc = mma_idesc<FMT>(128 * halves, 0);
                     // A's tiles, then each half's: 4 columns per tile; for NVFP4 tile j of both
-                    // halves lie side by side, as one product of 256 columns reads them
+                    // halves lie side by side, as one product of 256 columns reads them.
+                    // (Descriptors hold addresses in units of 16 bytes.)
 #pragma unroll
-                    for (int j = 0; j < S::kScaleTiles; ++j) {
-                        tc_copy_scales(col + 4 * j, scale_desc(sfs + 512 * j));
-                        for (int h = 0; h < halves; ++h)
-                            tc_copy_scales(col + 4 * S::kScaleTiles + 8 * j + 4 * h,
-                                           scale_desc(sfs + kScaleBytes * (1 + h) + 512 * j));
-                    }
-                    const int64_t left = t.depth - (int64_t)s * S::kElems;
-                    const int products = (int)min((int64_t)(S::kElems / S::kMma), (left + S::kMma - 1) / S::kMma);
-                    for (int k = 0; k < products; ++k) {
+                    for (int k = 0; k < S::kElems / S::kMma; ++k) {
+                        if (k >= products) break;
                         const int j = S::kScaleTiles == 1 ? 0 : k;
-                        tc_mma<FMT>(acc, operand_desc(data + 32 * k), operand_desc(data + kBytesA + 32 * k),
-                                    mma_idesc<FMT>(128 * halves, k), col + 4 * j, col + 4 * S::kScaleTiles + 8 * j,
-                                    (s | k) != 0);
+                        if (j == k) {
+                            tc_copy_scales(col + 4 * j, ds + 32 * j);
+                            tc_copy_scales(col + 4 * S::kScaleTiles + 8 * j, ds + ((kScaleBytes + 512 * j) >> 4));
+                            if (halves == 2)
+                                tc_copy_scales(col + 4 * S::kScaleTiles + 8 * j + 4, ds + ((2 * kScaleBytes + 512 * j) >> 4));
+                        }
+                        tc_mma<FMT>(acc, da + 2 * k, db + 2 * k,
+                                    idesc | (FMT == QZ_FMT_MXFP8 ? ((uint32_t)k << 4) | ((uint32_t)k << 29) : 0u), col + 4 * j,
+                                    col + 4 * S::kScaleTiles + 8 * j, (s | k) != 0);
                     }
                     tc_commit(smem_addr(&ctl->empty[st]));
+                    if (s + 1 == steps) tc_commit(smem_addr(&ctl->acc_full[done_tiles & 1]));
                 }
-                tc_commit(smem_addr(&ctl->acc_full[done_tiles & 1]));
-                ++done_tiles;
+                __syncwarp();
             }
+            ++done_tiles;
         }
     } else if (warp < kRowWarps) {
         // ------------------------------------------------------------ rows of x
