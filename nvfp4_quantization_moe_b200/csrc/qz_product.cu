@@ -14,18 +14,23 @@
 // 32 KB of weights, and four such stages (192 KB, almost the whole shared
 // memory) keep enough bytes in flight for HBM when the tile has few live rows.
 //
-// Roles of the 14 warps of the one CTA per SM (persistent over its tiles):
-//   0..3   x: each lane owns one row's scales (linear; 16 bytes at a time, three
+// Roles of the 12 warps of the one CTA per SM (persistent over its tiles).
+// Twelve, because that leaves a thread 168 registers: with the shared memory in
+// use L1 is too small to hold spills, and an epilogue that spilled 500 bytes a
+// thread took three times as long.
+//   0, 1   x: a lane owns two rows' scales (linear; 16 bytes at a time, three
 //          such pieces ahead, written into the 512-byte tile form), and with a
 //          row index the warps also gather the rows themselves by 16-byte
 //          cp.async in the 128-byte swizzle.  (TMA's gather of four rows was
 //          measured first: about 55 ns per 512 bytes, 352 us against 181 us
-//          without an index on 4096 tokens x 8 experts, 2 x 768 x 2048.)
+//          without an index on 4096 tokens x 8 experts, 2 x 768 x 2048.)  They
+//          also fetch the weights' scales: a swizzled 512-byte tile is exactly
+//          what tcgen05.cp wants, one bulk copy.
+//   2      TMA: the weights (tiled, 128-byte swizzle), and x when it has no index.
+//          A thread issues a copy in about 65 clocks, so a stage's copies are
+//          shared with the warps above.
+//   3      one thread copies scales to tensor memory and issues the products
 //   4..11  epilogue: warp w % 4 owns the lanes (rows) 32 (w % 4) .. + 31
-//   12     TMA: weights (tiled, 128-byte swizzle), their scales (a swizzled
-//          512-byte tile is exactly what tcgen05.cp wants: one bulk copy), and
-//          x when it has no index
-//   13     one thread copies scales to tensor memory and issues the products
 //
 // Tensor memory (512 columns): two accumulators of 256 columns and the scales
 // do not fit side by side, so the accumulators overlap, [0, 256) and
@@ -45,10 +50,10 @@ namespace qz {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kTileM = 128;
-constexpr int kStages = 4;
-constexpr int kProductThreads = 448;
-constexpr int kRowWarps = 4;
+constexpr int kProductThreads = 384;
+constexpr int kRowWarps = 2;
 constexpr int kEpilogueWarps = 8;
+constexpr int kStagingBytes = 2048;               // of an epilogue warp: 64 bytes of its 32 rows
 constexpr uint32_t kRowBytes = 128;               // contraction bytes of a stage
 constexpr uint32_t kBytesA = kTileM * kRowBytes;  // 16 KB; each half of B the same
 constexpr uint32_t kBytesData = 3 * kBytesA;
@@ -60,12 +65,12 @@ template <int FMT>
 struct Shape;
 template <>
 struct Shape<QZ_FMT_MXFP8> {
-    static constexpr int kElems = 128, kMma = 32, kBlock = 32, kScaleTiles = 1;
+    static constexpr int kElems = 128, kMma = 32, kBlock = 32, kScaleTiles = 1, kStages = 4;
     static constexpr int kScaleCols = 12, kScaleBufs = kStages, kShared = 64;
 };
 template <>
 struct Shape<QZ_FMT_NVFP4> {
-    static constexpr int kElems = 256, kMma = 64, kBlock = 16, kScaleTiles = 4;
+    static constexpr int kElems = 256, kMma = 64, kBlock = 16, kScaleTiles = 4, kStages = 3;
     static constexpr int kScaleCols = 48, kScaleBufs = 2, kShared = 96;
 };
 
@@ -74,7 +79,7 @@ struct Shape<QZ_FMT_NVFP4> {
 template <int FMT>
 constexpr uint32_t kScaleStage = 3u * 512u * Shape<FMT>::kScaleTiles;
 template <int FMT>
-constexpr uint32_t kStagesBytes = kStages * (kBytesData + kScaleStage<FMT>);
+constexpr uint32_t kStagesBytes = Shape<FMT>::kStages * (kBytesData + kScaleStage<FMT>);
 
 struct ProductArgs {
     int act, n_experts, gated, x_per_row, gather, n_blocks;
@@ -109,7 +114,7 @@ struct Tile {
 
 // The shared-memory words of the roles, in front of the stages.
 struct Control {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[4], empty[4];
     uint64_t acc_full[2], acc_free;
     uint32_t tmem;
     int abort;
@@ -180,30 +185,52 @@ __device__ __forceinline__ uint32_t load_word(const uint8_t* p, int64_t take, bo
 // epilogue pieces
 // ---------------------------------------------------------------------------
 
-// A lane handles 16 columns of its row at a time (the register budget of 14
-// warps), two such pieces making one MXFP8 block.
+// A lane computes 32 columns of its row at a time (one MXFP8 block); the code
+// that does so exists once in a kernel: unrolled over a tile's columns it was
+// larger than the instruction caches and took twice the time.
 
-// 16 fp32 columns as 8 bf16 words.
-__device__ __forceinline__ void to_words(const float (&v)[16], uint32_t* w) {
+// 32 fp32 columns as bf16 words.
+__device__ __forceinline__ void to_words(const float (&v)[32], uint32_t (&w)[16]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = bf16x2_of(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 16; ++i) w[i] = bf16x2_of(v[2 * i], v[2 * i + 1]);
 }
 
-// The first `cols` (a multiple of 8) of 16 columns of a row.
-__device__ __forceinline__ void store_words(uint16_t* p, const uint32_t* w, int cols) {
-    const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
-    if (cols >= 16 && ((uintptr_t)p & 31) == 0) {
-        st_v8(p, a, b);
-        return;
+// Each lane's 64 bytes w (of row `lane`) to 64-byte pieces of 32 rows in
+// global memory, `pitch` bytes apart, by way of the warp's 2 KB of shared
+// memory: a store instruction then covers 64 consecutive bytes of 8 rows in
+// place of 32 bytes of 32 rows.  Only the first `rows` rows and `bytes` bytes
+// are written; ADD adds fp32 values to what is there.
+template <bool ADD>
+__device__ __forceinline__ void store_rows(uint8_t* to, int64_t pitch, const uint32_t (&w)[16], int rows, int bytes,
+                                           uint8_t* staging, int lane) {
+    // 16-byte chunk c of row r lies at c ^ (r / 2 % 4): no bank conflicts either way
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(staging + 64 * lane + 16 * (c ^ ((lane >> 1) & 3))) =
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    __syncwarp();
+    const int c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        uint4 v = *reinterpret_cast<const uint4*>(staging + 64 * r + 16 * (c ^ ((r >> 1) & 3)));
+        if (r < rows && 16 * c < bytes) {
+            uint8_t* const at = to + r * pitch + 16 * c;
+            if (ADD) {
+                const float4 b = *reinterpret_cast<const float4*>(at);
+                v = make_uint4(__float_as_uint(__uint_as_float(v.x) + b.x), __float_as_uint(__uint_as_float(v.y) + b.y),
+                               __float_as_uint(__uint_as_float(v.z) + b.z), __float_as_uint(__uint_as_float(v.w) + b.w));
+            }
+            st_v4(at, v);
+        }
     }
-    if (cols > 0) st_v4(p, a);
-    if (cols > 8) st_v4(p + 8, b);
 }
 
-// v += the first `cols` of 16 bf16 columns at p.
-__device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[16]) {
+// v += the first `cols` of 32 bf16 columns at p.
+__device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
         if (8 * i >= cols) continue;
         const uint4 r = *reinterpret_cast<const uint4*>(p + 8 * i);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -215,68 +242,55 @@ __device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[
     }
 }
 
-// The first n (a multiple of 8) of 16 fp32 columns at p, added to what is there if `add`.
-__device__ __forceinline__ void store_f32(float* p, float (&v)[16], int n, bool add) {
-    const bool wide = ((uintptr_t)p & 31) == 0;
+// SiLU and GELU are both z sigmoid(z (a + b z^2)), with (1, 0) and (2 sqrt(2/pi), 2 sqrt(2/pi) 0.044715).
+__device__ __forceinline__ void activate(int act, float (&v)[32]) {
+    if (act == QZ_ACT_NONE) return;
+    if (act == QZ_ACT_RELU) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        if (8 * q >= n) continue;
-        uint4 y[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float4 f = make_float4(v[8 * q + 4 * j], v[8 * q + 4 * j + 1], v[8 * q + 4 * j + 2], v[8 * q + 4 * j + 3]);
-            if (add) {
-                const float4 b = *(reinterpret_cast<const float4*>(p) + 2 * q + j);
-                f = make_float4(f.x + b.x, f.y + b.y, f.z + b.z, f.w + b.w);
-            }
-            y[j] = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
-        }
-        if (wide) {
-            st_v8(p + 8 * q, y[0], y[1]);
-        } else {
-            st_v4(p + 8 * q, y[0]);
-            st_v4(p + 8 * q + 4, y[1]);
-        }
+        for (int i = 0; i < 32; ++i) v[i] = fmaxf(v[i], 0.0f);
+        return;
     }
-}
-
-template <int ACT>
-__device__ __forceinline__ void act16(float (&v)[16]) {
+    const float a = act == QZ_ACT_GELU ? kGelu2 : 1.0f, b = act == QZ_ACT_GELU ? kGelu2 * kGeluC : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = act_value<ACT>(v[i]);
-}
-
-__device__ __forceinline__ void activate(int act, float (&v)[16]) {
-    if (act == QZ_ACT_SILU) act16<QZ_ACT_SILU>(v);
-    else if (act == QZ_ACT_GELU) act16<QZ_ACT_GELU>(v);
-    else if (act == QZ_ACT_RELU) act16<QZ_ACT_RELU>(v);
+    for (int i = 0; i < 32; ++i) v[i] *= sigmoid32(v[i] * fmaf(b * v[i], v[i], a));
 }
 
 __device__ __forceinline__ float amax_scale(const float* amax, int64_t i) {
     return amax != nullptr ? __fdiv_rn(__ldg(amax + i), 2688.0f) : 1.0f;
 }
 
-// Accumulator columns times g (NVFP4's second-level scales), 0 for a row that does not exist.
-__device__ __forceinline__ void scaled(const uint32_t (&raw)[16], float g, bool exists, float (&v)[16]) {
+// Accumulator columns times g (NVFP4's second-level scales), zeros for a row that does not exist.
+template <int FMT>
+__device__ __forceinline__ void scale_row(float g, bool exists, float (&v)[32]) {
+    if (FMT == QZ_FMT_NVFP4) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = exists ? __uint_as_float(raw[i]) * g : 0.0f;
+        for (int i = 0; i < 32; ++i) v[i] *= g;
+    }
+    if (!exists) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    }
 }
 
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
 
-// GRAD: the weight gradient (args.g), otherwise the product (args.p).
+enum Kind { kPlain, kGated, kWeightGrad };  // the product, its gated form (args.p), the weight gradient (args.g)
+
 union Args {
     ProductArgs p;
     GradArgs g;
 };
 
-template <int FMT, bool GRAD>
+template <int FMT, int KIND>
 __global__ void __launch_bounds__(kProductThreads, 1)
     experts_kernel(const __grid_constant__ Args args, const __grid_constant__ CUtensorMap map_a,
-                   const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_up) {
+                   const __grid_constant__ CUtensorMap map_low, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_up) {
     typedef Shape<FMT> S;
+    constexpr int kStages = S::kStages;
+    constexpr bool GRAD = KIND == kWeightGrad, GATED = KIND == kGated;
     constexpr uint32_t kSfBase = kStages * kBytesData, kSfStage = kScaleStage<FMT>;
     constexpr uint32_t kScaleBytes = 512u * S::kScaleTiles;  // of 128 rows
     constexpr int kAcc1 = 256 - S::kShared;
@@ -285,7 +299,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // the stages start at the next 1024-byte boundary (the swizzle's period)
     const uint32_t base = (smem_addr(smem) + 1023u) & ~1023u;
     uint8_t* const stages = smem + (base - smem_addr(smem));
-    Control* const ctl = reinterpret_cast<Control*>(stages + kStagesBytes<FMT>);
+    uint8_t* const staging = stages + kStagesBytes<FMT>;  // of the epilogue warps
+    Control* const ctl = reinterpret_cast<Control*>(staging + kEpilogueWarps * kStagingBytes);
     int* const s_prefix = reinterpret_cast<int*>(ctl + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -294,8 +309,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            // TMA; the warps of x's scales; every lane of them when it gathers rows
-            mbar_init(smem_addr(&ctl->full[i]), GRAD ? 1 : 1 + kRowWarps + (p.gather ? 32 * kRowWarps : 0));
+            // TMA; the row warps; every lane of them when they gather
+            mbar_init(smem_addr(&ctl->full[i]), 1 + kRowWarps + (!GRAD && p.gather ? 32 * kRowWarps : 0));
             mbar_init(smem_addr(&ctl->empty[i]), 1);
         }
         mbar_init(smem_addr(&ctl->acc_full[0]), 1);
@@ -306,7 +321,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_b);
     }
-    if (warp == 13) tmem_alloc(smem_addr(&ctl->tmem), 512);
+    if (warp == 3) tmem_alloc(smem_addr(&ctl->tmem), 512);
     int total;
     if (GRAD) {
         total = g.n_experts * g.m_blocks * g.n_blocks;
@@ -344,56 +359,48 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // 128-column halves of B that tile t multiplies with
     auto halves_of = [&](const Tile& t) -> int {
         if (GRAD) return (int64_t)t.n * 256 + 128 < g.k ? 2 : 1;
-        return p.gated || (int64_t)t.n * 256 + 128 < p.n ? 2 : 1;
+        return GATED || (int64_t)t.n * 256 + 128 < p.n ? 2 : 1;
     };
     auto stages_of = [&](const Tile& t) -> int { return (int)((t.depth + S::kElems - 1) / S::kElems); };
 
-    if (warp == 12) {
+    if (warp == 2) {
         // ------------------------------------------------------------ TMA
-        int it = 0;
-        for (int u = blockIdx.x; u < total; u += gridDim.x) {
-            Tile t;
-            if (!tile_of(u, t)) continue;
-            const int halves = halves_of(t), steps = stages_of(t);
-            const int boxes = (t.live + 31) / 32;
-            const uint32_t bytes_a = GRAD ? kBytesA : p.gather ? 0u : boxes * 32 * kRowBytes;
-            for (int s = 0; s < steps; ++s, ++it) {
-                const int st = it % kStages;
-                if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
-                const uint32_t bar = smem_addr(&ctl->full[st]), dst = base + st * kBytesData;
-                const uint32_t dst_sf = base + kSfBase + st * kSfStage;
-                const int64_t tile0 = (GRAD ? t.first / (4 * S::kBlock) : 0) + (int64_t)s * S::kScaleTiles;
-                const uint32_t sf_bytes = 512u * (uint32_t)min((int64_t)S::kScaleTiles, scale_tiles - tile0);
-                if (elect_one()) {
-                    mbar_arrive_tx(bar, bytes_a + halves * (kBytesA + sf_bytes) + (GRAD ? sf_bytes : 0u));
-                    for (int h = 0; h < halves; ++h) {
-                        const uint32_t db = dst + kBytesA * (1 + h), ds = dst_sf + kScaleBytes * (1 + h);
-                        if (GRAD) {
-                            const int r = t.n * 256 + 128 * h;
-                            tma_load_2d(db, &map_b, bar, (int)(t.first * 128 / S::kElems) + s * (int)kRowBytes, r);
-                            bulk_load(ds, g.x_sf + (((int64_t)(r / 128)) * scale_tiles + tile0) * 512, sf_bytes, bar);
-                        } else {
-                            const bool up = p.gated && h;
-                            const int r = p.gated ? t.n * 128 : t.n * 256 + 128 * h;
-                            tma_load_3d(db, up ? &map_up : &map_b, bar, s * (int)kRowBytes, r, t.e);
-                            bulk_load(ds, (up ? p.up_sf : p.w_sf) + t.e * p.w_sf_stride +
-                                              ((int64_t)(r / 128) * scale_tiles + tile0) * 512,
-                                      sf_bytes, bar);
-                        }
-                    }
+        if (elect_one()) {
+            int it = 0;
+            for (int u = blockIdx.x; u < total; u += gridDim.x) {
+                Tile t;
+                if (!tile_of(u, t)) continue;
+                const int halves = halves_of(t), steps = stages_of(t);
+                const int row0 = GATED ? t.n * 128 : t.n * 256, row1 = GATED ? row0 : row0 + 128;
+                // x without an index: one box of 128 rows, or boxes of 32 when there are fewer
+                const bool tall = t.live > 96;
+                const int boxes = GRAD || p.gather ? 0 : tall ? 1 : (t.live + 31) / 32;
+                const uint32_t bytes = (uint32_t)halves * kBytesA +
+                                       (GRAD || boxes && tall ? kBytesA : (uint32_t)boxes * 32 * kRowBytes);
+                int x = GRAD ? (int)(t.first * kRowBytes / S::kElems) : 0;
+                for (int s = 0; s < steps; ++s, ++it, x += kRowBytes) {
+                    const int st = it % kStages;
+                    if (!mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort)) goto done;
+                    const uint32_t bar = smem_addr(&ctl->full[st]), dst = base + st * kBytesData;
+                    mbar_arrive_tx(bar, bytes);
                     if (GRAD) {
-                        tma_load_2d(dst, &map_a, bar, (int)(t.first * 128 / S::kElems) + s * (int)kRowBytes, t.m * kTileM);
-                        bulk_load(dst_sf, g.dz_sf + ((int64_t)t.m * scale_tiles + tile0) * 512, sf_bytes, bar);
-                    } else if (!p.gather) {
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(dst + b * 32 * kRowBytes, &map_a, bar, s * (int)kRowBytes, (int)t.first + 32 * b);
+                        tma_load_2d(dst + kBytesA, &map_b, bar, x, row0);
+                        if (halves == 2) tma_load_2d(dst + 2 * kBytesA, &map_b, bar, x, row1);
+                        tma_load_2d(dst, &map_a, bar, x, t.m * kTileM);
+                    } else {
+                        tma_load_3d(dst + kBytesA, &map_b, bar, x, row0, t.e);
+                        if (halves == 2) tma_load_3d(dst + 2 * kBytesA, GATED ? &map_up : &map_b, bar, x, row1, t.e);
+                        if (tall && boxes) tma_load_2d(dst, &map_a, bar, x, (int)t.first);
+                        else
+                            for (int b = 0; b < boxes; ++b)
+                                tma_load_2d(dst + b * 32 * kRowBytes, &map_low, bar, x, (int)t.first + 32 * b);
                     }
                 }
-                __syncwarp();
             }
         }
-    } else if (warp == 13) {
+    } else if (warp == 3) {
         // ------------------------------------------------------------ MMA
+        if (elect_one()) {
         int it = 0, done_tiles = 0;
         for (int u = blockIdx.x; u < total; u += gridDim.x) {
             Tile t;
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const int halves = halves_of(t), steps = stages_of(t);
             if (steps == 0) continue;
             // the epilogue of the tile before has drained the columns both accumulators share
-            if (done_tiles > 0 && !__all_sync(kFull, mbar_wait(smem_addr(&ctl->acc_free), (done_tiles - 1) & 1, abort))) goto done;
+            if (done_tiles > 0 && !mbar_wait(smem_addr(&ctl->acc_free), (done_tiles - 1) & 1, abort)) goto done;
             tc_fence_after();
             const uint32_t acc = tmem + ((done_tiles & 1) ? kAcc1 : 0);
             const int last = (int)((t.depth - (int64_t)(steps - 1) * S::kElems + S::kMma - 1) / S::kMma);
@@ -410,13 +417,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 // scale buffers are fewer than stages: the products that read this one two steps ago are done
                 if (S::kScaleBufs < kStages && it >= S::kScaleBufs) {
                     const int b = it - S::kScaleBufs;
-                    if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[b % kStages]), (b / kStages) & 1, abort))) goto done;
+                    if (!mbar_wait(smem_addr(&ctl->empty[b % kStages]), (b / kStages) & 1, abort)) goto done;
                 }
-                if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->full[st]), (it / kStages) & 1, abort))) goto done;
-                if (!GRAD && p.gather) fence_async();  // the gathered rows were written by cp.async
+                if (!mbar_wait(smem_addr(&ctl->full[st]), (it / kStages) & 1, abort)) goto done;
+                if (!GRAD && p.gather) fence_async();  // the row warps' writes (see there)
                 tc_fence_after();
                 const int products = s + 1 < steps ? S::kElems / S::kMma : last;
-                if (elect_one()) {
+                {
                     const uint32_t data = base + st * kBytesData, sfs = base + kSfBase + st * kSfStage;
                     const uint32_t col = tmem + kScaleCol + (it % S::kScaleBufs) * S::kScaleCols;
                     const uint64_t da = operand_desc(data), db = operand_desc(data + kBytesA), ds = scale_desc(sfs);
@@ -441,88 +448,114 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     tc_commit(smem_addr(&ctl->empty[st]));
                     if (s + 1 == steps) tc_commit(smem_addr(&ctl->acc_full[done_tiles & 1]));
                 }
-                __syncwarp();
             }
             ++done_tiles;
         }
+        }
     } else if (warp < kRowWarps) {
-        // ------------------------------------------------------------ rows of x
-        if (!GRAD) {
-            // a piece: 16 bytes of the lane's row's scales, for kPiece stages
-            constexpr int kPiece = 4 / S::kScaleTiles;
-            const bool words = (kv & 3) == 0, quads = (kv & 15) == 0 && aligned(p.x_sf, 16);
-            // the scales run ahead of the stages over their own walk of the tiles
-            int su = (int)blockIdx.x - (int)gridDim.x, ssteps = 0, ss = 0;
-            const uint8_t* srow = nullptr;
-            auto next_piece = [&]() -> uint4 {
-                ss += kPiece;
-                if (ss >= ssteps) {
-                    su += gridDim.x;
-                    ss = 0;
-                    ssteps = 0;
-                    srow = nullptr;
-                    if (su < total) {
-                        Tile t;
-                        tile_of(su, t);
-                        ssteps = stages_of(t);
-                        const int at = 32 * warp + lane;
+        // ------------------------------------------------------------ rows of x, scales
+        // a piece: 16 bytes of a row's scales, for kPiece stages
+        constexpr int kPiece = 4 / S::kScaleTiles;
+        const bool words = (kv & 3) == 0, quads = (kv & 15) == 0 && !GRAD && aligned(p.x_sf, 16);
+        // the scales of rows 64 warp + lane and + 32 run ahead of the stages, over a walk of the tiles of their own
+        int su = (int)blockIdx.x - (int)gridDim.x, ssteps = 0, ss = 0;
+        const uint8_t* srow[2] = {nullptr, nullptr};
+        auto next_piece = [&](uint4 (&v)[2]) {
+            v[0] = v[1] = make_uint4(0, 0, 0, 0);
+            if (GRAD) return;
+            ss += kPiece;
+            if (ss >= ssteps) {
+                su += gridDim.x;
+                ss = ssteps = 0;
+                srow[0] = srow[1] = nullptr;
+                if (su < total) {
+                    Tile t;
+                    tile_of(su, t);
+                    ssteps = stages_of(t);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int at = 64 * warp + 32 * j + lane;
                         int64_t r = -1;
                         if (at < t.live) r = p.gather ? (int64_t)__ldg(p.rows + t.first + at) : t.first + at;
-                        if (r >= 0 && r < p.x_rows) srow = p.x_sf + r * kv;
+                        if (r >= 0 && r < p.x_rows) srow[j] = p.x_sf + r * kv;
                     }
                 }
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (srow != nullptr) {
-                    const int64_t at = (int64_t)ss * S::kScaleTiles * 4;
-                    if (quads) {
-                        v = __ldg(reinterpret_cast<const uint4*>(srow + at));
-                    } else {
-                        v.x = load_word(srow + at, kv - at, words);
-                        v.y = load_word(srow + at + 4, kv - at - 4, words);
-                        v.z = load_word(srow + at + 8, kv - at - 8, words);
-                        v.w = load_word(srow + at + 12, kv - at - 12, words);
-                    }
-                }
-                return v;
-            };
-            uint4 p0 = next_piece(), p1 = next_piece(), p2 = next_piece();
-            // rows that this lane helps to gather: 32 warp + lane / 8 + 4 i, 16-byte chunk lane % 8
-            const int chunk = lane & 7, sub = lane >> 3;
-            auto index_of = [&](int u) -> int {
-                if (!p.gather || u >= total) return 0;
-                Tile t;
-                tile_of(u, t);
-                const int at = 32 * warp + lane;
-                return at < t.live ? __ldg(p.rows + t.first + at) : -1;
-            };
-            const int64_t row_bytes = p.k * kRowBytes / S::kElems;
-            int it = 0;
-            int next_index = index_of(blockIdx.x);
-            for (int u = blockIdx.x; u < total; u += gridDim.x) {
-                Tile t;
-                tile_of(u, t);
-                const int steps = stages_of(t);
-                const uint8_t* from[8];
-                if (p.gather) {
-                    // an index that is no row of x reads row 0; the epilogue zeroes the result
-                    const int index = next_index;
-                    next_index = index_of(u + gridDim.x);
+            }
+            const int64_t at = (int64_t)ss * S::kScaleTiles * 4;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = __shfl_sync(kFull, index, sub + 4 * i);
-                        from[i] = p.x_q + (r > 0 && r < p.x_rows ? r : 0) * row_bytes + 16 * chunk;
-                    }
+            for (int j = 0; j < 2; ++j) {
+                if (srow[j] == nullptr) continue;
+                if (quads) {
+                    v[j] = __ldg(reinterpret_cast<const uint4*>(srow[j] + at));
+                } else {
+                    v[j].x = load_word(srow[j] + at, kv - at, words);
+                    v[j].y = load_word(srow[j] + at + 4, kv - at - 4, words);
+                    v[j].z = load_word(srow[j] + at + 8, kv - at - 8, words);
+                    v[j].w = load_word(srow[j] + at + 12, kv - at - 12, words);
                 }
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const int st = it % kStages;
-                    if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
-                    const uint32_t bar = smem_addr(&ctl->full[st]);
+            }
+        };
+        uint4 p0[2], p1[2], p2[2];
+        next_piece(p0);
+        next_piece(p1);
+        next_piece(p2);
+        // rows that this lane helps to gather: 64 warp + lane / 8 + 4 i, 16-byte chunk lane % 8
+        const int chunk = lane & 7, sub = lane >> 3;
+        auto indices_of = [&](int u, int (&v)[2]) {
+            v[0] = v[1] = -1;
+            if (GRAD || !p.gather || u >= total) return;
+            Tile t;
+            tile_of(u, t);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int at = 64 * warp + 32 * j + lane;
+                if (at < t.live) v[j] = __ldg(p.rows + t.first + at);
+            }
+        };
+        const int64_t row_bytes = GRAD ? 0 : p.k * kRowBytes / S::kElems;
+        int it = 0;
+        int ahead[2];
+        indices_of(blockIdx.x, ahead);
+        for (int u = blockIdx.x; u < total; u += gridDim.x) {
+            Tile t;
+            if (!tile_of(u, t)) continue;
+            const int halves = halves_of(t), steps = stages_of(t);
+            const uint8_t* from[16];
+            if (!GRAD && p.gather) {
+                // an index that is no row of x reads row 0; the epilogue zeroes the result
+                const int index[2] = {ahead[0], ahead[1]};
+                indices_of(u + gridDim.x, ahead);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int r = __shfl_sync(kFull, index[i / 8], (sub + 4 * i) & 31);
+                    from[i] = p.x_q + (r > 0 && r < p.x_rows ? r : 0) * row_bytes + 16 * chunk;
+                }
+            }
+            // the weights' scales: the tiles of a 128-row block lie side by side along the contraction; warp 0
+            // fetches those of the first half of B (and the gradient's A), warp 1 those of the second
+            int left = (int)scale_tiles;
+            const uint8_t *sfb = nullptr, *sfa = nullptr;
+            if (GRAD) {
+                const int64_t tile0 = t.first / (4 * S::kBlock);
+                left -= (int)tile0;
+                if (warp == 0 || halves == 2) sfb = g.x_sf + ((int64_t)(2 * t.n + warp) * scale_tiles + tile0) * 512;
+                if (warp == 0) sfa = g.dz_sf + ((int64_t)t.m * scale_tiles + tile0) * 512;
+            } else {
+                const int64_t block = GATED ? t.n : 2 * t.n + warp;
+                if (warp == 0 || halves == 2)
+                    sfb = (GATED && warp ? p.up_sf : p.w_sf) + t.e * p.w_sf_stride + block * scale_tiles * 512;
+            }
+            for (int s = 0; s < steps; ++s, ++it, left -= S::kScaleTiles) {
+                const int st = it % kStages;
+                if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
+                const uint32_t bar = smem_addr(&ctl->full[st]);
+                if (!GRAD) {
                     if (p.gather) {
                         const int64_t at = (int64_t)s * kRowBytes;
                         const bool in = at + 16 * chunk < row_bytes;  // past the row's end: zeros
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 32 * warp + sub + 4 * i;
+                        for (int i = 0; i < 16; ++i) {
+                            const int r = 64 * warp + sub + 4 * i;
                             if (r >= t.live) continue;  // such a row is multiplied but never stored
                             const uint32_t to = base + st * kBytesData + r * kRowBytes + ((chunk ^ (r & 7)) << 4);
                             asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(to),
@@ -531,27 +564,42 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         }
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
                     }
-                    uint8_t* dst = stages + kSfBase + st * kSfStage + 16 * lane + 4 * warp;
+                    uint8_t* dst = stages + kSfBase + st * kSfStage + 16 * lane + 8 * warp;
                     if (S::kScaleTiles == 4) {
-                        *reinterpret_cast<uint32_t*>(dst) = p0.x;
-                        *reinterpret_cast<uint32_t*>(dst + 512) = p0.y;
-                        *reinterpret_cast<uint32_t*>(dst + 1024) = p0.z;
-                        *reinterpret_cast<uint32_t*>(dst + 1536) = p0.w;
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(p0[0].x, p0[1].x);
+                        *reinterpret_cast<uint2*>(dst + 512) = make_uint2(p0[0].y, p0[1].y);
+                        *reinterpret_cast<uint2*>(dst + 1024) = make_uint2(p0[0].z, p0[1].z);
+                        *reinterpret_cast<uint2*>(dst + 1536) = make_uint2(p0[0].w, p0[1].w);
                     } else {
-                        *reinterpret_cast<uint32_t*>(dst) = (s & 2) ? ((s & 1) ? p0.w : p0.z) : ((s & 1) ? p0.y : p0.x);
+                        const uint32_t a = (s & 2) ? ((s & 1) ? p0[0].w : p0[0].z) : ((s & 1) ? p0[0].y : p0[0].x);
+                        const uint32_t b = (s & 2) ? ((s & 1) ? p0[1].w : p0[1].z) : ((s & 1) ? p0[1].y : p0[1].x);
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(a, b);
                     }
-                    fence_async();
+                    // a fence here would also wait for the rows in flight: with gathered rows the
+                    // thread that issues the products fences, after the barrier and before it reads
+                    if (!p.gather) fence_async();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar);
-                    if (kPiece == 1 || (s & (kPiece - 1)) == kPiece - 1 || s + 1 == steps) {
-                        p0 = p1;
-                        p1 = p2;
-                        p2 = next_piece();
+                }
+                if (elect_one()) {
+                    const uint32_t dst = base + kSfBase + st * kSfStage;
+                    const uint32_t bytes = 512u * (uint32_t)min(S::kScaleTiles, left);
+                    const int64_t at = (int64_t)s * kScaleBytes;
+                    mbar_arrive_tx(bar, (sfb ? bytes : 0u) + (sfa ? bytes : 0u));
+                    if (sfb) bulk_load(dst + kScaleBytes * (1 + warp), sfb + at, bytes, bar);
+                    if (sfa) bulk_load(dst, sfa + at, bytes, bar);
+                }
+                __syncwarp();
+                if (kPiece == 1 || (s & (kPiece - 1)) == kPiece - 1 || s + 1 == steps) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        p0[j] = p1[j];
+                        p1[j] = p2[j];
                     }
+                    next_piece(p2);
                 }
             }
         }
-    } else {
+    } else if (warp < 4 + kEpilogueWarps) {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3, group = (warp - 4) >> 2;
         const int r = 32 * quarter + lane;  // row of the tile
@@ -576,7 +624,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (FMT == QZ_FMT_NVFP4 && exists) {
                     const float ga = amax_scale(p.x_amax, p.x_per_row ? row : 0);
                     scale0 = ga * amax_scale(p.w_amax, t.e);
-                    scale1 = p.gated ? ga * amax_scale(p.up_amax, t.e) : scale0;
+                    scale1 = GATED ? ga * amax_scale(p.up_amax, t.e) : scale0;
                 }
             }
             const int buf = done_tiles & 1;
@@ -586,81 +634,102 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 tc_fence_after();
                 ++done_tiles;
             }
+            // A warp has 64 columns of each half, in units of 32 (gated: of both halves at once).  The columns
+            // shared with the other accumulator lie in one half, the second of buffer 0, the first of buffer 1:
+            // its two units are loaded first, and with that the next tile's products may begin.
+            const int own = buf ? 0 : 1, c0 = 64 * group;
+            const int half = GATED || halves == 2 ? own : 0;
+            const int units = GATED ? 2 : 2 * halves;
+            float x[32], next[32];
+            if (any) {
+                tc_load32(acc + 128 * half + c0, x);
+                tc_load32(acc + 128 * half + c0 + 32, next);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl->acc_free));
+            }
+            uint8_t* const stage = staging + (warp - 4) * kStagingBytes;
+            const int64_t width = GRAD ? g.k : p.n;
+            const int rows = GRAD ? (int)min((int64_t)32, g.n - (int64_t)t.m * kTileM - 32 * quarter) : t.live - 32 * quarter;
+            const bool row_in = lane < rows;
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                // 32 columns of each half; those shared with the other accumulator first: the upper
-                // columns of the second half (buffer 0), the lower ones of the first (buffer 1)
-                const int c = 32 * (group + 2 * (buf ? i : 1 - i));
-                const int passes = !GRAD && p.gated ? 1 : halves;
-#pragma unroll 1
-                for (int h = 0; h < passes; ++h) {
-                    uint32_t words[16];
-                    const int64_t col = !GRAD && p.gated ? (int64_t)t.n * 128 + c : (int64_t)t.n * 256 + 128 * h + c;
-                    const int cols = (int)min((int64_t)32, (GRAD ? g.k : p.n) - col);
-                    const bool store = cols > 0 && (GRAD ? (int64_t)t.m * kTileM + r < g.n : r < t.live);
+            for (int i = 0; i < units; ++i) {
+                const int h = GATED ? 0 : i < 2 ? half : 1 - half;
+                const int64_t at = (GATED ? (int64_t)t.n * 128 : (int64_t)t.n * 256 + 128 * h) + c0 + 32 * (i & 1);
+                const int cols = (int)min((int64_t)32, width - at);
+                float y[32];  // gated: the up projection
+                if (GATED) {
+                    tc_load32(acc + 128 * (1 - own) + c0 + 32 * i, y);
+                    if (own) {
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        float x[16], y[16];
-                        __syncwarp();  // rows that are not stored have skipped ahead
-                        {
-                            uint32_t raw[16], raw_up[16];
-                            if (any) {
-                                tc_load16(acc + 128 * h + c + 16 * b, raw);
-                                if (!GRAD && p.gated) tc_load16(acc + 128 + c + 16 * b, raw_up);
-                                tc_wait_load();
-                                if (b == 1 && h == passes - 1 && i == (S::kShared <= 64 ? 0 : 1)) {
-                                    tc_fence_before();
-                                    __syncwarp();
-                                    if (lane == 0) mbar_arrive(smem_addr(&ctl->acc_free));
-                                }
-                            }
-                            scaled(raw, scale0, exists && any, x);
-                            if (!GRAD && p.gated) scaled(raw_up, scale1, exists && any, y);
-                        }
-                        const int n = cols - 16 * b;  // columns of this piece
-                        if (!store || n <= 0) continue;
-                        const int64_t at = col + 16 * b;
-                        if (GRAD) {
-                            const int64_t to = (t.e * g.n + (int64_t)t.m * kTileM + r) * g.k + at;
-                            if (g.f32) {
-                                store_f32(static_cast<float*>(g.out) + to, x, n, g.accumulate);
-                            } else {
-                                uint16_t* o = static_cast<uint16_t*>(g.out) + to;
-                                if (g.accumulate) add_row(o, n, x);
-                                to_words(x, words);
-                                store_words(o, words, n);
-                            }
-                            continue;
-                        }
-                        if (p.bias) add_row(p.bias + t.e * p.n + at, n, x);
-                        if (p.gated && p.up_bias) add_row(p.up_bias + t.e * p.n + at, n, y);
-                        if (p.pre) {
-                            uint16_t* o = p.pre + slot * p.ld_pre + at;
-                            to_words(x, words + 8 * b);
-                            store_words(o, words + 8 * b, n);
-                            if (p.gated) {
-                                to_words(y, words + 8 * b);
-                                store_words(o + p.n, words + 8 * b, n);
-                            }
-                        }
-                        activate(p.act, x);
-                        if (p.gated) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) x[j] *= y[j];
-                        }
-                        if (p.residual) add_row(p.residual + slot * p.ld_residual + at, n, x);
-                        to_words(x, words + 8 * b);
-                        store_words(p.out + slot * p.ld_out + at, words + 8 * b, n);
-                        if (p.q && b == 1) {  // n is a multiple of 32: a whole block in this lane
-                            uint32_t codes[8];
-                            const uint32_t sc = qzq::mxfp8_block(words, codes);
-                            uint8_t* to = p.q + slot * p.n + col;
-                            st_v4(to, make_uint4(codes[0], codes[1], codes[2], codes[3]));
-                            st_v4(to + 16, make_uint4(codes[4], codes[5], codes[6], codes[7]));
-                            p.sf[slot * (p.n / 32) + col / 32] = (uint8_t)sc;
+                        for (int j = 0; j < 32; ++j) {
+                            const float z = x[j];
+                            x[j] = y[j];
+                            y[j] = z;
                         }
                     }
+                    scale_row<FMT>(scale1, exists, y);
                 }
+                scale_row<FMT>(scale0, exists && any, x);
+                uint32_t w[16];
+                if (cols <= 0 || rows <= 0) {
+                    // nothing of this unit is in the matrix
+                } else if (GRAD) {
+                    const int64_t to = (t.e * g.n + (int64_t)t.m * kTileM + 32 * quarter) * g.k + at;
+                    if (g.f32) {
+                        uint8_t* o = reinterpret_cast<uint8_t*>(static_cast<float*>(g.out) + to);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(x[16 * b + j]);
+                            if (g.accumulate) store_rows<true>(o + 64 * b, 4 * g.k, w, rows, 4 * (cols - 16 * b), stage, lane);
+                            else store_rows<false>(o + 64 * b, 4 * g.k, w, rows, 4 * (cols - 16 * b), stage, lane);
+                        }
+                    } else {
+                        uint16_t* o = static_cast<uint16_t*>(g.out) + to;
+                        if (g.accumulate && row_in) add_row(o + lane * g.k, cols, x);
+                        to_words(x, w);
+                        store_rows<false>(reinterpret_cast<uint8_t*>(o), 2 * g.k, w, rows, 2 * cols, stage, lane);
+                    }
+                } else {
+                    if (p.bias) add_row(p.bias + t.e * p.n + at, cols, x);
+                    if (GATED && p.up_bias) add_row(p.up_bias + t.e * p.n + at, cols, y);
+                    const int64_t slot0 = t.first + 32 * quarter;  // of lane 0
+                    if (p.pre) {
+                        uint8_t* o = reinterpret_cast<uint8_t*>(p.pre + slot0 * p.ld_pre + at);
+                        to_words(x, w);
+                        store_rows<false>(o, 2 * p.ld_pre, w, rows, 2 * cols, stage, lane);
+                        if (GATED) {
+                            to_words(y, w);
+                            store_rows<false>(o + 2 * p.n, 2 * p.ld_pre, w, rows, 2 * cols, stage, lane);
+                        }
+                    }
+                    activate(p.act, x);
+                    if (GATED) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] *= y[j];
+                    }
+                    if (p.residual && row_in) add_row(p.residual + slot * p.ld_residual + at, cols, x);
+                    to_words(x, w);
+                    store_rows<false>(reinterpret_cast<uint8_t*>(p.out + slot0 * p.ld_out + at), 2 * p.ld_out, w, rows,
+                                      2 * cols, stage, lane);
+                    if (p.q && row_in) {  // n is a multiple of 32: a whole block in this lane
+                        uint32_t c[8];
+                        const uint32_t scale = qzq::mxfp8_block(w, c);
+                        uint8_t* to = p.q + slot * p.n + at;
+                        if (((uintptr_t)to & 31) == 0) {
+                            st_v8(to, make_uint4(c[0], c[1], c[2], c[3]), make_uint4(c[4], c[5], c[6], c[7]));
+                        } else {
+                            st_v4(to, make_uint4(c[0], c[1], c[2], c[3]));
+                            st_v4(to + 16, make_uint4(c[4], c[5], c[6], c[7]));
+                        }
+                        p.sf[slot * (p.n / 32) + at / 32] = (uint8_t)scale;
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = next[j];
+                if (any && i + 2 < units) tc_load32(acc + 128 * (1 - half) + c0 + 32 * i, next);
             }
         }
     }
@@ -676,7 +745,7 @@ done:
         while (global_ns() - start < 20000000ull) __nanosleep(1000);
     }
     tc_fence_after();
-    if (warp == 13) tmem_free(tmem, 512);
+    if (warp == 3) tmem_free(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -715,17 +784,16 @@ static bool make_map(CUtensorMap* m, const void* p, int64_t row_bytes, int64_t r
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, bool GRAD>
-static cudaError_t launch_experts(const Args& a, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mu,
-                                  int n_experts, int grid, cudaStream_t s) {
-    const size_t smem = 1024 + kStagesBytes<FMT> + sizeof(Control) + (n_experts + 1) * sizeof(int);
+template <int FMT, int KIND>
+static cudaError_t launch_experts(const Args& a, const CUtensorMap& ma, const CUtensorMap& ml, const CUtensorMap& mb,
+                                  const CUtensorMap& mu, int n_experts, int grid, cudaStream_t s) {
+    constexpr size_t fixed = 1024 + kStagesBytes<FMT> + kEpilogueWarps * kStagingBytes + sizeof(Control);
     // asked for at its largest: the attribute is one value per device
-    const size_t most = 1024 + kStagesBytes<FMT> + sizeof(Control) + (QZ_MAX_ROUTE_EXPERTS + 1) * sizeof(int);
-    static_assert(1024 + kStagesBytes<FMT> + sizeof(Control) + (QZ_MAX_ROUTE_EXPERTS + 1) * sizeof(int) <= 232448,
-                  "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(experts_kernel<FMT, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    constexpr size_t most = fixed + (QZ_MAX_ROUTE_EXPERTS + 1) * sizeof(int);
+    static_assert(most <= 232448, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(experts_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
-    experts_kernel<FMT, GRAD><<<grid, kProductThreads, smem, s>>>(a, ma, mb, mu);
+    experts_kernel<FMT, KIND><<<grid, kProductThreads, fixed + (n_experts + 1) * sizeof(int), s>>>(a, ma, ml, mb, mu);
     return cudaGetLastError();
 }
 
@@ -768,8 +836,10 @@ cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsign
     q.sf = p.sf;
     q.d_err = d_err;
     const int64_t row_bytes = fp4 ? p.k / 2 : p.k;
-    CUtensorMap ma, mb, mu;
-    if (!make_map(&ma, x, row_bytes, p.x_rows > 0 ? p.x_rows : 1, 0, 0, 32)) return cudaErrorInvalidValue;
+    const int64_t x_rows = p.x_rows > 0 ? p.x_rows : 1;
+    CUtensorMap ma, ml, mb, mu;
+    if (!make_map(&ma, x, row_bytes, x_rows, 0, 0, 128) || !make_map(&ml, x, row_bytes, x_rows, 0, 0, 32))
+        return cudaErrorInvalidValue;
     if (!make_map(&mb, p.w_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
     mu = mb;
     if (q.gated && !make_map(&mu, p.up_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
@@ -777,8 +847,11 @@ cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsign
     const int64_t most = ((p.slots + kTileM - 1) / kTileM + p.n_experts) * q.n_blocks;
     const int64_t rows = p.slots < p.n_experts ? p.slots * q.n_blocks : most;
     const int grid = (int)(rows < ctas ? rows : ctas);
-    return fp4 ? launch_experts<QZ_FMT_NVFP4, false>(a, ma, mb, mu, p.n_experts, grid, s)
-               : launch_experts<QZ_FMT_MXFP8, false>(a, ma, mb, mu, p.n_experts, grid, s);
+    if (q.gated)
+        return fp4 ? launch_experts<QZ_FMT_NVFP4, kGated>(a, ma, ml, mb, mu, p.n_experts, grid, s)
+                   : launch_experts<QZ_FMT_MXFP8, kGated>(a, ma, ml, mb, mu, p.n_experts, grid, s);
+    return fp4 ? launch_experts<QZ_FMT_NVFP4, kPlain>(a, ma, ml, mb, mu, p.n_experts, grid, s)
+               : launch_experts<QZ_FMT_MXFP8, kPlain>(a, ma, ml, mb, mu, p.n_experts, grid, s);
 }
 
 cudaError_t launch_weight_grad(const qz_weight_grad& p, int ctas, cudaStream_t s, unsigned* d_err) {
@@ -810,8 +883,8 @@ cudaError_t launch_weight_grad(const qz_weight_grad& p, int ctas, cudaStream_t s
     const int64_t tiles = (int64_t)p.n_experts * q.m_blocks * q.n_blocks;
     if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     const int grid = (int)(tiles < ctas ? tiles : ctas);
-    return fp4 ? launch_experts<QZ_FMT_NVFP4, true>(a, ma, mb, mb, p.n_experts, grid, s)
-               : launch_experts<QZ_FMT_MXFP8, true>(a, ma, mb, mb, p.n_experts, grid, s);
+    return fp4 ? launch_experts<QZ_FMT_NVFP4, kWeightGrad>(a, ma, ma, mb, mb, p.n_experts, grid, s)
+               : launch_experts<QZ_FMT_MXFP8, kWeightGrad>(a, ma, ma, mb, mb, p.n_experts, grid, s);
 }
 
 }  // namespace qz
