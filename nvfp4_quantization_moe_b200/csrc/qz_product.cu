@@ -18,14 +18,12 @@
 // Twelve, because that leaves a thread 168 registers: with the shared memory in
 // use L1 is too small to hold spills, and an epilogue that spilled 500 bytes a
 // thread took three times as long.
-//   0, 1   x: a lane owns two rows' scales (linear; 16 bytes at a time, three
-//          such pieces ahead, written into the 512-byte tile form), and with a
-//          row index the warps also gather the rows themselves by 16-byte
-//          cp.async in the 128-byte swizzle.  (TMA's gather of four rows was
-//          measured first: about 55 ns per 512 bytes, 352 us against 181 us
-//          without an index on 4096 tokens x 8 experts, 2 x 768 x 2048.)  They
-//          also fetch the weights' scales: a swizzled 512-byte tile is exactly
-//          what tcgen05.cp wants, one bulk copy.
+//   0, 1   scales: a lane copies two rows' scales of x (linear) by 4-byte
+//          cp.async into the 512-byte tile form; the weights' scales need one bulk
+//          copy, since a swizzled 512-byte tile is exactly what tcgen05.cp wants.
+//          With a row index the elected lane also gathers the rows of x, four at
+//          a time (TMA).  (Gathering by 16-byte cp.async was measured: 16 KB a
+//          stage took 1,600 clocks whatever the warps, three times the products.)
 //   2      TMA: the weights (tiled, 128-byte swizzle), and x when it has no index.
 //          A thread issues a copy in about 65 clocks, so a stage's copies are
 //          shared with the warps above.
@@ -84,7 +82,7 @@ constexpr uint32_t kStagesBytes = Shape<FMT>::kStages * (kBytesData + kScaleStag
 struct ProductArgs {
     int act, n_experts, gated, x_per_row, gather, n_blocks;
     int64_t n, k, x_rows, slots, w_sf_stride;
-    const uint8_t *x_q, *x_sf, *w_sf, *up_sf;
+    const uint8_t *x_sf, *w_sf, *up_sf;
     const float *x_amax, *w_amax, *up_amax;
     const int32_t *rows, *offsets, *counts;
     const uint16_t *bias, *up_bias, *residual;
@@ -119,6 +117,7 @@ struct Control {
     uint32_t tmem;
     int abort;
     long long scratch[33];
+    alignas(16) int index[kTileM];
 };
 
 // ---------------------------------------------------------------------------
@@ -309,8 +308,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            // TMA; the row warps; every lane of them when they gather
-            mbar_init(smem_addr(&ctl->full[i]), 1 + kRowWarps + (!GRAD && p.gather ? 32 * kRowWarps : 0));
+            // TMA; the scale warps' bulk copies; their lanes' copies of x's scales
+            mbar_init(smem_addr(&ctl->full[i]), 1 + kRowWarps + (GRAD ? 0 : 32 * kRowWarps));
             mbar_init(smem_addr(&ctl->empty[i]), 1);
         }
         mbar_init(smem_addr(&ctl->acc_full[0]), 1);
@@ -420,7 +419,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     if (!mbar_wait(smem_addr(&ctl->empty[b % kStages]), (b / kStages) & 1, abort)) goto done;
                 }
                 if (!mbar_wait(smem_addr(&ctl->full[st]), (it / kStages) & 1, abort)) goto done;
-                if (!GRAD && p.gather) fence_async();  // the row warps' writes (see there)
+                if (!GRAD) fence_async();  // the scale warps' writes (see there)
                 tc_fence_after();
                 const int products = s + 1 < steps ? S::kElems / S::kMma : last;
                 {
@@ -453,84 +452,31 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
         }
     } else if (warp < kRowWarps) {
-        // ------------------------------------------------------------ rows of x, scales
-        // a piece: 16 bytes of a row's scales, for kPiece stages
-        constexpr int kPiece = 4 / S::kScaleTiles;
-        const bool words = (kv & 3) == 0, quads = (kv & 15) == 0 && !GRAD && aligned(p.x_sf, 16);
-        // the scales of rows 64 warp + lane and + 32 run ahead of the stages, over a walk of the tiles of their own
-        int su = (int)blockIdx.x - (int)gridDim.x, ssteps = 0, ss = 0;
-        const uint8_t* srow[2] = {nullptr, nullptr};
-        auto next_piece = [&](uint4 (&v)[2]) {
-            v[0] = v[1] = make_uint4(0, 0, 0, 0);
-            if (GRAD) return;
-            ss += kPiece;
-            if (ss >= ssteps) {
-                su += gridDim.x;
-                ss = ssteps = 0;
-                srow[0] = srow[1] = nullptr;
-                if (su < total) {
-                    Tile t;
-                    tile_of(su, t);
-                    ssteps = stages_of(t);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int at = 64 * warp + 32 * j + lane;
-                        int64_t r = -1;
-                        if (at < t.live) r = p.gather ? (int64_t)__ldg(p.rows + t.first + at) : t.first + at;
-                        if (r >= 0 && r < p.x_rows) srow[j] = p.x_sf + r * kv;
-                    }
-                }
-            }
-            const int64_t at = (int64_t)ss * S::kScaleTiles * 4;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (srow[j] == nullptr) continue;
-                if (quads) {
-                    v[j] = __ldg(reinterpret_cast<const uint4*>(srow[j] + at));
-                } else {
-                    v[j].x = load_word(srow[j] + at, kv - at, words);
-                    v[j].y = load_word(srow[j] + at + 4, kv - at - 4, words);
-                    v[j].z = load_word(srow[j] + at + 8, kv - at - 8, words);
-                    v[j].w = load_word(srow[j] + at + 12, kv - at - 12, words);
-                }
-            }
-        };
-        uint4 p0[2], p1[2], p2[2];
-        next_piece(p0);
-        next_piece(p1);
-        next_piece(p2);
-        // rows that this lane helps to gather: 64 warp + lane / 8 + 4 i, 16-byte chunk lane % 8
-        const int chunk = lane & 7, sub = lane >> 3;
-        auto indices_of = [&](int u, int (&v)[2]) {
-            v[0] = v[1] = -1;
-            if (GRAD || !p.gather || u >= total) return;
-            Tile t;
-            tile_of(u, t);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int at = 64 * warp + 32 * j + lane;
-                if (at < t.live) v[j] = __ldg(p.rows + t.first + at);
-            }
-        };
-        const int64_t row_bytes = GRAD ? 0 : p.k * kRowBytes / S::kElems;
+        // ------------------------------------------------------------ scales, gathered rows
+        const bool words = (kv & 3) == 0;  // a row's scales start on a word
+        int* const index = ctl->index + 64 * warp;  // rows 64 warp .. + 63 of the tile
         int it = 0;
-        int ahead[2];
-        indices_of(blockIdx.x, ahead);
         for (int u = blockIdx.x; u < total; u += gridDim.x) {
             Tile t;
             if (!tile_of(u, t)) continue;
             const int halves = halves_of(t), steps = stages_of(t);
-            const uint8_t* from[16];
-            if (!GRAD && p.gather) {
-                // an index that is no row of x reads row 0; the epilogue zeroes the result
-                const int index[2] = {ahead[0], ahead[1]};
-                indices_of(u + gridDim.x, ahead);
+            const uint8_t* srow[2] = {nullptr, nullptr};
+            if (!GRAD) {
+                // an index that is no row of x reads row 0 and a row past the expert's end nothing at all:
+                // the epilogue writes zeros for the former and does not store the latter
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = __shfl_sync(kFull, index[i / 8], (sub + 4 * i) & 31);
-                    from[i] = p.x_q + (r > 0 && r < p.x_rows ? r : 0) * row_bytes + 16 * chunk;
+                for (int j = 0; j < 2; ++j) {
+                    const int at = 64 * warp + 32 * j + lane;
+                    int64_t r = t.first + at;
+                    if (p.gather && at < t.live) r = __ldg(p.rows + r);
+                    if (r < 0 || r >= p.x_rows) r = 0;
+                    if (at < t.live && p.x_rows > 0) srow[j] = p.x_sf + r * kv;
+                    index[32 * j + lane] = (int)r;
                 }
+                __syncwarp();
             }
+            const int quads = !GRAD && p.gather ? max(0, min(16, (t.live - 64 * warp + 3) / 4)) : 0;
             // the weights' scales: the tiles of a 128-row block lie side by side along the contraction; warp 0
             // fetches those of the first half of B (and the gradient's A), warp 1 those of the second
             int left = (int)scale_tiles;
@@ -548,55 +494,44 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int s = 0; s < steps; ++s, ++it, left -= S::kScaleTiles) {
                 const int st = it % kStages;
                 if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
-                const uint32_t bar = smem_addr(&ctl->full[st]);
-                if (!GRAD) {
-                    if (p.gather) {
-                        const int64_t at = (int64_t)s * kRowBytes;
-                        const bool in = at + 16 * chunk < row_bytes;  // past the row's end: zeros
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int r = 64 * warp + sub + 4 * i;
-                            if (r >= t.live) continue;  // such a row is multiplied but never stored
-                            const uint32_t to = base + st * kBytesData + r * kRowBytes + ((chunk ^ (r & 7)) << 4);
-                            asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(to),
-                                         "l"(in ? from[i] + at : p.x_q), "r"(in ? 16 : 0)
-                                         : "memory");
-                        }
-                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-                    }
-                    uint8_t* dst = stages + kSfBase + st * kSfStage + 16 * lane + 8 * warp;
-                    if (S::kScaleTiles == 4) {
-                        *reinterpret_cast<uint2*>(dst) = make_uint2(p0[0].x, p0[1].x);
-                        *reinterpret_cast<uint2*>(dst + 512) = make_uint2(p0[0].y, p0[1].y);
-                        *reinterpret_cast<uint2*>(dst + 1024) = make_uint2(p0[0].z, p0[1].z);
-                        *reinterpret_cast<uint2*>(dst + 1536) = make_uint2(p0[0].w, p0[1].w);
-                    } else {
-                        const uint32_t a = (s & 2) ? ((s & 1) ? p0[0].w : p0[0].z) : ((s & 1) ? p0[0].y : p0[0].x);
-                        const uint32_t b = (s & 2) ? ((s & 1) ? p0[1].w : p0[1].z) : ((s & 1) ? p0[1].y : p0[1].x);
-                        *reinterpret_cast<uint2*>(dst) = make_uint2(a, b);
-                    }
-                    // a fence here would also wait for the rows in flight: with gathered rows the
-                    // thread that issues the products fences, after the barrier and before it reads
-                    if (!p.gather) fence_async();
-                    __syncwarp();
-                }
+                const uint32_t bar = smem_addr(&ctl->full[st]), sf = base + kSfBase + st * kSfStage;
                 if (elect_one()) {
-                    const uint32_t dst = base + kSfBase + st * kSfStage;
                     const uint32_t bytes = 512u * (uint32_t)min(S::kScaleTiles, left);
                     const int64_t at = (int64_t)s * kScaleBytes;
-                    mbar_arrive_tx(bar, (sfb ? bytes : 0u) + (sfa ? bytes : 0u));
-                    if (sfb) bulk_load(dst + kScaleBytes * (1 + warp), sfb + at, bytes, bar);
-                    if (sfa) bulk_load(dst, sfa + at, bytes, bar);
+                    mbar_arrive_tx(bar, (sfb ? bytes : 0u) + (sfa ? bytes : 0u) + quads * 4 * kRowBytes);
+                    if (sfb) bulk_load(sf + kScaleBytes * (1 + warp), sfb + at, bytes, bar);
+                    if (sfa) bulk_load(sf, sfa + at, bytes, bar);
+                    const uint32_t rows = base + st * kBytesData + 64 * warp * kRowBytes;
+#pragma unroll 4
+                    for (int i = 0; i < quads; ++i)
+                        tma_gather4(rows + i * 4 * kRowBytes, &map_low, bar, s * (int)kRowBytes,
+                                    *reinterpret_cast<const int4*>(index + 4 * i));
                 }
                 __syncwarp();
-                if (kPiece == 1 || (s & (kPiece - 1)) == kPiece - 1 || s + 1 == steps) {
+                if (GRAD) continue;
+                // row r's four scales of 512-byte tile q: word r / 32 of its 16-byte line r % 32
+                const int64_t at = (int64_t)s * S::kScaleTiles * 4;
+                const uint32_t dst = sf + 16 * lane + 8 * warp;
+#pragma unroll
+                for (int q = 0; q < S::kScaleTiles; ++q) {
+                    const int64_t take = kv - at - 4 * q;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        p0[j] = p1[j];
-                        p1[j] = p2[j];
+                        const uint32_t to = dst + 512 * q + 4 * j;
+                        if (words) {
+                            const bool in = srow[j] != nullptr && take > 0;  // otherwise zeros
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to),
+                                         "l"(in ? srow[j] + at + 4 * q : p.w_sf), "r"(in ? 4 : 0)
+                                         : "memory");
+                        } else {
+                            const uint32_t v = srow[j] != nullptr ? load_word(srow[j] + at + 4 * q, take, false) : 0u;
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+                        }
                     }
-                    next_piece(p2);
                 }
+                // these writes are the generic proxy's: the thread that issues the products fences after the barrier
+                if (words) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+                else mbar_arrive(bar);
             }
         }
     } else if (warp < 4 + kEpilogueWarps) {
@@ -813,7 +748,6 @@ cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsign
     q.w_sf_stride = p.w_sf_stride;
     // an x without rows: every slot reads a row of zeros, so any mapped memory does
     const void* x = p.x_rows > 0 ? p.x_q : p.w_q;
-    q.x_q = static_cast<const uint8_t*>(x);
     q.x_sf = p.x_sf;
     q.w_sf = p.w_sf;
     q.up_sf = p.up_sf;
@@ -838,7 +772,7 @@ cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsign
     const int64_t row_bytes = fp4 ? p.k / 2 : p.k;
     const int64_t x_rows = p.x_rows > 0 ? p.x_rows : 1;
     CUtensorMap ma, ml, mb, mu;
-    if (!make_map(&ma, x, row_bytes, x_rows, 0, 0, 128) || !make_map(&ml, x, row_bytes, x_rows, 0, 0, 32))
+    if (!make_map(&ma, x, row_bytes, x_rows, 0, 0, 128) || !make_map(&ml, x, row_bytes, x_rows, 0, 0, q.gather ? 1 : 32))
         return cudaErrorInvalidValue;
     if (!make_map(&mb, p.w_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
     mu = mb;
