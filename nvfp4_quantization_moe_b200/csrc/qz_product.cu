@@ -18,15 +18,14 @@
 // Twelve, because that leaves a thread 168 registers: with the shared memory in
 // use L1 is too small to hold spills, and an epilogue that spilled 500 bytes a
 // thread took three times as long.
-//   0, 1   scales: a lane copies two rows' scales of x (linear) by 4-byte
-//          cp.async into the 512-byte tile form; the weights' scales need one bulk
-//          copy, since a swizzled 512-byte tile is exactly what tcgen05.cp wants.
-//          With a row index the elected lane also gathers the rows of x, four at
-//          a time (TMA).  (Gathering by 16-byte cp.async was measured: 16 KB a
-//          stage took 1,600 clocks whatever the warps, three times the products.)
-//   2      TMA: the weights (tiled, 128-byte swizzle), and x when it has no index.
-//          A thread issues a copy in about 65 clocks, so a stage's copies are
-//          shared with the warps above.
+//   0, 1   x's scales: a lane owns two rows (linear) and writes them into the
+//          512-byte tile form, from registers loaded three pieces ahead.  With a
+//          row index the elected lane also gathers the rows of x, four at a time
+//          (TMA).  (Gathering by 16-byte cp.async was measured: 16 KB a stage
+//          took 1,600 clocks whatever the warps, three times the products.)
+//   2      TMA: the weights (tiled, 128-byte swizzle), their scales (a swizzled
+//          512-byte tile is exactly what tcgen05.cp wants: one bulk copy), and x
+//          when it has no index
 //   3      one thread copies scales to tensor memory and issues the products
 //   4..11  epilogue: warp w % 4 owns the lanes (rows) 32 (w % 4) .. + 31
 //
@@ -171,13 +170,143 @@ __device__ __forceinline__ bool grad_tile(const GradArgs& a, int u, Tile& t) {
 // x's scales: linear rows to 512-byte tiles
 // ---------------------------------------------------------------------------
 
-// `take` (1..4) bytes at p as a little-endian word, the others 0.
-__device__ __forceinline__ uint32_t load_word(const uint8_t* p, int64_t take, bool word_aligned) {
-    if (take >= 4 && word_aligned) return __ldg(reinterpret_cast<const uint32_t*>(p));
-    uint32_t v = 0;
-    for (int i = 0; i < 4; ++i)
-        if (i < take) v |= (uint32_t)__ldg(p + i) << (8 * i);
+// 16 bytes of a row's scales from byte `at` on, in loads of W bytes, without a
+// wait: where the row ends sooner, loads stay inside it and what they bring is
+// not used.  (Volatile, so that the compiler neither waits for a load to merge
+// it with another value nor moves it to its use.)
+template <int W>
+__device__ __forceinline__ uint4 load_piece(const uint8_t* row, int64_t at, int64_t kv) {
+    uint4 v;
+    if (W == 16) {
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(row + at));
+    } else if (W == 8) {
+        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(row + at));
+        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.z), "=r"(v.w) : "l"(row + min(at + 8, kv - 8)));
+    } else if (W == 4) {
+        asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v.x) : "l"(row + at));
+        asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v.y) : "l"(row + min(at + 4, kv - 4)));
+        asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v.z) : "l"(row + min(at + 8, kv - 4)));
+        asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v.w) : "l"(row + min(at + 12, kv - 4)));
+    } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (at + i < kv) w[i / 4] |= (uint32_t)__ldg(row + at + i) << (8 * (i % 4));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
     return v;
+}
+
+// One of the two warps: rows 64 warp + lane and + 32 of every tile's scales, and
+// the gather of rows 64 warp .. + 63.
+template <int FMT, bool GATED, int W>
+__device__ __forceinline__ void scale_warp(const ProductArgs& p, const int* s_prefix, Control* ctl, uint32_t base, int total,
+                                           const CUtensorMap& map_low, int warp, int lane) {
+    typedef Shape<FMT> S;
+    constexpr int kStages = S::kStages;
+    constexpr int kParts = FMT == QZ_FMT_MXFP8 ? 1 : 2;  // 16-byte parts of a piece
+    constexpr int kPiece = kParts * 4 / S::kScaleTiles;  // stages of a piece: 4 (MXFP8), 2 (NVFP4)
+    volatile int* const abort = &ctl->abort;
+    const int64_t kv = p.k / S::kBlock;
+    const int steps = (int)((p.k + S::kElems - 1) / S::kElems);
+    int* const index = ctl->index + 64 * warp;
+    // the pieces are loaded ahead of the stages, over a walk of the tiles of their own;
+    // a row that does not exist reads some row that does (the epilogue writes zeros, or does not store it)
+    int su = (int)blockIdx.x - (int)gridDim.x, ss = steps;
+    const uint8_t* srow[2] = {p.x_rows > 0 ? p.x_sf : p.w_sf, p.x_rows > 0 ? p.x_sf : p.w_sf};
+    auto rows_of = [&](int u, int (&r)[2]) {
+        const Tile t = product_tile(p, s_prefix, u);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int at = 64 * warp + 32 * j + lane;
+            int64_t i = t.first + at;
+            if (p.rows && at < t.live) i = __ldg(p.rows + i);
+            r[j] = i >= 0 && i < p.x_rows ? (int)i : 0;
+        }
+    };
+    auto next_piece = [&](uint4 (&v)[2][kParts]) {
+        ss += kPiece;
+        if (ss >= steps) {
+            ss = 0;
+            su += gridDim.x;
+            if (su < total) {
+                int r[2];
+                rows_of(su, r);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (p.x_rows > 0) srow[j] = p.x_sf + r[j] * kv;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const int64_t at = (int64_t)ss * S::kScaleTiles * 4 + 16 * i;
+                v[j][i] = load_piece<W>(srow[j], kParts == 1 ? at : min(at, (kv - 1) & ~(int64_t)15), kv);
+            }
+    };
+    uint4 p0[2][kParts], p1[2][kParts], p2[2][kParts];
+    next_piece(p0);
+    next_piece(p1);
+    next_piece(p2);
+    int it = 0;
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        const Tile t = product_tile(p, s_prefix, u);
+        const int quads = p.gather ? max(0, min(16, (t.live - 64 * warp + 3) / 4)) : 0;
+        if (p.gather) {
+            int r[2];
+            rows_of(u, r);
+            __syncwarp();
+            index[lane] = r[0];
+            index[32 + lane] = r[1];
+            __syncwarp();
+        }
+        for (int s = 0; s < steps; ++s, ++it) {
+            const int st = it % kStages;
+            if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) return;
+            const uint32_t bar = smem_addr(&ctl->full[st]);
+            // row r's four scales of a 512-byte tile: word r / 32 of its 16-byte line r % 32
+            const uint32_t dst = base + kStages * kBytesData + st * kScaleStage<FMT> + 16 * lane + 8 * warp;
+            if (FMT == QZ_FMT_NVFP4) {
+                const uint4 a = (s & 1) ? p0[0][kParts - 1] : p0[0][0], b = (s & 1) ? p0[1][kParts - 1] : p0[1][0];
+                st_shared_v2(dst, a.x, b.x);
+                st_shared_v2(dst + 512, a.y, b.y);
+                st_shared_v2(dst + 1024, a.z, b.z);
+                st_shared_v2(dst + 1536, a.w, b.w);
+            } else {
+                const uint4 a = p0[0][0], b = p0[1][0];
+                st_shared_v2(dst, (s & 2) ? ((s & 1) ? a.w : a.z) : ((s & 1) ? a.y : a.x),
+                             (s & 2) ? ((s & 1) ? b.w : b.z) : ((s & 1) ? b.y : b.x));
+            }
+            fence_async();
+            __syncwarp();
+            if (elect_one()) {
+                if (quads > 0) {
+                    mbar_arrive_tx(bar, quads * 4 * kRowBytes);
+                    const uint32_t to = base + st * kBytesData + 64 * warp * kRowBytes;
+#pragma unroll 4
+                    for (int i = 0; i < quads; ++i)
+                        tma_gather4(to + i * 4 * kRowBytes, &map_low, bar, s * (int)kRowBytes,
+                                    *reinterpret_cast<const int4*>(index + 4 * i));
+                } else {
+                    mbar_arrive(bar);
+                }
+            }
+            __syncwarp();
+            if ((s & (kPiece - 1)) == kPiece - 1 || s + 1 == steps) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < kParts; ++i) {
+                        p0[j][i] = p1[j][i];
+                        p1[j][i] = p2[j][i];
+                    }
+                next_piece(p2);
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -226,10 +355,11 @@ __device__ __forceinline__ void store_rows(uint8_t* to, int64_t pitch, const uin
     }
 }
 
-// v += the first `cols` of 32 bf16 columns at p.
-__device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[32]) {
+// v[i] += column i at p, for the first `cols` (a multiple of 8) of N bf16 columns.
+template <int N>
+__device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N / 8; ++i) {
         if (8 * i >= cols) continue;
         const uint4 r = *reinterpret_cast<const uint4*>(p + 8 * i);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -242,16 +372,17 @@ __device__ __forceinline__ void add_row(const uint16_t* p, int cols, float (&v)[
 }
 
 // SiLU and GELU are both z sigmoid(z (a + b z^2)), with (1, 0) and (2 sqrt(2/pi), 2 sqrt(2/pi) 0.044715).
-__device__ __forceinline__ void activate(int act, float (&v)[32]) {
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&v)[N]) {
     if (act == QZ_ACT_NONE) return;
     if (act == QZ_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaxf(v[i], 0.0f);
+        for (int i = 0; i < N; ++i) v[i] = fmaxf(v[i], 0.0f);
         return;
     }
     const float a = act == QZ_ACT_GELU ? kGelu2 : 1.0f, b = act == QZ_ACT_GELU ? kGelu2 * kGeluC : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= sigmoid32(v[i] * fmaf(b * v[i], v[i], a));
+    for (int i = 0; i < N; ++i) v[i] *= sigmoid32(v[i] * fmaf(b * v[i], v[i], a));
 }
 
 __device__ __forceinline__ float amax_scale(const float* amax, int64_t i) {
@@ -259,15 +390,15 @@ __device__ __forceinline__ float amax_scale(const float* amax, int64_t i) {
 }
 
 // Accumulator columns times g (NVFP4's second-level scales), zeros for a row that does not exist.
-template <int FMT>
-__device__ __forceinline__ void scale_row(float g, bool exists, float (&v)[32]) {
+template <int FMT, int N>
+__device__ __forceinline__ void scale_row(float g, bool exists, float (&v)[N]) {
     if (FMT == QZ_FMT_NVFP4) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= g;
+        for (int i = 0; i < N; ++i) v[i] *= g;
     }
     if (!exists) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        for (int i = 0; i < N; ++i) v[i] = 0.0f;
     }
 }
 
@@ -308,8 +439,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            // TMA; the scale warps' bulk copies; their lanes' copies of x's scales
-            mbar_init(smem_addr(&ctl->full[i]), 1 + kRowWarps + (GRAD ? 0 : 32 * kRowWarps));
+            mbar_init(smem_addr(&ctl->full[i]), GRAD ? 1 : 1 + kRowWarps);  // TMA; the warps of x's scales
             mbar_init(smem_addr(&ctl->empty[i]), 1);
         }
         mbar_init(smem_addr(&ctl->acc_full[0]), 1);
@@ -376,12 +506,32 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const int boxes = GRAD || p.gather ? 0 : tall ? 1 : (t.live + 31) / 32;
                 const uint32_t bytes = (uint32_t)halves * kBytesA +
                                        (GRAD || boxes && tall ? kBytesA : (uint32_t)boxes * 32 * kRowBytes);
+                // the tiles of a 128-row block of scales lie side by side along the contraction
+                int left = (int)scale_tiles;
+                const uint8_t *sf0, *sf1, *sfa = nullptr;
+                if (GRAD) {
+                    const int64_t tile0 = t.first / (4 * S::kBlock);
+                    left -= (int)tile0;
+                    sf0 = g.x_sf + ((int64_t)(2 * t.n) * scale_tiles + tile0) * 512;
+                    sf1 = sf0 + scale_tiles * 512;
+                    sfa = g.dz_sf + ((int64_t)t.m * scale_tiles + tile0) * 512;
+                } else {
+                    const int64_t block = GATED ? t.n : 2 * t.n, at = t.e * p.w_sf_stride + block * scale_tiles * 512;
+                    sf0 = p.w_sf + at;
+                    sf1 = GATED ? p.up_sf + at : sf0 + scale_tiles * 512;
+                }
                 int x = GRAD ? (int)(t.first * kRowBytes / S::kElems) : 0;
-                for (int s = 0; s < steps; ++s, ++it, x += kRowBytes) {
+                for (int s = 0; s < steps; ++s, ++it, x += kRowBytes, left -= S::kScaleTiles) {
                     const int st = it % kStages;
                     if (!mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort)) goto done;
                     const uint32_t bar = smem_addr(&ctl->full[st]), dst = base + st * kBytesData;
-                    mbar_arrive_tx(bar, bytes);
+                    const uint32_t sf = base + kSfBase + st * kSfStage;
+                    const uint32_t sf_bytes = 512u * (uint32_t)min(S::kScaleTiles, left);
+                    const int64_t at = (int64_t)s * kScaleBytes;
+                    mbar_arrive_tx(bar, bytes + (halves + (GRAD ? 1 : 0)) * sf_bytes);
+                    bulk_load(sf + kScaleBytes, sf0 + at, sf_bytes, bar);
+                    if (halves == 2) bulk_load(sf + 2 * kScaleBytes, sf1 + at, sf_bytes, bar);
+                    if (GRAD) bulk_load(sf, sfa + at, sf_bytes, bar);
                     if (GRAD) {
                         tma_load_2d(dst + kBytesA, &map_b, bar, x, row0);
                         if (halves == 2) tma_load_2d(dst + 2 * kBytesA, &map_b, bar, x, row1);
@@ -419,7 +569,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     if (!mbar_wait(smem_addr(&ctl->empty[b % kStages]), (b / kStages) & 1, abort)) goto done;
                 }
                 if (!mbar_wait(smem_addr(&ctl->full[st]), (it / kStages) & 1, abort)) goto done;
-                if (!GRAD) fence_async();  // the scale warps' writes (see there)
                 tc_fence_after();
                 const int products = s + 1 < steps ? S::kElems / S::kMma : last;
                 {
@@ -452,87 +601,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
         }
     } else if (warp < kRowWarps) {
-        // ------------------------------------------------------------ scales, gathered rows
-        const bool words = (kv & 3) == 0;  // a row's scales start on a word
-        int* const index = ctl->index + 64 * warp;  // rows 64 warp .. + 63 of the tile
-        int it = 0;
-        for (int u = blockIdx.x; u < total; u += gridDim.x) {
-            Tile t;
-            if (!tile_of(u, t)) continue;
-            const int halves = halves_of(t), steps = stages_of(t);
-            const uint8_t* srow[2] = {nullptr, nullptr};
-            if (!GRAD) {
-                // an index that is no row of x reads row 0 and a row past the expert's end nothing at all:
-                // the epilogue writes zeros for the former and does not store the latter
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int at = 64 * warp + 32 * j + lane;
-                    int64_t r = t.first + at;
-                    if (p.gather && at < t.live) r = __ldg(p.rows + r);
-                    if (r < 0 || r >= p.x_rows) r = 0;
-                    if (at < t.live && p.x_rows > 0) srow[j] = p.x_sf + r * kv;
-                    index[32 * j + lane] = (int)r;
-                }
-                __syncwarp();
-            }
-            const int quads = !GRAD && p.gather ? max(0, min(16, (t.live - 64 * warp + 3) / 4)) : 0;
-            // the weights' scales: the tiles of a 128-row block lie side by side along the contraction; warp 0
-            // fetches those of the first half of B (and the gradient's A), warp 1 those of the second
-            int left = (int)scale_tiles;
-            const uint8_t *sfb = nullptr, *sfa = nullptr;
-            if (GRAD) {
-                const int64_t tile0 = t.first / (4 * S::kBlock);
-                left -= (int)tile0;
-                if (warp == 0 || halves == 2) sfb = g.x_sf + ((int64_t)(2 * t.n + warp) * scale_tiles + tile0) * 512;
-                if (warp == 0) sfa = g.dz_sf + ((int64_t)t.m * scale_tiles + tile0) * 512;
-            } else {
-                const int64_t block = GATED ? t.n : 2 * t.n + warp;
-                if (warp == 0 || halves == 2)
-                    sfb = (GATED && warp ? p.up_sf : p.w_sf) + t.e * p.w_sf_stride + block * scale_tiles * 512;
-            }
-            for (int s = 0; s < steps; ++s, ++it, left -= S::kScaleTiles) {
-                const int st = it % kStages;
-                if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) goto done;
-                const uint32_t bar = smem_addr(&ctl->full[st]), sf = base + kSfBase + st * kSfStage;
-                if (elect_one()) {
-                    const uint32_t bytes = 512u * (uint32_t)min(S::kScaleTiles, left);
-                    const int64_t at = (int64_t)s * kScaleBytes;
-                    mbar_arrive_tx(bar, (sfb ? bytes : 0u) + (sfa ? bytes : 0u) + quads * 4 * kRowBytes);
-                    if (sfb) bulk_load(sf + kScaleBytes * (1 + warp), sfb + at, bytes, bar);
-                    if (sfa) bulk_load(sf, sfa + at, bytes, bar);
-                    const uint32_t rows = base + st * kBytesData + 64 * warp * kRowBytes;
-#pragma unroll 4
-                    for (int i = 0; i < quads; ++i)
-                        tma_gather4(rows + i * 4 * kRowBytes, &map_low, bar, s * (int)kRowBytes,
-                                    *reinterpret_cast<const int4*>(index + 4 * i));
-                }
-                __syncwarp();
-                if (GRAD) continue;
-                // row r's four scales of 512-byte tile q: word r / 32 of its 16-byte line r % 32
-                const int64_t at = (int64_t)s * S::kScaleTiles * 4;
-                const uint32_t dst = sf + 16 * lane + 8 * warp;
-#pragma unroll
-                for (int q = 0; q < S::kScaleTiles; ++q) {
-                    const int64_t take = kv - at - 4 * q;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t to = dst + 512 * q + 4 * j;
-                        if (words) {
-                            const bool in = srow[j] != nullptr && take > 0;  // otherwise zeros
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to),
-                                         "l"(in ? srow[j] + at + 4 * q : p.w_sf), "r"(in ? 4 : 0)
-                                         : "memory");
-                        } else {
-                            const uint32_t v = srow[j] != nullptr ? load_word(srow[j] + at + 4 * q, take, false) : 0u;
-                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
-                        }
-                    }
-                }
-                // these writes are the generic proxy's: the thread that issues the products fences after the barrier
-                if (words) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-                else mbar_arrive(bar);
-            }
+        // ------------------------------------------------------------ scales of x, gathered rows
+        if (!GRAD) {
+            // the widest load that a row's start and length allow; x's scales need only word alignment
+            const int align = aligned(p.x_sf, 16) ? 16 : aligned(p.x_sf, 8) ? 8 : 4;
+            const int width = (int)min((int64_t)align, kv & -kv);
+            if (width == 16) scale_warp<FMT, GATED, 16>(p, s_prefix, ctl, base, total, map_low, warp, lane);
+            else if (width == 8) scale_warp<FMT, GATED, 8>(p, s_prefix, ctl, base, total, map_low, warp, lane);
+            else if (width == 4) scale_warp<FMT, GATED, 4>(p, s_prefix, ctl, base, total, map_low, warp, lane);
+            else scale_warp<FMT, GATED, 1>(p, s_prefix, ctl, base, total, map_low, warp, lane);
         }
     } else if (warp < 4 + kEpilogueWarps) {
         // ------------------------------------------------------------ epilogue
@@ -592,24 +669,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const int h = GATED ? 0 : i < 2 ? half : 1 - half;
                 const int64_t at = (GATED ? (int64_t)t.n * 128 : (int64_t)t.n * 256 + 128 * h) + c0 + 32 * (i & 1);
                 const int cols = (int)min((int64_t)32, width - at);
-                float y[32];  // gated: the up projection
-                if (GATED) {
-                    tc_load32(acc + 128 * (1 - own) + c0 + 32 * i, y);
-                    if (own) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float z = x[j];
-                            x[j] = y[j];
-                            y[j] = z;
-                        }
-                    }
-                    scale_row<FMT>(scale1, exists, y);
-                }
-                scale_row<FMT>(scale0, exists && any, x);
                 uint32_t w[16];
                 if (cols <= 0 || rows <= 0) {
                     // nothing of this unit is in the matrix
                 } else if (GRAD) {
+                    scale_row<FMT>(scale0, any, x);
                     const int64_t to = (t.e * g.n + (int64_t)t.m * kTileM + 32 * quarter) * g.k + at;
                     if (g.f32) {
                         uint8_t* o = reinterpret_cast<uint8_t*>(static_cast<float*>(g.out) + to);
@@ -627,25 +691,59 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         store_rows<false>(reinterpret_cast<uint8_t*>(o), 2 * g.k, w, rows, 2 * cols, stage, lane);
                     }
                 } else {
-                    if (p.bias) add_row(p.bias + t.e * p.n + at, cols, x);
-                    if (GATED && p.up_bias) add_row(p.up_bias + t.e * p.n + at, cols, y);
                     const int64_t slot0 = t.first + 32 * quarter;  // of lane 0
-                    if (p.pre) {
-                        uint8_t* o = reinterpret_cast<uint8_t*>(p.pre + slot0 * p.ld_pre + at);
-                        to_words(x, w);
-                        store_rows<false>(o, 2 * p.ld_pre, w, rows, 2 * cols, stage, lane);
-                        if (GATED) {
-                            to_words(y, w);
-                            store_rows<false>(o + 2 * p.n, 2 * p.ld_pre, w, rows, 2 * cols, stage, lane);
-                        }
-                    }
-                    activate(p.act, x);
                     if (GATED) {
+                        const uint32_t other = acc + 128 * (1 - own) + c0 + 32 * i;  // the half that is not held
+                        if (p.pre) {
+                            // the held half, then the other: z goes to columns at, u to n + at
+                            float z[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] *= y[j];
+                            for (int j = 0; j < 32; ++j) z[j] = x[j];
+#pragma unroll 1
+                            for (int k = 0; k < 2; ++k) {
+                                const bool is_u = (own != 0) != (k == 1);
+                                if (k == 1) tc_load32(other, z);
+                                scale_row<FMT>(is_u ? scale1 : scale0, exists, z);
+                                const uint16_t* bias = is_u ? p.up_bias : p.bias;
+                                if (bias) add_row(bias + t.e * p.n + at, cols, z);
+                                to_words(z, w);
+                                store_rows<false>(reinterpret_cast<uint8_t*>(p.pre + slot0 * p.ld_pre + at + (is_u ? p.n : 0)),
+                                                  2 * p.ld_pre, w, rows, 2 * cols, stage, lane);
+                            }
+                        }
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            float z[16], u[16];
+                            tc_load16(other + 16 * b, u);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float held = x[16 * b + j], o = u[j];
+                                z[j] = own ? o : held;
+                                u[j] = own ? held : o;
+                            }
+                            scale_row<FMT>(scale0, exists, z);
+                            scale_row<FMT>(scale1, exists, u);
+                            if (p.bias) add_row(p.bias + t.e * p.n + at + 16 * b, cols - 16 * b, z);
+                            if (p.up_bias) add_row(p.up_bias + t.e * p.n + at + 16 * b, cols - 16 * b, u);
+                            activate(p.act, z);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) z[j] *= u[j];
+                            if (p.residual && row_in) add_row(p.residual + slot * p.ld_residual + at + 16 * b, cols - 16 * b, z);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) w[8 * b + j] = bf16x2_of(z[2 * j], z[2 * j + 1]);
+                        }
+                    } else {
+                        scale_row<FMT>(scale0, exists, x);
+                        if (p.bias) add_row(p.bias + t.e * p.n + at, cols, x);
+                        if (p.pre) {
+                            to_words(x, w);
+                            store_rows<false>(reinterpret_cast<uint8_t*>(p.pre + slot0 * p.ld_pre + at), 2 * p.ld_pre, w, rows,
+                                              2 * cols, stage, lane);
+                        }
+                        activate(p.act, x);
+                        if (p.residual && row_in) add_row(p.residual + slot * p.ld_residual + at, cols, x);
+                        to_words(x, w);
                     }
-                    if (p.residual && row_in) add_row(p.residual + slot * p.ld_residual + at, cols, x);
-                    to_words(x, w);
                     store_rows<false>(reinterpret_cast<uint8_t*>(p.out + slot0 * p.ld_out + at), 2 * p.ld_out, w, rows,
                                       2 * cols, stage, lane);
                     if (p.q && row_in) {  // n is a multiple of 32: a whole block in this lane

@@ -68,6 +68,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+__device__ __forceinline__ void st_shared_v2(uint32_t to, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(a), "r"(b) : "memory");
+}
+
 // Generic-proxy writes to shared memory before this fence are seen by
 // asynchronous (TMA, tcgen05) reads ordered after it.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -192,9 +196,21 @@ __device__ __forceinline__ uint32_t mma_idesc(int n, int word_byte) {
     return common | (1u << 7) | (1u << 10);
 }
 
-// 32 consecutive columns of this thread's lane, loaded and waited for in one
+// 16 or 32 consecutive columns of this thread's lane, loaded and waited for in one
 // statement: the registers are written asynchronously until the wait, and a
 // copy or a spill that the compiler put between the two would read old values.
+__device__ __forceinline__ void tc_load16(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+        "}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tc_load32(uint32_t taddr, float (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
