@@ -136,19 +136,28 @@ __device__ __forceinline__ Range expert_range(const int32_t* offsets, const int3
     return r;
 }
 
-// Product: s_prefix holds the experts' row tiles; an expert's tiles are ordered
-// by column block, row tiles innermost, so that CTAs working side by side read
-// the same weights.
-__device__ __forceinline__ Tile product_tile(const ProductArgs& a, const int* s_prefix, int u) {
+// The product's list of experts in shared memory: row tiles before each, its
+// first slot, and the rows of its last tile less one (a tile must be found
+// without a trip to global memory by every role, at every tile).
+struct ExpertList {
+    int* prefix;    // [n_experts + 1]
+    int* first;     // [n_experts]
+    uint8_t* last;  // [n_experts]
+};
+
+constexpr size_t list_bytes(int n) { return (size_t)(2 * n + 1) * sizeof(int) + (size_t)n; }
+
+// An expert's tiles are ordered by column block, row tiles innermost, so that
+// CTAs working side by side read the same weights.
+__device__ __forceinline__ Tile product_tile(const ProductArgs& a, const ExpertList& list, int u) {
     Tile t;
-    t.e = find_owner(s_prefix, a.n_experts, u / a.n_blocks);
-    const int tiles = s_prefix[t.e + 1] - s_prefix[t.e];
-    const int v = u - s_prefix[t.e] * a.n_blocks;
+    t.e = find_owner(list.prefix, a.n_experts, u / a.n_blocks);
+    const int tiles = list.prefix[t.e + 1] - list.prefix[t.e];
+    const int v = u - list.prefix[t.e] * a.n_blocks;
     t.n = v / tiles;
     t.m = v - t.n * tiles;
-    const Range r = expert_range(a.offsets, a.counts, t.e, a.slots);
-    t.first = r.off + (int64_t)t.m * kTileM;
-    t.live = (int)min((int64_t)kTileM, r.cnt - (int64_t)t.m * kTileM);
+    t.first = (int64_t)list.first[t.e] + (int64_t)t.m * kTileM;
+    t.live = t.m + 1 < tiles ? kTileM : list.last[t.e] + 1;
     t.depth = a.k;
     return t;
 }
@@ -202,7 +211,7 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t* row, int64_t at, int6
 // One of the two warps: rows 64 warp + lane and + 32 of every tile's scales, and
 // the gather of rows 64 warp .. + 63.
 template <int FMT, bool GATED, int W>
-__device__ __forceinline__ void scale_warp(const ProductArgs& p, const int* s_prefix, Control* ctl, uint32_t base, int total,
+__device__ __forceinline__ void scale_warp(const ProductArgs& p, const ExpertList& list, Control* ctl, uint32_t base, int total,
                                            const CUtensorMap& map_low, int warp, int lane) {
     typedef Shape<FMT> S;
     constexpr int kStages = S::kStages;
@@ -217,7 +226,7 @@ __device__ __forceinline__ void scale_warp(const ProductArgs& p, const int* s_pr
     int su = (int)blockIdx.x - (int)gridDim.x, ss = steps;
     const uint8_t* srow[2] = {p.x_rows > 0 ? p.x_sf : p.w_sf, p.x_rows > 0 ? p.x_sf : p.w_sf};
     auto rows_of = [&](int u, int (&r)[2]) {
-        const Tile t = product_tile(p, s_prefix, u);
+        const Tile t = product_tile(p, list, u);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int at = 64 * warp + 32 * j + lane;
@@ -253,7 +262,7 @@ __device__ __forceinline__ void scale_warp(const ProductArgs& p, const int* s_pr
     next_piece(p2);
     int it = 0;
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
-        const Tile t = product_tile(p, s_prefix, u);
+        const Tile t = product_tile(p, list, u);
         const int quads = p.gather ? max(0, min(16, (t.live - 64 * warp + 3) / 4)) : 0;
         if (p.gather) {
             int r[2];
@@ -431,7 +440,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint8_t* const stages = smem + (base - smem_addr(smem));
     uint8_t* const staging = stages + kStagesBytes<FMT>;  // of the epilogue warps
     Control* const ctl = reinterpret_cast<Control*>(staging + kEpilogueWarps * kStagingBytes);
-    int* const s_prefix = reinterpret_cast<int*>(ctl + 1);
+    ExpertList list;
+    list.prefix = reinterpret_cast<int*>(ctl + 1);
+    list.first = list.prefix + (GRAD ? 0 : args.p.n_experts + 1);
+    list.last = reinterpret_cast<uint8_t*>(list.first + (GRAD ? 0 : args.p.n_experts));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ProductArgs& p = args.p;
@@ -464,10 +476,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         __syncthreads();
     } else {
         unsigned bad = 0;
-        total = p.n_blocks * block_prefix(p.n_experts, s_prefix, ctl->scratch,
+        total = p.n_blocks * block_prefix(p.n_experts, list.prefix, ctl->scratch,
                                           [&](int e) -> long long {
                                               const Range r = expert_range(p.offsets, p.counts, e, p.slots);
                                               bad |= r.bad;
+                                              list.first[e] = (int)r.off;
+                                              list.last[e] = (uint8_t)((r.cnt + kTileM - 1) % kTileM);
                                               return r.bad ? 0 : (r.cnt + kTileM - 1) / kTileM;
                                           },
                                           p.d_err);  // ends with a barrier
@@ -482,7 +496,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // what each role needs to know of tile u; false: nothing is to be done
     auto tile_of = [&](int u, Tile& t) -> bool {
         if (GRAD) return grad_tile(g, u, t);
-        t = product_tile(p, s_prefix, u);
+        t = product_tile(p, list, u);
         return true;
     };
     // 128-column halves of B that tile t multiplies with
@@ -606,10 +620,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             // the widest load that a row's start and length allow; x's scales need only word alignment
             const int align = aligned(p.x_sf, 16) ? 16 : aligned(p.x_sf, 8) ? 8 : 4;
             const int width = (int)min((int64_t)align, kv & -kv);
-            if (width == 16) scale_warp<FMT, GATED, 16>(p, s_prefix, ctl, base, total, map_low, warp, lane);
-            else if (width == 8) scale_warp<FMT, GATED, 8>(p, s_prefix, ctl, base, total, map_low, warp, lane);
-            else if (width == 4) scale_warp<FMT, GATED, 4>(p, s_prefix, ctl, base, total, map_low, warp, lane);
-            else scale_warp<FMT, GATED, 1>(p, s_prefix, ctl, base, total, map_low, warp, lane);
+            if (width == 16) scale_warp<FMT, GATED, 16>(p, list, ctl, base, total, map_low, warp, lane);
+            else if (width == 8) scale_warp<FMT, GATED, 8>(p, list, ctl, base, total, map_low, warp, lane);
+            else if (width == 4) scale_warp<FMT, GATED, 4>(p, list, ctl, base, total, map_low, warp, lane);
+            else scale_warp<FMT, GATED, 1>(p, list, ctl, base, total, map_low, warp, lane);
         }
     } else if (warp < 4 + kEpilogueWarps) {
         // ------------------------------------------------------------ epilogue
@@ -654,8 +668,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const int units = GATED ? 2 : 2 * halves;
             float x[32], next[32];
             if (any) {
-                tc_load32(acc + 128 * half + c0, x);
-                tc_load32(acc + 128 * half + c0 + 32, next);
+                tc_load64(acc + 128 * half + c0, x, next);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ctl->acc_free));
@@ -822,11 +835,11 @@ static cudaError_t launch_experts(const Args& a, const CUtensorMap& ma, const CU
                                   const CUtensorMap& mu, int n_experts, int grid, cudaStream_t s) {
     constexpr size_t fixed = 1024 + kStagesBytes<FMT> + kEpilogueWarps * kStagingBytes + sizeof(Control);
     // asked for at its largest: the attribute is one value per device
-    constexpr size_t most = fixed + (QZ_MAX_ROUTE_EXPERTS + 1) * sizeof(int);
+    constexpr size_t most = fixed + list_bytes(QZ_MAX_ROUTE_EXPERTS);
     static_assert(most <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(experts_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
-    experts_kernel<FMT, KIND><<<grid, kProductThreads, fixed + (n_experts + 1) * sizeof(int), s>>>(a, ma, ml, mb, mu);
+    experts_kernel<FMT, KIND><<<grid, kProductThreads, fixed + list_bytes(n_experts), s>>>(a, ma, ml, mb, mu);
     return cudaGetLastError();
 }
 
