@@ -669,14 +669,21 @@ typedef struct qz_product {
  *   h = act(z),  gated: h = act(z) * u,  u = A U_e^T + up_bias_e   -> pre[s] (second half)
  *   out[s] = bf16(h + residual[s]),  q, sf[s] = the MXFP8 form of out[s]
  * Only live slots are written.  A d_rows entry outside [0, x_rows) stands for a
- * row of zeros.  One launch, no allocation, no dependence of the results on the
- * grid.  The same call is the data gradient: dA = dZ W is the product of the
+ * row of zeros.  No allocation, no dependence of the results on the grid.  With
+ * d_rows and opts->d_workspace (16-byte aligned, qz_product_bytes(p) bytes, not
+ * shared with a call that may overlap) a large call first copies its rows into
+ * slot order there, which is faster than gathering them in the product; the
+ * results are the same.  The same call is the data gradient: dA = dZ W is the product of the
  * row-wise quantized dZ with W quantized column-wise ([k, n] payloads from
  * qz_quantize_grouped_colwise).
  * Errors: QZ_ERR_INVALID_ARG for sizes, enums, null pointers or strides outside
  * the above, slots or x_rows above 2^31 - 1, up_bias or up_amax without up_q;
  * QZ_ERR_ALIGNMENT; QZ_ERR_CUDA when a tensor map or the launch is refused. */
 qz_status qz_expert_product(const qz_product *p, void *stream, const qz_launch_opts *opts);
+
+/* Device scratch with which qz_expert_product is faster, in bytes; 0 where it
+ * would use none (few slots, no d_rows) and for sizes it refuses. */
+size_t qz_product_bytes(const qz_product *p);
 
 /* The experts' weight gradients (HOST struct, read during the call).  Operands
  * are column-wise quantized over ALL slots at once (one entry of

@@ -62,6 +62,7 @@ EXPORTED = (
     "qz_plan_bytes",
     "qz_plan_experts",
     "qz_expert_product",
+    "qz_product_bytes",
     "qz_expert_weight_grad",
     "qz_expert_activation_grad",
     "qz_dispatch_experts",
@@ -206,6 +207,8 @@ def load(path: str = LIB_PATH):
         lib.qz_plan_experts.argtypes = [P, i64, I, I, I, P, P, P, P, P, ctypes.c_size_t, P]
         lib.qz_expert_product.restype = I
         lib.qz_expert_product.argtypes = [P, P, P]
+        lib.qz_product_bytes.restype = ctypes.c_size_t
+        lib.qz_product_bytes.argtypes = [P]
         lib.qz_expert_weight_grad.restype = I
         lib.qz_expert_weight_grad.argtypes = [P, P, P]
         lib.qz_expert_activation_grad.restype = I
@@ -760,7 +763,7 @@ def _expert_lists(offsets, counts, n_experts: int, dev: int):
 
 def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, out: torch.Tensor, *, rows=None,
                    up=None, bias=None, up_bias=None, activation: int = ACT_NONE, residual=None, pre=None, q=None,
-                   sf=None, stream=None, err=None, max_ctas: int = 0):
+                   sf=None, workspace=None, stream=None, err=None, max_ctas: int = 0):
     """The experts' matrix products with bias, activation, gate and residual in
     the epilogue (qz_expert_product).
 
@@ -772,7 +775,8 @@ def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, 
     out: bf16 [slots, N]; rows: int32 [slots] row of x of each slot (None: the
     slot's own number); bias, up_bias: bf16 [E, N]; residual: bf16 [slots, N];
     pre: bf16 [slots, N or 2N] receives the pre-activations; q [slots, N] and
-    sf [slots, N/32] receive the MXFP8 form of out."""
+    sf [slots, N/32] receive the MXFP8 form of out.  A large call with rows
+    uses a workspace (allocated unless given) to put them in order first."""
     xq, xsf, xa = _parts(x, "x")
     wq, wsf, wa = _parts(w, "w")
     _require(xq.dim() == 2 and wq.dim() == 3 and out.dim() == 2, "x must be [R, K], w [E, N, K], out [slots, N]")
@@ -825,7 +829,16 @@ def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, 
                  upp[1], upp[2], wp[3], wp[4], _tensor(bias, "bias", torch.bfloat16, dev, (E, N), optional=True),
                  _tensor(up_bias, "up_bias", torch.bfloat16, dev, (E, N), optional=True), r, ldr, o, ldo, z, ldz,
                  0 if q is None else _codes(q, "q", N, FMT_MXFP8, dev), 0 if sf is None else sf.data_ptr())
-    _check(load().qz_expert_product(ctypes.byref(p), _raw_stream(stream, dev), _opts(err, max_ctas)), "qz_expert_product")
+    lib, ref, s = load(), ctypes.byref(p), _raw_stream(stream, dev)
+    if workspace is not None:
+        _tensor(workspace, "workspace", torch.uint8, dev)
+    elif rows is not None:
+        need = lib.qz_product_bytes(ref)
+        if need:
+            workspace = out.new_empty(need, dtype=torch.uint8)
+            if stream is not None and hasattr(stream, "cuda_stream"):
+                workspace.record_stream(stream)
+    _check(lib.qz_expert_product(ref, s, _opts(err, max_ctas, workspace)), "qz_expert_product")
     return out
 
 

@@ -50,7 +50,8 @@ cudaError_t launch_route_grad(const void* logits, int type, int64_t T, int E, in
 size_t plan_bytes(int64_t n, int E);
 cudaError_t launch_plan(const int32_t* ids, int64_t T, int k, int E, int align, int64_t slots, int32_t* offsets,
                         int32_t* counts, int32_t* rows, int32_t* pair_slots, void* ws, cudaStream_t s);
-cudaError_t launch_product(const qz_product& p, int ctas, cudaStream_t s, unsigned* d_err);
+size_t product_bytes(const qz_product& p);
+cudaError_t launch_product(const qz_product& call, int ctas, cudaStream_t s, unsigned* d_err, void* ws);
 cudaError_t launch_weight_grad(const qz_weight_grad& p, int ctas, cudaStream_t s, unsigned* d_err);
 cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p, int64_t slots,
                             int64_t n, int act, bool gated, const int32_t* offsets, const int32_t* counts,
@@ -514,7 +515,17 @@ qz_status qz_expert_product(const qz_product* p, void* stream, const qz_launch_o
     if (!aligned(p->x_sf, 4) || !aligned(p->x_amax, 4) || !aligned(p->w_amax, 4) || !aligned(p->up_amax, 4) ||
         !aligned(p->d_rows, 4) || !aligned(p->d_offsets, 4) || !aligned(p->d_counts, 4))
         return QZ_ERR_ALIGNMENT;
-    return from_cuda(qz::launch_product(*p, one_per_sm(opts), (cudaStream_t)stream, err_word(opts)));
+    void* const ws = opts ? opts->d_workspace : nullptr;
+    if (ws && opts->workspace_bytes < qz::product_bytes(*p)) return QZ_ERR_INVALID_ARG;
+    if (!aligned(ws, 16)) return QZ_ERR_ALIGNMENT;
+    return from_cuda(qz::launch_product(*p, one_per_sm(opts), (cudaStream_t)stream, err_word(opts), ws));
+}
+
+size_t qz_product_bytes(const qz_product* p) {
+    if (!p || (p->fmt != QZ_FMT_MXFP8 && p->fmt != QZ_FMT_NVFP4) || p->k < 32 || p->k % 32 != 0 || p->k > QZ_MAX_LD ||
+        p->slots < 0 || p->slots > kMaxIndex)
+        return 0;
+    return qz::product_bytes(*p);
 }
 
 qz_status qz_expert_weight_grad(const qz_weight_grad* p, void* stream, const qz_launch_opts* opts) {
