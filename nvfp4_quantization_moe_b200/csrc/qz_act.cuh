@@ -38,18 +38,20 @@ struct ActPair {
     float value, grad;
 };
 
-// act(z) and act'(z), with the accurate exponential: both feed sums.
+// act(z) and act'(z).  With e = exp(-|v|) neither sigmoid(v) nor 1 - sigmoid(v)
+// cancels; SiLU and GELU are both z sigmoid(v), v = z (a + b z^2), v' = a + 3 b z^2.
 __device__ __forceinline__ ActPair act_with_grad(int act, float z) {
     ActPair p;
     if (act == QZ_ACT_SILU || act == QZ_ACT_GELU) {
+        const float a = act == QZ_ACT_GELU ? kGelu2 : 1.0f, b = act == QZ_ACT_GELU ? kGelu2 * kGeluC : 0.0f;
         const float z2 = z * z;
-        const float v = act == QZ_ACT_SILU ? z : kGelu2 * fmaf(kGeluC * z2, z, z);
-        const float e = expf(-fabsf(v));
-        const float q = 1.0f / (1.0f + e);
-        const float s = v >= 0.0f ? q : e * q, rest = v >= 0.0f ? e * q : q;  // sigmoid(v) and 1 - sigmoid(v)
-        const float dv = act == QZ_ACT_SILU ? 1.0f : kGelu2 * fmaf(3.0f * kGeluC, z2, 1.0f);
+        const float v = z * fmaf(b, z2, a);
+        const float e = __expf(-fabsf(v));
+        const float q = __fdividef(1.0f, 1.0f + e);
+        const float eq = e * q;
+        const float s = v >= 0.0f ? q : eq;
         p.value = z * s;
-        p.grad = fmaf(z * s * rest, dv, s);
+        p.grad = fmaf(z * (q * eq), fmaf(3.0f * b, z2, a), s);  // sigmoid(v) (1 - sigmoid(v)) = q e q
     } else if (act == QZ_ACT_RELU) {
         p.value = fmaxf(z, 0.0f);
         p.grad = z > 0.0f ? 1.0f : 0.0f;

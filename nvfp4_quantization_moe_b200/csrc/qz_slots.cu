@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kDispatchThreads)
 constexpr int kGradWarps = 8;
 constexpr int kGradCols = 256;
 constexpr int kGradSplit = 8;  // cluster size
+constexpr int kRowsAhead = 4;
 
 template <bool GATED>
 __global__ void __launch_bounds__(kGradWarps * 32) __cluster_dims__(1, kGradSplit, 1)
@@ -193,31 +194,46 @@ __global__ void __launch_bounds__(kGradWarps * 32) __cluster_dims__(1, kGradSpli
     }
     float sz[8] = {0, 0, 0, 0, 0, 0, 0, 0}, su[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (c < n) {
-        for (int64_t i = r * kGradWarps + warp; i < count; i += kGradSplit * kGradWarps) {
-            const int64_t s = begin + i;
-            float d[8], z[8], dz[8];
-            unpack8(ld_stream(dout + s * ld_d + c), d);
-            unpack8(ld_stream(pre + s * ld_p + c), z);
-            if (GATED) {
-                float u[8], du[8];
-                unpack8(ld_stream(pre + s * ld_p + n + c), u);
+        // kRowsAhead rows' loads are in flight before the first is used
+        constexpr int64_t kStep = kGradSplit * kGradWarps;
+        for (int64_t i0 = r * kGradWarps + warp; i0 < count; i0 += kRowsAhead * kStep) {
+            uint4 vd[kRowsAhead], vz[kRowsAhead], vu[kRowsAhead];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const ActPair p = act_with_grad(act, z[j]);
-                    du[j] = d[j] * p.value;
-                    dz[j] = d[j] * u[j] * p.grad;
-                    su[j] += du[j];
-                    sz[j] += dz[j];
-                }
-                st_v4(dpre + s * ld_q + n + c, pack8(du));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    dz[j] = d[j] * act_with_grad(act, z[j]).grad;
-                    sz[j] += dz[j];
-                }
+            for (int k = 0; k < kRowsAhead; ++k) {
+                const int64_t s = begin + i0 + k * kStep;
+                if (i0 + k * kStep >= count) continue;
+                vd[k] = ld_stream(dout + s * ld_d + c);
+                vz[k] = ld_stream(pre + s * ld_p + c);
+                if (GATED) vu[k] = ld_stream(pre + s * ld_p + n + c);
             }
-            st_v4(dpre + s * ld_q + c, pack8(dz));
+#pragma unroll
+            for (int k = 0; k < kRowsAhead; ++k) {
+                const int64_t s = begin + i0 + k * kStep;
+                if (i0 + k * kStep >= count) continue;
+                float d[8], z[8], dz[8];
+                unpack8(vd[k], d);
+                unpack8(vz[k], z);
+                if (GATED) {
+                    float u[8], du[8];
+                    unpack8(vu[k], u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const ActPair p = act_with_grad(act, z[j]);
+                        du[j] = d[j] * p.value;
+                        dz[j] = d[j] * u[j] * p.grad;
+                        su[j] += du[j];
+                        sz[j] += dz[j];
+                    }
+                    st_v4(dpre + s * ld_q + n + c, pack8(du));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        dz[j] = d[j] * act_with_grad(act, z[j]).grad;
+                        sz[j] += dz[j];
+                    }
+                }
+                st_v4(dpre + s * ld_q + c, pack8(dz));
+            }
         }
         for (int64_t s = begin + count + r * kGradWarps + warp; s < next; s += kGradSplit * kGradWarps) {
             st_v4(dpre + s * ld_q + c, make_uint4(0, 0, 0, 0));
