@@ -569,7 +569,7 @@ typedef struct qz_router {
  *   groups of largest value keep their experts.
  *   ids = the top_k experts in descending order; equal values go to the lower
  *   index.  Biased scores and group values are compared in binary64.
- *   w_j = s_j (over sum_j s_j if renormalize; 0 if that sum is 0) * scale, fp32.
+ *   w_j = s_j (over sum_j s_j if renormalize; 0 if that sum is 0 in binary64) * scale, fp32.
  * A logit of -inf or NaN, or a biased score of -inf or NaN, masks an expert: it
  * is never chosen and counts 0 in a softmax.  Choices that remain empty get
  * id -1 and weight 0 (all of them in a row that is masked entirely).  A logit

@@ -16,23 +16,27 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     return r;
 }
 
-// exp(x) through the hardware's 2^x: within 2 + floor(1.17 |x|) ulp for the
-// fp32 range (CUDA programming guide), far below the bf16 step of the result
-// for the |x| < 90 that matter.
+// e^x as 2^(x log2 e) on the special function unit: PTX bounds ex2.approx by 2
+// ulp, and the rounded product adds |x| / 2 ulp at most; results below 2^-126
+// are 0.  rcp.approx is within 1 ulp.  Both are single instructions, and far
+// below the half step of a bf16 result.
+__device__ __forceinline__ float fast_exp(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // 1 / (1 + exp(-x)); exp(-x) overflows to inf below -88 and the quotient is 0.
-__device__ __forceinline__ float sigmoid32(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+__device__ __forceinline__ float sigmoid32(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
 
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
-
-// z (1 + tanh(v)) / 2 = z / (1 + exp(-2 v)): no cancellation for negative z.
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-    if (ACT == QZ_ACT_RELU) return fmaxf(z, 0.0f);
-    if (ACT == QZ_ACT_SILU) return z * sigmoid32(z);
-    if (ACT == QZ_ACT_GELU) return z * sigmoid32(kGelu2 * fmaf(kGeluC * z * z, z, z));
-    return z;
-}
 
 struct ActPair {
     float value, grad;
@@ -40,19 +44,20 @@ struct ActPair {
 
 // act(z) and act'(z).  With e = exp(-|v|) neither sigmoid(v) nor 1 - sigmoid(v)
 // cancels; SiLU and GELU are both z sigmoid(v), v = z (a + b z^2), v' = a + 3 b z^2.
-__device__ __forceinline__ ActPair act_with_grad(int act, float z) {
+template <int ACT>
+__device__ __forceinline__ ActPair act_with_grad(float z) {
     ActPair p;
-    if (act == QZ_ACT_SILU || act == QZ_ACT_GELU) {
-        const float a = act == QZ_ACT_GELU ? kGelu2 : 1.0f, b = act == QZ_ACT_GELU ? kGelu2 * kGeluC : 0.0f;
+    if (ACT == QZ_ACT_SILU || ACT == QZ_ACT_GELU) {
         const float z2 = z * z;
-        const float v = z * fmaf(b, z2, a);
-        const float e = __expf(-fabsf(v));
-        const float q = __fdividef(1.0f, 1.0f + e);
+        const float v = ACT == QZ_ACT_GELU ? z * fmaf(kGelu2 * kGeluC, z2, kGelu2) : z;
+        const float e = fast_exp(-fabsf(v));
+        const float q = fast_rcp(1.0f + e);
         const float eq = e * q;
         const float s = v >= 0.0f ? q : eq;
+        const float zr = z * (q * eq);  // z sigmoid(v) (1 - sigmoid(v))
         p.value = z * s;
-        p.grad = fmaf(z * (q * eq), fmaf(3.0f * b, z2, a), s);  // sigmoid(v) (1 - sigmoid(v)) = q e q
-    } else if (act == QZ_ACT_RELU) {
+        p.grad = ACT == QZ_ACT_GELU ? fmaf(zr, fmaf(3.0f * kGelu2 * kGeluC, z2, kGelu2), s) : zr + s;
+    } else if (ACT == QZ_ACT_RELU) {
         p.value = fmaxf(z, 0.0f);
         p.grad = z > 0.0f ? 1.0f : 0.0f;
     } else {

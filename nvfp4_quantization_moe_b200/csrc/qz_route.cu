@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "../../include/qz.h"
+#include "qz_act.cuh"
 #include "qz_device.cuh"
 
 namespace qz {
@@ -91,19 +92,30 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-__device__ __forceinline__ double sigmoid64(double x) {
-    const double e = exp(-fabs(x));  // at most 1: no overflow on either side
-    return (x >= 0 ? 1.0 : e) / (1.0 + e);
-}
+// The logit below which a sigmoid is 0 in binary64.
+constexpr float kNoScore = -745.0f;
 
-// x[i] for a warp-uniform register index i.
-template <int PER>
-__device__ __forceinline__ float pick(const float (&x)[PER], int i) {
-    float v = x[0];
+// The warp's best key is taken out of `key` and its index returned (-1: no key
+// is left).  Lane l's key j belongs to index l + 32 j.
+template <int PER, typename K>
+__device__ __forceinline__ int take_best(K (&key)[PER], int lane, K& top) {
+    K best = key[0];
+    uint32_t idx = lane;
 #pragma unroll
-    for (int j = 1; j < PER; ++j)
-        if (j == i) v = x[j];
-    return v;
+    for (int j = 1; j < PER; ++j) {
+        if (key[j] > best) {
+            best = key[j];
+            idx = lane + 32 * j;
+        }
+    }
+    top = warp_best(best, idx);
+    if (top == 0) return -1;
+    if ((int)(idx & 31) == lane) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (j == (int)(idx >> 5)) key[j] = 0;
+    }
+    return (int)idx;
 }
 
 // The two largest of two pairs (a1 >= a2, b1 >= b2) into the first.
@@ -115,12 +127,13 @@ __device__ __forceinline__ void merge_two(F& a1, F& a2, F b1, F b2) {
 
 __device__ __forceinline__ uint32_t key_of(float v) { return key32(v); }
 __device__ __forceinline__ unsigned long long key_of(double v) { return key64(v); }
-__device__ __forceinline__ float score_exp(float v) { return expf(v); }
+__device__ __forceinline__ float score_exp(float v) { return fast_exp(v); }
 __device__ __forceinline__ double score_exp(double v) { return exp(v); }
+__device__ __forceinline__ float score_rcp(float v) { return fast_rcp(v); }
+__device__ __forceinline__ double score_rcp(double v) { return 1.0 / v; }
 
 struct Choice {
     int id;        // lane j: choice j, -1 if there is none
-    float logit;   // its logit, -inf if there is none
     bool certain;  // the fp32 choice cannot differ from the binary64 one
 };
 
@@ -135,14 +148,14 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const F e = x[j] > -INFINITY ? score_exp(sigmoid ? -fabs((F)x[j]) : (F)x[j] - (F)m) : (F)0;
-        v[j] = !sigmoid ? e : !(x[j] > -INFINITY) ? (F)0 : (x[j] >= 0 ? (F)1 : e) / ((F)1 + e);
+        v[j] = !sigmoid ? e : !(x[j] > -INFINITY) ? (F)0 : (x[j] >= 0 ? (F)1 : e) * score_rcp((F)1 + e);
         part += v[j];
     }
     F largest = 0;  // score or |v|, for the error bound
     if (!sigmoid) {
-        const F sum = warp_sum(part);
+        const F scale = score_rcp(warp_sum(part));
 #pragma unroll
-        for (int j = 0; j < PER; ++j) v[j] = v[j] / sum;
+        for (int j = 0; j < PER; ++j) v[j] = v[j] * scale;
     }
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -152,9 +165,9 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
         if (!(x[j] > -INFINITY) || v[j] != v[j]) v[j] = -INFINITY;
         else if (sizeof(F) == 4 && fabs(v[j]) < INFINITY) largest = fmax(largest, (F)fabs(v[j]));
     }
-    // fp32: exp within 2 ulp, its argument's rounding (|x - m| e^(x - m) <= 1 / e), a sum of E terms in
-    // a tree, a quotient and a sum: below 16 roundings of the largest magnitude
-    const F bound = sizeof(F) == 4 ? (F)warp_max((float)largest) * (F)(16.0 / 16777216.0) : (F)0;
+    // fp32: 2^x within 2 ulp, its argument's rounding (|x - m| e^(x - m) <= 1 / e), a sum of E terms in
+    // a tree, a reciprocal within 1 ulp, a product and a sum: below 24 half ulps of the largest magnitude
+    const F bound = sizeof(F) == 4 ? (F)warp_max((float)largest) * (F)(24.0 / 16777216.0) : (F)0;
     bool certain = true;
 
     decltype(key_of(F())) key[PER];
@@ -200,38 +213,22 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
         if (GROUPS && i < a.E && !((kept >> (i / size)) & 1u)) key[j] = 0;
     }
 
-    Choice r = {-1, -INFINITY, certain};
+    Choice r = {-1, certain};
     F last = INFINITY;
     // one round more than top_k, where the fp32 verdict wants the value behind the last choice
     const int rounds = a.k + (sizeof(F) == 4 && !by_logit ? 1 : 0);
     for (int c = 0; c < rounds; ++c) {
-        auto best = key[0];
-        uint32_t idx = lane;
-#pragma unroll
-        for (int j = 1; j < PER; ++j) {
-            if (key[j] > best) {
-                best = key[j];
-                idx = lane + 32 * j;
-            }
-        }
-        const auto top = warp_best(best, idx);
-        if (top == 0) break;  // no expert is left
-        const int at = (int)(idx >> 5), from = (int)(idx & 31);
+        decltype(key_of(F())) top;
+        const int idx = take_best<PER>(key, lane, top);
+        if (idx < 0) break;  // no expert is left
         if (sizeof(F) == 4 && !by_logit) {
             const F now = (F)__uint_as_float((top & 0x80000000u) ? (uint32_t)top ^ 0x80000000u : ~(uint32_t)top);
             if (c > 0 && !(last - now > 2 * bound)) r.certain = false;
             last = now;
         }
-        if (c == a.k) break;
-        const float logit = __shfl_sync(kFull, pick<PER>(x, at), from);
-        if (lane == c) {
-            r.id = (int)idx;
-            r.logit = logit;
-        }
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (j == at && lane == from) key[j] = 0;
+        if (lane == c) r.id = idx;  // the round behind the last choice is not a choice
     }
+    if (lane >= a.k) r.id = -1;
     return r;
 }
 
@@ -255,53 +252,38 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     const bool sigmoid = a.score == QZ_SCORE_SIGMOID;
 
     int id = -1;
-    float chosen = -INFINITY;
     if (SIMPLE) {
         uint32_t key[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) key[j] = key32(x[j]);
         for (int c = 0; c < a.k; ++c) {
-            uint32_t best = key[0], idx = lane;
-#pragma unroll
-            for (int j = 1; j < PER; ++j) {
-                if (key[j] > best) {
-                    best = key[j];
-                    idx = lane + 32 * j;
-                }
-            }
-            if (warp_best(best, idx) == 0) break;  // no expert is left
-            const int at = (int)(idx >> 5), from = (int)(idx & 31);
-            const float v = __shfl_sync(kFull, pick<PER>(x, at), from);
-            if (lane == c) {
-                id = (int)idx;
-                chosen = v;
-            }
-#pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (j == at && lane == from) key[j] = 0;
+            uint32_t top;
+            const int idx = take_best<PER>(key, lane, top);
+            if (idx < 0) break;  // no expert is left
+            if (lane == c) id = idx;
         }
     } else {
         double* scratch = s_values + warp * (a.E + a.E / 32 + 1);
         Choice r = choose<PER, float, GROUPS>(a, x, m, reinterpret_cast<float*>(scratch), lane);
         if (!r.certain) r = choose<PER, double, GROUPS>(a, x, m, scratch, lane);
         id = r.id;
-        chosen = r.logit;
     }
 
-    // weights: the chosen scores, in binary64 for a sigmoid (whose value may be
-    // far below 1 for every choice), relative to the largest chosen logit for
-    // a renormalized softmax
+    // weights: lane j's choice again from memory (the row is in L1), with the accurate exponential
     const bool live = id >= 0;
+    const float chosen = live ? load_logit<BF16>(a.logits, t * a.ld + id) : -INFINITY;
+    const float top = warp_max(chosen);
     float w = 0.0f;
-    if (sigmoid) {
-        const double s = live ? sigmoid64((double)chosen) : 0.0;
-        const double total = a.renorm ? warp_sum(s) : 1.0;
-        w = total > 0.0 ? (float)(s / total) : 0.0f;
+    if (sigmoid && !(a.renorm && top < -20.0f)) {
+        const float e = expf(-fabsf(chosen));
+        const float s = live ? (chosen >= 0.0f ? 1.0f : e) / (1.0f + e) : 0.0f;
+        w = a.renorm ? s / warp_sum(s) : s;  // the sum is at least sigmoid(-20)
     } else if (a.renorm) {
-        const float top = warp_max(chosen);
+        // relative to the largest chosen logit; below -20 a sigmoid is its exponential to fp32, so that
+        // a row of tiny scores keeps its ratios (below kNoScore they are 0 in binary64 too)
         const float s = live ? expf(chosen - top) : 0.0f;
         const float total = warp_sum(s);
-        w = live ? s / total : 0.0f;
+        w = live && !(sigmoid && top < kNoScore) ? s / total : 0.0f;
     } else {
         float part = 0.0f;
 #pragma unroll
@@ -357,11 +339,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(RouteGradA
         const float s = live ? (chosen >= 0 ? 1.0f : e) / (1.0f + e) : 0.0f;
         const float rest = (chosen >= 0 ? e : 1.0f) / (1.0f + e);  // 1 - s without cancellation
         if (a.renorm) {
-            // relative to the largest chosen score, so that a row of tiny scores keeps its ratios
+            // tiny scores as in the forward
             const float top = warp_max(chosen);
-            const float et = expf(-fabsf(top));
-            const float lead = (top >= 0 ? 1.0f : et) / (1.0f + et);
-            const float r = live && lead > 0.0f ? s / lead : 0.0f;
+            const float r = top < -20.0f ? (live && top >= kNoScore ? expf(chosen - top) : 0.0f) : s;
             const float S = warp_sum(r);
             const float w = S > 0.0f ? r / S : 0.0f;
             dot = warp_sum(g * w);
@@ -431,7 +411,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(RouteGradA
 // pairs; otherwise a launch that counts each chunk and one that places.
 
 constexpr int kPlanWarps = 16;
-constexpr int kPlanChunk = 4096;  // least pairs of a chunk when there are several
+constexpr int kPlanChunk = 2048;  // least pairs of a chunk when there are several
 constexpr int kPlanMost = 128;    // most chunks: each CTA of the second launch reads every chunk's counts
 constexpr int kPlanOne = 8192;    // pairs up to which one CTA sorts alone
 
@@ -478,7 +458,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_count_kernel(PlanArgs a)
 }
 
 __global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a) {
-    extern __shared__ int s_cnt[];  // [warps][E], then [E] first slots, then [warps] scan scratch
+    extern __shared__ int s_cnt[];  // [warps][E], then [E] first slots, [warps] scan scratch, [E] pairs before
     int* s_first = s_cnt + kPlanWarps * a.E;
     int* s_scan = s_first + a.E;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -488,24 +468,50 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a)
     if (a.chunks == 1) {
         for (int64_t s = threadIdx.x; s < a.slots; s += blockDim.x) a.rows[s] = -1;
     }
-    // per expert: all pairs (its count), and the pairs of the chunks before this one.
-    // E <= 1024 = 2 * threads, so a thread owns the experts 2i and 2i + 1.
+    // per expert: all pairs (its count) and the pairs of the chunks before this one, by `share` threads
+    // each (a power of two; E <= 1024 = 2 threads' experts).  Sums of whole numbers: any order is the same.
+    const int threads = kPlanWarps * 32;
+    int* s_total = s_first;               // [E], then [E] before
+    int* s_before = s_scan + kPlanWarps;
+    for (int e = threadIdx.x; e < a.E; e += threads) s_total[e] = s_before[e] = 0;
+    __syncthreads();
+    if (a.chunks == 1) {
+        for (int e = threadIdx.x; e < a.E; e += threads) {
+            int c = 0;
+            for (int w = 0; w < kPlanWarps; ++w) c += s_cnt[w * a.E + e];
+            s_total[e] = c;
+        }
+    } else {
+        const int share = max(1, threads / a.E);
+        for (int i = threadIdx.x; i < share * a.E; i += threads) {
+            const int e = i % a.E;
+            int all = 0, early = 0;
+#pragma unroll 4
+            for (int c = i / a.E; c < a.chunks; c += share) {
+                const int v = __ldg(a.hist + (int64_t)c * a.E + e);
+                all += v;
+                early += c < (int)blockIdx.x ? v : 0;
+            }
+            if (share == 1) {
+                s_total[e] = all;
+                s_before[e] = early;
+            } else {
+                atomicAdd(s_total + e, all);
+                atomicAdd(s_before + e, early);
+            }
+        }
+    }
+    __syncthreads();
     int total[2] = {0, 0}, before[2] = {0, 0}, padded = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int e = 2 * threadIdx.x + h;
         if (e >= a.E) continue;
-        if (a.chunks == 1) {
-            for (int w = 0; w < kPlanWarps; ++w) total[h] += s_cnt[w * a.E + e];
-        } else {
-            for (int c = 0; c < a.chunks; ++c) {
-                const int v = a.hist[(int64_t)c * a.E + e];
-                total[h] += v;
-                if (c < (int)blockIdx.x) before[h] += v;
-            }
-        }
+        total[h] = s_total[e];
+        before[h] = s_before[e];
         padded += (total[h] + a.align - 1) & ~(a.align - 1);
     }
+    __syncthreads();  // s_first takes s_total's place
     int incl = padded;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -641,10 +647,10 @@ cudaError_t launch_plan(const int32_t* ids, int64_t T, int k, int E, int align, 
     a.hist = static_cast<int*>(ws);
     const int threads = kPlanWarps * 32;
     const size_t smem_count = (size_t)kPlanWarps * E * sizeof(int);
-    const size_t smem_place = smem_count + (size_t)(E + kPlanWarps) * sizeof(int);  // at most 68 KB
+    const size_t smem_place = smem_count + (size_t)(2 * E + kPlanWarps) * sizeof(int);  // at most 72 KB
     // asked for at its largest every time: the attribute is one value per device and
     // a smaller value of another call must not take it back
-    const int most = (kPlanWarps * QZ_MAX_ROUTE_EXPERTS + QZ_MAX_ROUTE_EXPERTS + kPlanWarps) * (int)sizeof(int);
+    const int most = (kPlanWarps * QZ_MAX_ROUTE_EXPERTS + 2 * QZ_MAX_ROUTE_EXPERTS + kPlanWarps) * (int)sizeof(int);
     if (smem_place > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);

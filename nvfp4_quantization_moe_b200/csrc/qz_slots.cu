@@ -169,12 +169,12 @@ __global__ void __launch_bounds__(kDispatchThreads)
 constexpr int kGradWarps = 8;
 constexpr int kGradCols = 256;
 constexpr int kGradSplit = 8;  // cluster size
-constexpr int kRowsAhead = 4;
+constexpr int kRowsAhead = 2;
 
-template <bool GATED>
-__global__ void __launch_bounds__(kGradWarps * 32) __cluster_dims__(1, kGradSplit, 1)
+template <int ACT, bool GATED>
+__global__ void __launch_bounds__(kGradWarps * 32, 3) __cluster_dims__(1, kGradSplit, 1)
     act_grad_kernel(const uint16_t* __restrict__ dout, int64_t ld_d, const uint16_t* __restrict__ pre, int64_t ld_p,
-                    int64_t slots, int64_t n, int act, const int32_t* __restrict__ offsets,
+                    int64_t slots, int64_t n, const int32_t* __restrict__ offsets,
                     const int32_t* __restrict__ counts, int n_experts, uint16_t* __restrict__ dpre, int64_t ld_q,
                     float* __restrict__ dbias, unsigned* d_err) {
     __shared__ float s_sum[kGradWarps][(GATED ? 2 : 1) * kGradCols];
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) __cluster_dims__(1, kGradSpli
                     unpack8(vu[k], u);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const ActPair p = act_with_grad(act, z[j]);
+                        const ActPair p = act_with_grad<ACT>(z[j]);
                         du[j] = d[j] * p.value;
                         dz[j] = d[j] * u[j] * p.grad;
                         su[j] += du[j];
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) __cluster_dims__(1, kGradSpli
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        dz[j] = d[j] * act_with_grad(act, z[j]).grad;
+                        dz[j] = d[j] * act_with_grad<ACT>(z[j]).grad;
                         sz[j] += dz[j];
                     }
                 }
@@ -291,18 +291,38 @@ cudaError_t launch_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* slot
     return cudaGetLastError();
 }
 
+template <int ACT>
+static cudaError_t act_grad_launch(bool gated, dim3 grid, const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p,
+                                   int64_t slots, int64_t n, const int32_t* offsets, const int32_t* counts, int n_experts,
+                                   uint16_t* dpre, int64_t ld_q, float* dbias, cudaStream_t s, unsigned* d_err) {
+    if (gated)
+        act_grad_kernel<ACT, true><<<grid, kGradWarps * 32, 0, s>>>(dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts,
+                                                                    dpre, ld_q, dbias, d_err);
+    else
+        act_grad_kernel<ACT, false><<<grid, kGradWarps * 32, 0, s>>>(dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts,
+                                                                     dpre, ld_q, dbias, d_err);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p, int64_t slots,
                             int64_t n, int act, bool gated, const int32_t* offsets, const int32_t* counts,
                             int n_experts, uint16_t* dpre, int64_t ld_q, float* dbias, cudaStream_t s,
                             unsigned* d_err) {
     const dim3 grid((unsigned)((n + kGradCols - 1) / kGradCols), kGradSplit, (unsigned)n_experts);
-    if (gated)
-        act_grad_kernel<true><<<grid, kGradWarps * 32, 0, s>>>(dout, ld_d, pre, ld_p, slots, n, act, offsets, counts,
-                                                               n_experts, dpre, ld_q, dbias, d_err);
-    else
-        act_grad_kernel<false><<<grid, kGradWarps * 32, 0, s>>>(dout, ld_d, pre, ld_p, slots, n, act, offsets, counts,
-                                                                n_experts, dpre, ld_q, dbias, d_err);
-    return cudaGetLastError();
+    switch (act) {
+        case QZ_ACT_RELU:
+            return act_grad_launch<QZ_ACT_RELU>(gated, grid, dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts, dpre,
+                                                ld_q, dbias, s, d_err);
+        case QZ_ACT_SILU:
+            return act_grad_launch<QZ_ACT_SILU>(gated, grid, dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts, dpre,
+                                                ld_q, dbias, s, d_err);
+        case QZ_ACT_GELU:
+            return act_grad_launch<QZ_ACT_GELU>(gated, grid, dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts, dpre,
+                                                ld_q, dbias, s, d_err);
+        default:
+            return act_grad_launch<QZ_ACT_NONE>(gated, grid, dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts, dpre,
+                                                ld_q, dbias, s, d_err);
+    }
 }
 
 }  // namespace qz

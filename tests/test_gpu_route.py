@@ -183,6 +183,15 @@ def test_route_grad_against_differences(score, renorm):
     ref.close(got[0], diff, tol, "dlogits")
 
 
+def test_route_grad_of_tiny_scores():
+    """Sigmoids far below fp32's range keep their ratios, and their gradients."""
+    x = torch.tensor([[-200.0, -201.0, -199.5, -400.0], [-30.0, -31.0, -29.0, -90.0]]).cuda()
+    ids, w = check_route(x, 3, SIGMOID)
+    dw = torch.tensor([[1.0, -2.0, 0.5], [3.0, 1.0, -1.0]]).cuda()
+    got = qz.route_experts_grad(x, ids, dw, score=SIGMOID)
+    ref.close(got, grad_reference(x, ids, dw, True, True, 1.0), 64 * ref.HALF_F32 * 3, "dlogits")
+
+
 # --- expert order -----------------------------------------------------------
 
 @pytest.mark.parametrize("T,E,k,align", [(0, 4, 2, 8), (1, 1, 1, 1), (1, 128, 8, 128), (5, 7, 3, 16), (333, 60, 4, 1),
