@@ -719,12 +719,16 @@ qz_status qz_expert_weight_grad(const qz_weight_grad *p, void *stream, const qz_
  *   d_dout: bf16 [slots, n];  d_pre, d_dpre: bf16 [slots, n] (gated: [slots, 2n], z then u),
  *   row strides ld_* (multiples of 8, pointers 16-byte aligned);  d_dbias: float [n_experts, n]
  *   (gated [n_experts, 2n]) or NULL;  d_offsets: int32 [n_experts + 1], ascending
- * Rows of d_dpre that are no live slot are written as zeros.
+ * Rows of d_dpre that are no live slot are written as zeros.  d_dbias needs
+ * opts->d_workspace, qz_activation_grad_bytes(slots, n, gated, n_experts) bytes,
+ * 16-byte aligned, not shared with a call that may overlap.
  * Errors: QZ_ERR_INVALID_ARG for sizes, enums or null pointers outside the above; QZ_ERR_ALIGNMENT. */
 qz_status qz_expert_activation_grad(const void *d_dout, int64_t ld_dout, const void *d_pre, int64_t ld_pre,
                                     int64_t slots, int64_t n, int activation, int gated, const int32_t *d_offsets,
                                     const int32_t *d_counts, int n_experts, void *d_dpre, int64_t ld_dpre,
                                     float *d_dbias, void *stream, const qz_launch_opts *opts);
+
+size_t qz_activation_grad_bytes(int64_t slots, int64_t n, int gated, int n_experts);
 
 /* Token order -> expert order: y[slots[t][j]] = bf16(w[t][j] x[t]); every slot
  * whose d_rows entry is -1 gets a row of zeros.  With d_other also

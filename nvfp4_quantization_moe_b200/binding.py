@@ -65,6 +65,7 @@ EXPORTED = (
     "qz_product_bytes",
     "qz_expert_weight_grad",
     "qz_expert_activation_grad",
+    "qz_activation_grad_bytes",
     "qz_dispatch_experts",
     "qz_combine_experts",
 )
@@ -211,6 +212,8 @@ def load(path: str = LIB_PATH):
         lib.qz_product_bytes.argtypes = [P]
         lib.qz_expert_weight_grad.restype = I
         lib.qz_expert_weight_grad.argtypes = [P, P, P]
+        lib.qz_activation_grad_bytes.restype = ctypes.c_size_t
+        lib.qz_activation_grad_bytes.argtypes = [i64, i64, I, I]
         lib.qz_expert_activation_grad.restype = I
         lib.qz_expert_activation_grad.argtypes = [P, i64, P, i64, i64, i64, I, I, P, P, I, P, i64, P, P, P]
         lib.qz_dispatch_experts.restype = I
@@ -644,6 +647,18 @@ def _codes(t, name: str, cols: int, fmt: int, dev: int) -> int:
     return t.data_ptr()
 
 
+def _scratch(nbytes: int, like: torch.Tensor, stream):
+    """Device scratch of one call from torch's allocator, None for none.  The
+    allocator may hand it to the current stream's next user, so a call on
+    another stream is recorded."""
+    if nbytes == 0:
+        return None
+    t = like.new_empty(nbytes, dtype=torch.uint8)
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return t
+
+
 def _parts(x, name: str):
     if not isinstance(x, (tuple, list)) or len(x) not in (2, 3):
         raise ValueError(f"{name} must be (payload, scales) or (payload, scales, amax)")
@@ -743,8 +758,8 @@ def plan_experts(ids: torch.Tensor, n_experts: int, *, align: int = 1, plan: Opt
         offsets, counts, rows, slots = ids.new_empty(2 * n_experts + 1 + n + T * k).split(
             (n_experts + 1, n_experts, n, T * k))
         plan = ExpertPlan(offsets, counts, rows, slots.view(T, k))
-    if need and workspace is None:
-        workspace = ids.new_empty(need, dtype=torch.uint8)
+    if workspace is None:
+        workspace = _scratch(need, ids, stream)
     ws = 0 if workspace is None else _tensor(workspace, "workspace", torch.uint8, dev)
     _check(lib.qz_plan_experts(i, T, k, int(n_experts), int(align),
                                _tensor(plan.offsets, "offsets", torch.int32, dev, (n_experts + 1,)),
@@ -833,11 +848,7 @@ def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, 
     if workspace is not None:
         _tensor(workspace, "workspace", torch.uint8, dev)
     elif rows is not None:
-        need = lib.qz_product_bytes(ref)
-        if need:
-            workspace = out.new_empty(need, dtype=torch.uint8)
-            if stream is not None and hasattr(stream, "cuda_stream"):
-                workspace.record_stream(stream)
+        workspace = _scratch(lib.qz_product_bytes(ref), out, stream)
     _check(lib.qz_expert_product(ref, s, _opts(err, max_ctas, workspace)), "qz_expert_product")
     return out
 
@@ -875,13 +886,13 @@ def expert_weight_grad(fmt: int, dz, x, offsets: torch.Tensor, counts: torch.Ten
 
 
 def expert_activation_grad(dout: torch.Tensor, pre: torch.Tensor, offsets: torch.Tensor, counts: torch.Tensor,
-                           dpre: torch.Tensor, *, activation: int, gated: bool = False, dbias=None, stream=None,
-                           err=None):
+                           dpre: torch.Tensor, *, activation: int, gated: bool = False, dbias=None, workspace=None,
+                           stream=None, err=None):
     """Gradient of expert_product's activation from its saved pre-activations,
     with the bias gradients (qz_expert_activation_grad): dout [slots, N], pre
     and dpre bf16 [slots, N or 2N], dbias fp32 [E, N or 2N] or None.  offsets
     must be [E + 1] or [E], as the plan writes them; rows of dpre that are no
-    live slot become zeros."""
+    live slot become zeros.  dbias needs a workspace (allocated unless given)."""
     _require(dout.dim() == 2, "dout must be [slots, N]")
     dev = dout.get_device()
     S, N = dout.shape
@@ -891,9 +902,13 @@ def expert_activation_grad(dout: torch.Tensor, pre: torch.Tensor, offsets: torch
     d, ldd = _matrix(dout, "dout", torch.bfloat16, dev, (S, N))
     z, ldz = _matrix(pre, "pre", torch.bfloat16, dev, (S, width))
     g, ldg = _matrix(dpre, "dpre", torch.bfloat16, dev, (S, width))
-    _check(load().qz_expert_activation_grad(d, ldd, z, ldz, S, N, int(activation), 1 if gated else 0, offs, cnts, E,
-                                            g, ldg, _tensor(dbias, "dbias", torch.float32, dev, (E, width), optional=True),
-                                            _raw_stream(stream, dev), _opts(err, 0)), "qz_expert_activation_grad")
+    lib, b, st = load(), _tensor(dbias, "dbias", torch.float32, dev, (E, width), optional=True), _raw_stream(stream, dev)
+    if workspace is not None:
+        _tensor(workspace, "workspace", torch.uint8, dev)
+    elif b:
+        workspace = _scratch(lib.qz_activation_grad_bytes(S, N, 1 if gated else 0, E), dout, stream)
+    _check(lib.qz_expert_activation_grad(d, ldd, z, ldz, S, N, int(activation), 1 if gated else 0, offs, cnts, E, g, ldg,
+                                         b, st, _opts(err, 0, workspace)), "qz_expert_activation_grad")
     return dpre
 
 

@@ -55,8 +55,9 @@ cudaError_t launch_product(const qz_product& call, int ctas, cudaStream_t s, uns
 cudaError_t launch_weight_grad(const qz_weight_grad& p, int ctas, cudaStream_t s, unsigned* d_err);
 cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p, int64_t slots,
                             int64_t n, int act, bool gated, const int32_t* offsets, const int32_t* counts,
-                            int n_experts, uint16_t* dpre, int64_t ld_q, float* dbias, cudaStream_t s,
+                            int n_experts, uint16_t* dpre, int64_t ld_q, float* dbias, float* sums, int sms, cudaStream_t s,
                             unsigned* d_err);
+size_t act_grad_bytes(int64_t slots, int64_t n, bool gated, int n_experts);
 cudaError_t launch_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* slots, const int32_t* rows, int64_t T,
                             int k, int64_t n_slots, int64_t H, const float* weights, uint16_t* y, int64_t ld_y,
                             const uint16_t* other, int64_t ld_o, float* dots, cudaStream_t s);
@@ -547,6 +548,13 @@ qz_status qz_expert_weight_grad(const qz_weight_grad* p, void* stream, const qz_
     return from_cuda(qz::launch_weight_grad(*p, one_per_sm(opts), (cudaStream_t)stream, err_word(opts)));
 }
 
+size_t qz_activation_grad_bytes(int64_t slots, int64_t n, int gated, int n_experts) {
+    if (slots < 0 || slots > kMaxIndex || n < 8 || n % 8 != 0 || n > QZ_MAX_LD || n_experts < 1 ||
+        n_experts > QZ_MAX_ROUTE_EXPERTS)
+        return 0;
+    return qz::act_grad_bytes(slots, n, gated != 0, n_experts);
+}
+
 qz_status qz_expert_activation_grad(const void* d_dout, int64_t ld_dout, const void* d_pre, int64_t ld_pre,
                                     int64_t slots, int64_t n, int activation, int gated, const int32_t* d_offsets,
                                     const int32_t* d_counts, int n_experts, void* d_dpre, int64_t ld_dpre,
@@ -559,10 +567,15 @@ qz_status qz_expert_activation_grad(const void* d_dout, int64_t ld_dout, const v
     if (!aligned(d_dout, 16) || !aligned(d_pre, 16) || !aligned(d_dpre, 16) || !aligned(d_dbias, 4) ||
         !aligned(d_offsets, 4) || !aligned(d_counts, 4))
         return QZ_ERR_ALIGNMENT;
+    void* const ws = opts ? opts->d_workspace : nullptr;
+    if (d_dbias && (!ws || opts->workspace_bytes < qz::act_grad_bytes(slots, n, gated != 0, n_experts)))
+        return QZ_ERR_INVALID_ARG;
+    if (!aligned(ws, 16)) return QZ_ERR_ALIGNMENT;
     return from_cuda(qz::launch_act_grad(static_cast<const uint16_t*>(d_dout), ld_dout,
                                          static_cast<const uint16_t*>(d_pre), ld_pre, slots, n, activation, gated != 0,
                                          d_offsets, d_counts, n_experts, static_cast<uint16_t*>(d_dpre), ld_dpre,
-                                         d_dbias, (cudaStream_t)stream, err_word(opts)));
+                                         d_dbias, static_cast<float*>(ws), device_sms(), (cudaStream_t)stream,
+                                         err_word(opts)));
 }
 
 qz_status qz_dispatch_experts(const void* d_x, int64_t ld_x, const int32_t* d_slots, const int32_t* d_rows, int64_t T,

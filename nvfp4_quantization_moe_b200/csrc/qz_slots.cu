@@ -6,7 +6,6 @@
 // All three stream bf16 rows once and are bound by HBM; the arithmetic is fp32
 // with one rounding to bf16 per output.  Sums that cross threads are formed in
 // a fixed order (no atomics), so results repeat bit for bit.
-#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -15,8 +14,6 @@
 #include "qz_device.cuh"
 
 namespace qz {
-
-namespace cg = cooperative_groups;
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     f[0] = bf16_lo(v.x);
@@ -160,56 +157,89 @@ __global__ void __launch_bounds__(kDispatchThreads)
 // activation gradient
 // ---------------------------------------------------------------------------
 //
-// CTA (c, r, e): 256 columns of the rows of expert e that cluster rank r owns.
-// A warp takes one row at a time, 8 columns per lane, and keeps its columns'
-// sums; the warps' sums, then the cluster's (through distributed shared
-// memory), are added in a fixed order.  The cluster of 8 splits an expert's
-// rows because there are too few (expert, column block) pairs to fill the GPU.
+// A piece of work is `piece` rows of one expert's range (up to the next
+// expert's start, so that the unused slots are zeroed on the way) x 256 columns,
+// and one warp's: 8 columns per lane, four rows' loads in flight, no barriers.  A
+// persistent grid takes the pieces in turn, which evens out experts of any
+// length.  (A cluster per expert and column block, joined through distributed
+// shared memory, was measured first: 98 us on 4096 x 8 rows of 2 x 768 over 128
+// experts, most of it waiting at barriers for uneven warps and for stores.)  A
+// warp leaves its piece's column sums in the workspace and a second launch adds
+// an expert's pieces in order.
 
 constexpr int kGradWarps = 8;
 constexpr int kGradCols = 256;
-constexpr int kGradSplit = 8;  // cluster size
-constexpr int kRowsAhead = 2;
+constexpr int kGradCtas = 2;       // per SM
+constexpr int kRowsAhead = 4;
+constexpr int64_t kMostPieces = 4096;  // pieces are 16 rows, or more when there would be more of them than this
+
+struct GradPieces {
+    const int32_t *offsets, *counts;
+    int64_t slots;
+    int n_experts, piece;
+};
+
+// An expert's range: first slot, live slots, end (the next expert's start; the buffer's end for the last).
+struct SlotRange {
+    int64_t begin, count, next;
+    bool bad;
+};
+
+__device__ __forceinline__ SlotRange slot_range(const GradPieces& a, int e) {
+    SlotRange r;
+    r.begin = __ldg(a.offsets + e);
+    r.count = __ldg(a.counts + e);
+    r.next = e + 1 < a.n_experts ? (int64_t)__ldg(a.offsets + e + 1) : a.slots;
+    r.bad = r.begin < 0 || r.count < 0 || r.begin + r.count > r.next || r.next > a.slots;
+    return r;
+}
+
+// Pieces before each expert, in shared memory; every thread of the block must call it.
+__device__ __forceinline__ int piece_prefix(const GradPieces& a, int* s_prefix, long long* s_scratch, unsigned* d_err) {
+    return block_prefix(
+        a.n_experts, s_prefix, s_scratch,
+        [&](int e) -> long long {
+            const SlotRange r = slot_range(a, e);
+            if (r.bad && blockIdx.x == 0 && d_err) atomicOr(d_err, QZ_DERR_SHAPE);
+            return r.bad ? 0 : (r.next - r.begin + a.piece - 1) / a.piece;
+        },
+        d_err);
+}
 
 template <int ACT, bool GATED>
-__global__ void __launch_bounds__(kGradWarps * 32, 3) __cluster_dims__(1, kGradSplit, 1)
-    act_grad_kernel(const uint16_t* __restrict__ dout, int64_t ld_d, const uint16_t* __restrict__ pre, int64_t ld_p,
-                    int64_t slots, int64_t n, const int32_t* __restrict__ offsets,
-                    const int32_t* __restrict__ counts, int n_experts, uint16_t* __restrict__ dpre, int64_t ld_q,
-                    float* __restrict__ dbias, unsigned* d_err) {
-    __shared__ float s_sum[kGradWarps][(GATED ? 2 : 1) * kGradCols];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e = blockIdx.z, r = blockIdx.y;
-    const int64_t c = (int64_t)blockIdx.x * kGradCols + 8 * lane;
-    const int64_t begin = __ldg(offsets + e);
-    int64_t count = __ldg(counts + e);
-    // the rows up to the next expert's (the end of the buffer for the last) are this expert's to zero
-    int64_t next = e + 1 < n_experts ? (int64_t)__ldg(offsets + e + 1) : slots;
-    const bool bad = begin < 0 || count < 0 || begin + count > slots || next < begin + count || next > slots;
-    if (bad) {
-        if (d_err && r == 0 && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(d_err, QZ_DERR_SHAPE);
-        count = 0;
-        next = begin;
-    }
-    float sz[8] = {0, 0, 0, 0, 0, 0, 0, 0}, su[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (c < n) {
-        // kRowsAhead rows' loads are in flight before the first is used
-        constexpr int64_t kStep = kGradSplit * kGradWarps;
-        for (int64_t i0 = r * kGradWarps + warp; i0 < count; i0 += kRowsAhead * kStep) {
+__global__ void __launch_bounds__(kGradWarps * 32, kGradCtas)
+    act_grad_kernel(GradPieces a, const uint16_t* __restrict__ dout, int64_t ld_d, const uint16_t* __restrict__ pre,
+                    int64_t ld_p, int64_t n, uint16_t* __restrict__ dpre, int64_t ld_q, float* __restrict__ sums,
+                    unsigned* d_err) {
+    extern __shared__ int s_prefix[];
+    __shared__ long long s_scratch[33];
+    const int lane = threadIdx.x & 31;
+    const int blocks = (int)((n + kGradCols - 1) / kGradCols);
+    const int64_t total = (int64_t)piece_prefix(a, s_prefix, s_scratch, d_err) * blocks;
+    const int64_t warps = (int64_t)gridDim.x * kGradWarps;
+    for (int64_t w = (int64_t)blockIdx.x * kGradWarps + (threadIdx.x >> 5); w < total; w += warps) {
+        const int p = (int)(w / blocks);
+        const int64_t c = (int64_t)(w - (int64_t)p * blocks) * kGradCols + 8 * lane;
+        const int e = find_owner(s_prefix, a.n_experts, p);
+        const SlotRange range = slot_range(a, e);
+        const int64_t first = range.begin + (int64_t)(p - s_prefix[e]) * a.piece;
+        const int64_t end = min(range.next, first + a.piece), live = min(end, range.begin + range.count);
+        if (c >= n) continue;
+        float sz[8] = {0, 0, 0, 0, 0, 0, 0, 0}, su[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int64_t s0 = first; s0 < live; s0 += kRowsAhead) {
             uint4 vd[kRowsAhead], vz[kRowsAhead], vu[kRowsAhead];
 #pragma unroll
             for (int k = 0; k < kRowsAhead; ++k) {
-                const int64_t s = begin + i0 + k * kStep;
-                if (i0 + k * kStep >= count) continue;
+                const int64_t s = s0 + k;
+                if (s >= live) continue;
                 vd[k] = ld_stream(dout + s * ld_d + c);
                 vz[k] = ld_stream(pre + s * ld_p + c);
                 if (GATED) vu[k] = ld_stream(pre + s * ld_p + n + c);
             }
 #pragma unroll
             for (int k = 0; k < kRowsAhead; ++k) {
-                const int64_t s = begin + i0 + k * kStep;
-                if (i0 + k * kStep >= count) continue;
+                const int64_t s = s0 + k;
+                if (s >= live) continue;
                 float d[8], z[8], dz[8];
                 unpack8(vd[k], d);
                 unpack8(vz[k], z);
@@ -218,9 +248,9 @@ __global__ void __launch_bounds__(kGradWarps * 32, 3) __cluster_dims__(1, kGradS
                     unpack8(vu[k], u);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const ActPair p = act_with_grad<ACT>(z[j]);
-                        du[j] = d[j] * p.value;
-                        dz[j] = d[j] * u[j] * p.grad;
+                        const ActPair q = act_with_grad<ACT>(z[j]);
+                        du[j] = d[j] * q.value;
+                        dz[j] = d[j] * u[j] * q.grad;
                         su[j] += du[j];
                         sz[j] += dz[j];
                     }
@@ -235,35 +265,73 @@ __global__ void __launch_bounds__(kGradWarps * 32, 3) __cluster_dims__(1, kGradS
                 st_v4(dpre + s * ld_q + c, pack8(dz));
             }
         }
-        for (int64_t s = begin + count + r * kGradWarps + warp; s < next; s += kGradSplit * kGradWarps) {
+        for (int64_t s = max(first, live); s < end; ++s) {
             st_v4(dpre + s * ld_q + c, make_uint4(0, 0, 0, 0));
             if (GATED) st_v4(dpre + s * ld_q + n + c, make_uint4(0, 0, 0, 0));
         }
-    }
-    if (dbias == nullptr) return;  // the same for every CTA of the cluster
+        if (sums != nullptr) {
+            if (live <= first) continue;  // no piece of a live row: not read either
+            float* to = sums + (int64_t)p * (GATED ? 2 * n : n) + c;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        s_sum[warp][8 * lane + j] = sz[j];
-        if (GATED) s_sum[warp][kGradCols + 8 * lane + j] = su[j];
-    }
-    __syncthreads();
-    const int width = (GATED ? 2 : 1) * kGradCols;
-    for (int i = threadIdx.x; i < width; i += blockDim.x) {
-        float v = 0.0f;
-        for (int w = 0; w < kGradWarps; ++w) v += s_sum[w][i];
-        s_sum[0][i] = v;
-    }
-    cluster.sync();
-    if (r == 0) {
-        for (int i = threadIdx.x; i < width; i += blockDim.x) {
-            const int64_t col = (int64_t)blockIdx.x * kGradCols + (i % kGradCols);
-            if (col >= n) continue;
-            float v = 0.0f;
-            for (int q = 0; q < kGradSplit; ++q) v += cluster.map_shared_rank(&s_sum[0][0], q)[i];
-            if (!bad) dbias[(int64_t)e * (GATED ? 2 * n : n) + (i / kGradCols) * n + col] = v;
+            for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+                const float(&v)[8] = h ? su : sz;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    st_v4(to + h * n + 4 * q, make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                                         __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
+            }
         }
     }
-    cluster.sync();  // no CTA leaves while its sums may still be read
+}
+
+// CTA (c, e): 128 columns of expert e's dbias, four per lane.  Warp w adds one
+// eighth of the expert's pieces in order, then the eighths are added in order.
+constexpr int kSumCols = 128;
+
+__global__ void __launch_bounds__(kGradWarps * 32)
+    bias_sum_kernel(GradPieces a, const float* __restrict__ sums, int64_t width, float* __restrict__ dbias) {
+    __shared__ int s_before[kGradWarps];
+    __shared__ float4 s_part[kGradWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.y;
+    const int64_t c = (int64_t)blockIdx.x * kSumCols + 4 * lane;
+    const SlotRange range = slot_range(a, e);
+    if (range.bad) return;  // the same for the whole CTA
+    int before = 0;         // pieces of the experts before this one
+    for (int i = threadIdx.x; i < e; i += kGradWarps * 32) {
+        const SlotRange r = slot_range(a, i);
+        if (!r.bad) before += (int)((r.next - r.begin + a.piece - 1) / a.piece);
+    }
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    if (lane == 0) s_before[warp] = before;
+    __syncthreads();
+    before = 0;
+#pragma unroll
+    for (int w = 0; w < kGradWarps; ++w) before += s_before[w];
+    const int pieces = (int)((range.count + a.piece - 1) / a.piece);  // with live rows
+    const int each = (pieces + kGradWarps - 1) / kGradWarps, end = min(pieces, (warp + 1) * each);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < width) {
+        const float* from = sums + (int64_t)before * width + c;
+#pragma unroll 4
+        for (int p = warp * each; p < end; ++p) {
+            const float4 u = __ldg(reinterpret_cast<const float4*>(from + (int64_t)p * width));
+            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        }
+    }
+    s_part[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && c < width) {
+#pragma unroll
+        for (int w = 1; w < kGradWarps; ++w) {
+            const float4 u = s_part[w][lane];
+            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        }
+        float* to = dbias + (int64_t)e * width + c;  // only float-aligned
+        to[0] = v.x;
+        to[1] = v.y;
+        to[2] = v.z;
+        to[3] = v.w;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -291,38 +359,42 @@ cudaError_t launch_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* slot
     return cudaGetLastError();
 }
 
-template <int ACT>
-static cudaError_t act_grad_launch(bool gated, dim3 grid, const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p,
-                                   int64_t slots, int64_t n, const int32_t* offsets, const int32_t* counts, int n_experts,
-                                   uint16_t* dpre, int64_t ld_q, float* dbias, cudaStream_t s, unsigned* d_err) {
-    if (gated)
-        act_grad_kernel<ACT, true><<<grid, kGradWarps * 32, 0, s>>>(dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts,
-                                                                    dpre, ld_q, dbias, d_err);
-    else
-        act_grad_kernel<ACT, false><<<grid, kGradWarps * 32, 0, s>>>(dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts,
-                                                                     dpre, ld_q, dbias, d_err);
-    return cudaGetLastError();
+static int grad_piece(int64_t slots) {
+    int piece = 16;
+    while ((slots + piece - 1) / piece > kMostPieces) piece *= 2;
+    return piece;
+}
+
+size_t act_grad_bytes(int64_t slots, int64_t n, bool gated, int n_experts) {
+    const int64_t pieces = slots / grad_piece(slots) + n_experts;  // each expert's last may be short
+    return (size_t)pieces * (size_t)(gated ? 2 * n : n) * sizeof(float);
 }
 
 cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p, int64_t slots,
                             int64_t n, int act, bool gated, const int32_t* offsets, const int32_t* counts,
-                            int n_experts, uint16_t* dpre, int64_t ld_q, float* dbias, cudaStream_t s,
+                            int n_experts, uint16_t* dpre, int64_t ld_q, float* dbias, float* sums, int sms, cudaStream_t s,
                             unsigned* d_err) {
-    const dim3 grid((unsigned)((n + kGradCols - 1) / kGradCols), kGradSplit, (unsigned)n_experts);
-    switch (act) {
-        case QZ_ACT_RELU:
-            return act_grad_launch<QZ_ACT_RELU>(gated, grid, dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts, dpre,
-                                                ld_q, dbias, s, d_err);
-        case QZ_ACT_SILU:
-            return act_grad_launch<QZ_ACT_SILU>(gated, grid, dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts, dpre,
-                                                ld_q, dbias, s, d_err);
-        case QZ_ACT_GELU:
-            return act_grad_launch<QZ_ACT_GELU>(gated, grid, dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts, dpre,
-                                                ld_q, dbias, s, d_err);
-        default:
-            return act_grad_launch<QZ_ACT_NONE>(gated, grid, dout, ld_d, pre, ld_p, slots, n, offsets, counts, n_experts, dpre,
-                                                ld_q, dbias, s, d_err);
-    }
+    typedef void (*Kernel)(GradPieces, const uint16_t*, int64_t, const uint16_t*, int64_t, int64_t, uint16_t*, int64_t, float*,
+                           unsigned*);
+    static const Kernel kernels[4][2] = {
+        {act_grad_kernel<QZ_ACT_NONE, false>, act_grad_kernel<QZ_ACT_NONE, true>},
+        {act_grad_kernel<QZ_ACT_RELU, false>, act_grad_kernel<QZ_ACT_RELU, true>},
+        {act_grad_kernel<QZ_ACT_SILU, false>, act_grad_kernel<QZ_ACT_SILU, true>},
+        {act_grad_kernel<QZ_ACT_GELU, false>, act_grad_kernel<QZ_ACT_GELU, true>},
+    };
+    const GradPieces a = {offsets, counts, slots, n_experts, grad_piece(slots)};
+    const int64_t most = (slots / a.piece + n_experts) * ((n + kGradCols - 1) / kGradCols);
+    const int64_t ctas = (most + kGradWarps - 1) / kGradWarps;
+    const unsigned grid = (unsigned)(ctas < (int64_t)sms * kGradCtas ? ctas : (int64_t)sms * kGradCtas);
+    const size_t smem = (size_t)(n_experts + 1) * sizeof(int);
+    kernels[act][gated]<<<grid, kGradWarps * 32, smem, s>>>(a, dout, ld_d, pre, ld_p, n, dpre, ld_q,
+                                                            dbias ? sums : nullptr, d_err);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || dbias == nullptr) return e;
+    const int64_t width = gated ? 2 * n : n;
+    bias_sum_kernel<<<dim3((unsigned)((width + kSumCols - 1) / kSumCols), (unsigned)n_experts), kGradWarps * 32, 0, s>>>(
+        a, sums, width, dbias);
+    return cudaGetLastError();
 }
 
 }  // namespace qz
