@@ -4,15 +4,19 @@
 //
 // Router.  One warp owns one token: lane l holds the logits of experts
 // l, l + 32, ... in registers, so a row is read once and every reduction is a
-// warp reduction.  The choice is top_k rounds of a warp-wide argmax over
-// order-preserving integer keys (redux.sync on the key, then on the index,
-// which gives ties to the lower index).  Without a bias or groups the key is
-// the fp32 logit itself.  With them two experts (or groups) may differ by less
-// than an fp32 rounding of their scores: the choice is first made in fp32, and
-// if any two neighbours that decide it are closer than the fp32 error bound,
-// this token's is made again in binary64 (about one token in a hundred; binary64
-// throughout took 81 us on 16384 tokens of 256 experts in 8 groups).  What
-// remains is bound by instruction issue, not by the 17 MB it reads.
+// warp reduction.  Keys are order-preserving integers.  The choice first bounds
+// itself from below by the top_k-th largest of the lanes' own maxima (one
+// redux.sync a round), which leaves little more than top_k candidates; these go
+// one to a lane and rank themselves against each other, ties to the lower
+// index.  (top_k rounds of a warp-wide argmax over all keys took 19 us in place of
+// 11 on 16384 x 256 logits: what bounds the kernel is instruction issue, not
+// the 17 MB it reads.)
+//
+// Without a bias or groups the key is the fp32 logit itself.  With them two
+// experts (or groups) may differ by less than an fp32 rounding of their scores:
+// the choice is first made in fp32, and if any two neighbours that decide it are
+// closer than the fp32 error bound, this token's is made again in binary64
+// (binary64 throughout took 81 us on 16384 tokens of 256 experts in 8 groups).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -34,6 +38,7 @@ struct RouteArgs {
     const float* bias;
     int64_t T, ld;
     int E, k, score, n_groups, top_groups, renorm;
+    int step_groups, step_rest;  // 32 experts further: groups, and experts of a group
     float scale;
     int32_t* ids;
     float* weights;
@@ -55,6 +60,11 @@ __device__ __forceinline__ uint32_t key32(float v) {
     v = v + 0.0f;  // -0 and +0 are one value
     const uint32_t b = __float_as_uint(v);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// The number of a key above 0.
+__device__ __forceinline__ float unkey32(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
 __device__ __forceinline__ unsigned long long key64(double v) {
@@ -98,7 +108,7 @@ constexpr float kNoScore = -745.0f;
 // The warp's best key is taken out of `key` and its index returned (-1: no key
 // is left).  Lane l's key j belongs to index l + 32 j.
 template <int PER, typename K>
-__device__ __forceinline__ int take_best(K (&key)[PER], int lane, K& top) {
+__device__ __forceinline__ int take_best(K (&key)[PER], int lane) {
     K best = key[0];
     uint32_t idx = lane;
 #pragma unroll
@@ -108,14 +118,70 @@ __device__ __forceinline__ int take_best(K (&key)[PER], int lane, K& top) {
             idx = lane + 32 * j;
         }
     }
-    top = warp_best(best, idx);
-    if (top == 0) return -1;
+    if (warp_best(best, idx) == 0) return -1;
     if ((int)(idx & 31) == lane) {
 #pragma unroll
         for (int j = 0; j < PER; ++j)
             if (j == (int)(idx >> 5)) key[j] = 0;
     }
     return (int)idx;
+}
+
+// A lane's share of the choice: expert `id` (-1: none) is choice `at`, if that is below top_k.
+struct Pick {
+    int id, at;
+};
+
+// top_k rounds of a warp-wide argmax.
+template <int PER, typename K>
+__device__ __forceinline__ Pick pick_by_rounds(K (&key)[PER], int k, int lane) {
+    Pick r = {-1, lane};
+    for (int c = 0; c < k; ++c) {
+        const int idx = take_best<PER>(key, lane);
+        if (idx < 0) break;  // no expert is left
+        if (lane == c) r.id = idx;
+    }
+    return r;
+}
+
+// The same by candidates (see the top of the file); with VERDICT the smallest
+// difference to the next value behind a chosen one goes to *gap.  false: more
+// than 32 candidates, nothing is decided.
+template <int PER, bool VERDICT>
+__device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, int lane, uint2* cand, Pick& r, float* gap) {
+    uint32_t left = key[0], bar = 1;
+#pragma unroll
+    for (int j = 1; j < PER; ++j) left = max(left, key[j]);
+    const int rounds = VERDICT ? k + 1 : k;  // the verdict wants the value behind the last choice too
+    for (int c = 0; c < rounds; ++c) {
+        bar = __reduce_max_sync(kFull, left);
+        if (left == bar) left = 0;
+    }
+    if (rounds > 32 || bar == 0) bar = 1;  // fewer lanes than choices: every key above 0
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const bool in = key[j] >= bar;
+        const unsigned mask = __ballot_sync(kFull, in);
+        const int at = n + __popc(mask & ((1u << lane) - 1u));
+        if (in && at < 32) cand[at] = make_uint2(key[j], (uint32_t)(lane + 32 * j));
+        n += __popc(mask);
+    }
+    if (n > 32) return false;
+    __syncwarp();
+    const uint2 mine = lane < n ? cand[lane] : make_uint2(0u, 0u);
+    int before = 0;
+    uint32_t behind = 0;
+    for (int i = 0; i < n; ++i) {
+        const uint2 other = cand[i];
+        const bool ahead = other.x > mine.x || (other.x == mine.x && other.y < mine.y);
+        if (ahead) ++before;
+        else if (VERDICT && i != lane) behind = max(behind, other.x);
+    }
+    r.id = lane < n ? (int)mine.y : -1;
+    r.at = lane < n ? before : lane;
+    if (VERDICT) *gap = lane < n && before < k && behind != 0 ? unkey32(mine.x) - unkey32(behind) : INFINITY;
+    return true;
 }
 
 // The two largest of two pairs (a1 >= a2, b1 >= b2) into the first.
@@ -133,15 +199,33 @@ __device__ __forceinline__ float score_rcp(float v) { return fast_rcp(v); }
 __device__ __forceinline__ double score_rcp(double v) { return 1.0 / v; }
 
 struct Choice {
-    int id;        // lane j: choice j, -1 if there is none
+    Pick pick;
     bool certain;  // the fp32 choice cannot differ from the binary64 one
 };
+
+// The picks, and for fp32 values whether the differences allow them.
+template <int PER, typename F>
+__device__ __forceinline__ void decide(const RouteArgs& a, unsigned long long (&key)[PER], int lane, uint2*, F, bool, Choice& r) {
+    r.pick = pick_by_rounds<PER>(key, a.k, lane);
+}
+
+template <int PER, typename F>
+__device__ __forceinline__ void decide(const RouteArgs& a, uint32_t (&key)[PER], int lane, uint2* cand, F bound, bool by_logit,
+                                       Choice& r) {
+    float gap = INFINITY;
+    if (!pick_by_rank<PER, true>(key, a.k, lane, cand, r.pick, &gap)) {
+        r.certain = r.certain && by_logit;
+        if (r.certain) r.pick = pick_by_rounds<PER>(key, a.k, lane);
+        return;
+    }
+    if (!by_logit && !__all_sync(kFull, gap > 2.0f * (float)bound)) r.certain = false;
+}
 
 // The choice by values of type F (float: with a verdict on its certainty).
 // `by_logit`: the logits order the experts themselves (no bias); the values
 // then only rank the groups.  `scratch` holds E + E / 32 + 1 values of F.
 template <int PER, typename F, bool GROUPS>
-__device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PER], float m, F* scratch, int lane) {
+__device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PER], float m, F* scratch, uint2* cand, int lane) {
     const bool sigmoid = a.score == QZ_SCORE_SIGMOID, by_logit = a.bias == nullptr;
     F v[PER];
     F part = 0;
@@ -206,29 +290,27 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
         kept = __ballot_sync(kFull, lane < a.n_groups && before < a.top_groups);
         if (sizeof(F) == 4) certain = !__any_sync(kFull, lane < a.n_groups && close);
     }
+    int group = 0, in_group = 0;  // of expert lane + 32 j, kept up without divisions
+    if (GROUPS) {
+        group = lane / size;
+        in_group = lane - group * size;
+    }
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int i = lane + 32 * j;
         key[j] = by_logit ? (v[j] > -INFINITY ? key_of((F)x[j]) : 0) : key_of(v[j]);
-        if (GROUPS && i < a.E && !((kept >> (i / size)) & 1u)) key[j] = 0;
+        if (GROUPS) {
+            if (lane + 32 * j < a.E && !((kept >> group) & 1u)) key[j] = 0;
+            group += a.step_groups;
+            in_group += a.step_rest;
+            if (in_group >= size) {
+                in_group -= size;
+                ++group;
+            }
+        }
     }
 
-    Choice r = {-1, certain};
-    F last = INFINITY;
-    // one round more than top_k, where the fp32 verdict wants the value behind the last choice
-    const int rounds = a.k + (sizeof(F) == 4 && !by_logit ? 1 : 0);
-    for (int c = 0; c < rounds; ++c) {
-        decltype(key_of(F())) top;
-        const int idx = take_best<PER>(key, lane, top);
-        if (idx < 0) break;  // no expert is left
-        if (sizeof(F) == 4 && !by_logit) {
-            const F now = (F)__uint_as_float((top & 0x80000000u) ? (uint32_t)top ^ 0x80000000u : ~(uint32_t)top);
-            if (c > 0 && !(last - now > 2 * bound)) r.certain = false;
-            last = now;
-        }
-        if (lane == c) r.id = idx;  // the round behind the last choice is not a choice
-    }
-    if (lane >= a.k) r.id = -1;
+    Choice r = {{-1, lane}, certain};
+    decide(a, key, lane, cand, bound, by_logit, r);
     return r;
 }
 
@@ -236,6 +318,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
 template <int PER, bool BF16, bool SIMPLE, bool GROUPS>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     extern __shared__ double s_values[];  // GROUPS: [warps][E + E / 32 + 1]
+    __shared__ uint2 s_cand[kRouteWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     if (t >= a.T) return;
@@ -245,33 +328,32 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
         const int i = lane + 32 * j;
         x[j] = i < a.E ? load_logit<BF16>(a.logits, t * a.ld + i) : -INFINITY;
     }
-    float m = x[0];
-#pragma unroll
-    for (int j = 1; j < PER; ++j) m = fmaxf(m, x[j]);
-    m = warp_max(m);
     const bool sigmoid = a.score == QZ_SCORE_SIGMOID;
+    float m = 0.0f;
+    if (!sigmoid && !(SIMPLE && a.renorm)) {  // what subtracts the row's maximum
+        m = x[0];
+#pragma unroll
+        for (int j = 1; j < PER; ++j) m = fmaxf(m, x[j]);
+        m = warp_max(m);
+    }
 
-    int id = -1;
+    uint2* const cand = s_cand[warp];
+    Pick pick = {-1, lane};
     if (SIMPLE) {
         uint32_t key[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) key[j] = key32(x[j]);
-        for (int c = 0; c < a.k; ++c) {
-            uint32_t top;
-            const int idx = take_best<PER>(key, lane, top);
-            if (idx < 0) break;  // no expert is left
-            if (lane == c) id = idx;
-        }
+        if (!pick_by_rank<PER, false>(key, a.k, lane, cand, pick, nullptr)) pick = pick_by_rounds<PER>(key, a.k, lane);
     } else {
         double* scratch = s_values + warp * (a.E + a.E / 32 + 1);
-        Choice r = choose<PER, float, GROUPS>(a, x, m, reinterpret_cast<float*>(scratch), lane);
-        if (!r.certain) r = choose<PER, double, GROUPS>(a, x, m, scratch, lane);
-        id = r.id;
+        Choice r = choose<PER, float, GROUPS>(a, x, m, reinterpret_cast<float*>(scratch), cand, lane);
+        if (!r.certain) r = choose<PER, double, GROUPS>(a, x, m, scratch, cand, lane);
+        pick = r.pick;
     }
 
-    // weights: lane j's choice again from memory (the row is in L1), with the accurate exponential
-    const bool live = id >= 0;
-    const float chosen = live ? load_logit<BF16>(a.logits, t * a.ld + id) : -INFINITY;
+    // weights: the lane's choice again from memory (the row is in L1), with the accurate exponential
+    const bool live = pick.id >= 0 && pick.at < a.k;
+    const float chosen = live ? load_logit<BF16>(a.logits, t * a.ld + pick.id) : -INFINITY;
     const float top = warp_max(chosen);
     float w = 0.0f;
     if (sigmoid && !(a.renorm && top < -20.0f)) {
@@ -291,9 +373,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
         const float total = warp_sum(part);
         w = live ? expf(chosen - m) / total : 0.0f;
     }
-    if (lane < a.k) {
-        a.ids[t * a.k + lane] = id;
-        a.weights[t * a.k + lane] = w * a.scale;
+    if (pick.at < a.k) {
+        a.ids[t * a.k + pick.at] = pick.id;
+        a.weights[t * a.k + pick.at] = w * a.scale;
     }
 }
 
@@ -592,8 +674,9 @@ static cudaError_t route_sized(const RouteArgs& a, cudaStream_t s) {
 
 cudaError_t launch_route(const void* logits, int type, int64_t T, int E, int64_t ld, const float* bias,
                          const qz_router& r, int32_t* ids, float* weights, cudaStream_t s) {
-    const RouteArgs a = {logits,       bias,          T,             ld,      E,  r.top_k, r.score, r.n_groups,
-                         r.top_groups, r.renormalize, r.scale, ids, weights};
+    const int size = E / r.n_groups;
+    const RouteArgs a = {logits,        bias,          T,         ld,        E,       r.top_k, r.score, r.n_groups,
+                         r.top_groups, r.renormalize, 32 / size, 32 % size, r.scale, ids,     weights};
     return type == QZ_TYPE_BF16 ? route_sized<true>(a, s) : route_sized<false>(a, s);
 }
 
