@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from dataclasses import dataclass
 from typing import Iterable, NamedTuple, Optional, Sequence
@@ -127,6 +128,10 @@ class _Product(ctypes.Structure):
                 ("q", ctypes.c_void_p), ("sf", ctypes.c_void_p)]
 
 
+# struct qz_product as bytes: packing them is several times faster than filling the ctypes mirror above
+_PRODUCT = struct.Struct("=4i4q12Q2q3QqQqQq2Q")
+
+
 class _WeightGrad(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int), ("n_experts", ctypes.c_int), ("out_type", ctypes.c_int),
                 ("accumulate", ctypes.c_int), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("slots", ctypes.c_int64),
@@ -143,6 +148,7 @@ class _Opts(ctypes.Structure):
 
 assert ctypes.sizeof(_Expert) == 56 and ctypes.sizeof(_SfPair) == 32 and ctypes.sizeof(_DqExpert) == 56
 assert ctypes.sizeof(_FusedSplit) == 96 and ctypes.sizeof(IpcHandle) == 88
+assert ctypes.sizeof(_Product) == _PRODUCT.size
 
 _lock = threading.Lock()
 _lib = None
@@ -660,9 +666,12 @@ def _scratch(nbytes: int, like: torch.Tensor, stream):
 
 
 def _parts(x, name: str):
-    if not isinstance(x, (tuple, list)) or len(x) not in (2, 3):
+    n = len(x) if isinstance(x, (tuple, list)) else 0
+    if n == 3:
+        return x
+    if n != 2:
         raise ValueError(f"{name} must be (payload, scales) or (payload, scales, amax)")
-    return x[0], x[1], (x[2] if len(x) == 3 else None)
+    return x[0], x[1], None
 
 
 def _router(top_k, score, n_groups, top_groups, renormalize, scale):
@@ -695,10 +704,14 @@ def route_experts(logits: torch.Tensor, top_k: int, *, score: int = SCORE_SOFTMA
     _require(top_k >= 1, "top_k must be at least 1")
     if ids is None:
         ids = logits.new_empty((T, top_k), dtype=torch.int32)
+        i = ids.data_ptr()
+    else:
+        i = _tensor(ids, "ids", torch.int32, dev, (T, top_k))
     if weights is None:
         weights = logits.new_empty((T, top_k), dtype=torch.float32)
-    i = _tensor(ids, "ids", torch.int32, dev, (T, top_k))
-    w = _tensor(weights, "weights", torch.float32, dev, (T, top_k))
+        w = weights.data_ptr()
+    else:
+        w = _tensor(weights, "weights", torch.float32, dev, (T, top_k))
     _check(load().qz_route_experts(x, kind, T, E, ld, b,
                                    _router(top_k, score, n_groups, n_groups if top_groups is None else top_groups,
                                            renormalize, scale), i, w, _raw_stream(stream, dev)), "qz_route_experts")
@@ -720,7 +733,9 @@ def route_experts_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
     g = _tensor(dweights, "dweights", torch.float32, dev, (T, k))
     if dlogits is None:
         dlogits = logits.new_empty((T, E))
-    d, ldd = _matrix(dlogits, "dlogits", logits.dtype, dev, (T, E))
+        d, ldd = dlogits.data_ptr(), E
+    else:
+        d, ldd = _matrix(dlogits, "dlogits", logits.dtype, dev, (T, E))
     _check(load().qz_route_experts_grad(x, kind, T, E, ld, _router(k, score, 1, 1, renormalize, scale), i, g, d, ldd,
                                         _raw_stream(stream, dev)), "qz_route_experts_grad")
     return dlogits
@@ -751,22 +766,28 @@ def plan_experts(ids: torch.Tensor, n_experts: int, *, align: int = 1, plan: Opt
     dev = ids.get_device()
     i = _tensor(ids, "ids", torch.int32, dev)
     lib = load()
-    n = lib.qz_plan_slots(T, k, int(n_experts), int(align))
-    need = lib.qz_plan_bytes(T, k, int(n_experts))
+    n = lib.qz_plan_slots(T, k, n_experts, align)
+    need = lib.qz_plan_bytes(T, k, n_experts)
     if plan is None:
         _require(n_experts >= 1, "n_experts must be at least 1")
-        offsets, counts, rows, slots = ids.new_empty(2 * n_experts + 1 + n + T * k).split(
-            (n_experts + 1, n_experts, n, T * k))
+        buf = ids.new_empty(2 * n_experts + 1 + n + T * k)
+        offsets, counts, rows, slots = buf.split((n_experts + 1, n_experts, n, T * k))
         plan = ExpertPlan(offsets, counts, rows, slots.view(T, k))
-    if workspace is None:
+        at = buf.data_ptr()
+        parts = (at, at + 4 * (n_experts + 1), at + 4 * (2 * n_experts + 1), at + 4 * (2 * n_experts + 1 + n))
+    else:
+        parts = (_tensor(plan.offsets, "offsets", torch.int32, dev, (n_experts + 1,)),
+                 _tensor(plan.counts, "counts", torch.int32, dev, (n_experts,)),
+                 _tensor(plan.rows, "rows", torch.int32, dev, (n,)),
+                 _tensor(plan.slots, "slots", torch.int32, dev, (T, k)))
+    ws = 0
+    if workspace is not None:
+        ws = _tensor(workspace, "workspace", torch.uint8, dev)
+    elif need:
         workspace = _scratch(need, ids, stream)
-    ws = 0 if workspace is None else _tensor(workspace, "workspace", torch.uint8, dev)
-    _check(lib.qz_plan_experts(i, T, k, int(n_experts), int(align),
-                               _tensor(plan.offsets, "offsets", torch.int32, dev, (n_experts + 1,)),
-                               _tensor(plan.counts, "counts", torch.int32, dev, (n_experts,)),
-                               _tensor(plan.rows, "rows", torch.int32, dev, (n,)),
-                               _tensor(plan.slots, "slots", torch.int32, dev, (T, k)), ws,
-                               0 if workspace is None else workspace.numel(), _raw_stream(stream, dev)), "qz_plan_experts")
+        ws = workspace.data_ptr()
+    _check(lib.qz_plan_experts(i, T, k, n_experts, align, *parts, ws, 0 if workspace is None else workspace.numel(),
+                               _raw_stream(stream, dev)), "qz_plan_experts")
     return plan
 
 
@@ -774,6 +795,23 @@ def _expert_lists(offsets, counts, n_experts: int, dev: int):
     """Addresses of offsets ([n_experts] or [n_experts + 1]) and counts."""
     _require(offsets.dim() == 1 and offsets.numel() in (n_experts, n_experts + 1), "offsets must be [n_experts + 1]")
     return _tensor(offsets, "offsets", torch.int32, dev), _tensor(counts, "counts", torch.int32, dev, (n_experts,))
+
+
+def _stacked(part, name: str, fmt: int, E: int, N: int, K: int, region: int, dev: int):
+    """(payload, scales, amax, payload stride, scale stride) of stacked expert weights."""
+    q, sf, amax = part
+    if q.dim() != 3 or q.shape[0] != E or q.shape[1] != N:
+        raise ValueError(f"{name} must be [E, N, K]")
+    apart, row, one = q.stride()
+    cols = q.shape[2]
+    if one != 1 or (N > 1 and row != cols):
+        raise ValueError(f"{name}: an expert's rows must be dense")
+    if (sf.dim() != 2 or sf.shape[0] != E or sf.dtype is not torch.uint8 or sf.stride(1) != 1 or sf.shape[1] < region
+            or sf.get_device() != dev):
+        raise ValueError(f"{name}: scales must be [E, region] bytes on the weights' device")
+    return (_codes(q, name, K, fmt, dev), sf.data_ptr(),
+            _tensor(amax, "a weight's amax", torch.float32, dev, (E,)) if fmt == FMT_NVFP4 else 0,
+            apart if E > 1 else N * cols, sf.stride(0) if E > 1 else (sf.shape[1] + 15) // 16 * 16)
 
 
 def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, out: torch.Tensor, *, rows=None,
@@ -794,62 +832,55 @@ def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, 
     uses a workspace (allocated unless given) to put them in order first."""
     xq, xsf, xa = _parts(x, "x")
     wq, wsf, wa = _parts(w, "w")
-    _require(xq.dim() == 2 and wq.dim() == 3 and out.dim() == 2, "x must be [R, K], w [E, N, K], out [slots, N]")
-    _require(fmt in (FMT_MXFP8, FMT_NVFP4), "fmt must be FMT_MXFP8 or FMT_NVFP4")
+    if xq.dim() != 2 or wq.dim() != 3 or out.dim() != 2:
+        raise ValueError("x must be [R, K], w [E, N, K], out [slots, N]")
+    if fmt != FMT_MXFP8 and fmt != FMT_NVFP4:
+        raise ValueError("fmt must be FMT_MXFP8 or FMT_NVFP4")
+    if not xq.is_contiguous():
+        raise ValueError("x must be contiguous")
     fp4 = fmt == FMT_NVFP4
     dev = out.get_device()
     E, N, _ = wq.shape
-    K = xq.shape[1] * (2 if fp4 else 1)
-    R, S = xq.shape[0], out.shape[0]
-    _require(xq.is_contiguous(), "x must be contiguous")
+    R, K = xq.shape
+    S = out.shape[0]
+    if fp4:
+        K *= 2
     kv = K // (16 if fp4 else 32)
 
-    def weight(part, name):
-        pq, psf, pa = part
-        if pq.dim() != 3 or pq.shape[0] != E or pq.shape[1] != N:
-            raise ValueError(f"{name} must be [E, N, K]")
-        apart, row, one = pq.stride()
-        if one != 1 or (N > 1 and row != pq.shape[2]):
-            raise ValueError(f"{name}: an expert's rows must be dense")
-        if (psf.dim() != 2 or psf.shape[0] != E or psf.dtype is not torch.uint8 or psf.stride(1) != 1
-                or psf.shape[1] < region or psf.get_device() != dev):
-            raise ValueError(f"{name}: scales must be [E, region] bytes on the current CUDA device")
-        return (_codes(pq, name, K, fmt, dev), psf.data_ptr(),
-                _tensor(pa, "a weight's amax", torch.float32, dev, (E,)) if fp4 else 0,
-                apart if E > 1 else N * pq.shape[2], psf.stride(0) if E > 1 else (psf.shape[1] + 15) // 16 * 16)
-
     region = load().qz_sf_bytes(N, K, fmt, SF_SWIZZLED)
-
-    wp = weight((wq, wsf, wa), "w")
+    wp = _stacked((wq, wsf, wa), "w", fmt, E, N, K, region, dev)
     upp = (0, 0, 0)
     if up is not None:
-        upp = weight(_parts(up, "up"), "up")
-        _require(upp[3:] == wp[3:], "w and up must have the same strides")
+        upp = _stacked(_parts(up, "up"), "up", fmt, E, N, K, region, dev)
+        if upp[3:] != wp[3:]:
+            raise ValueError("w and up must have the same strides")
     offs, cnts = _expert_lists(offsets, counts, E, dev)
     o, ldo = _matrix(out, "out", torch.bfloat16, dev, (S, N))
     r, ldr = _matrix(residual, "residual", torch.bfloat16, dev, (S, N), optional=True)
     z, ldz = _matrix(pre, "pre", torch.bfloat16, dev, (S, N if up is None else 2 * N), optional=True)
-    _require((q is None) == (sf is None), "q and sf come together")
+    if (q is None) != (sf is None):
+        raise ValueError("q and sf come together")
+    qp = sfp = amax = 0
     if q is not None:
-        _require(q.is_contiguous() and q.shape == (S, N), "q must be a contiguous [slots, N]")
-        _require(sf.is_contiguous() and sf.dtype == torch.uint8 and sf.shape == (S, N // 32), "sf must be [slots, N/32] bytes")
-        _require(sf.get_device() == dev, "sf must be on the current CUDA device")
-    amax = 0
+        if not q.is_contiguous() or q.shape != (S, N):
+            raise ValueError("q must be a contiguous [slots, N]")
+        qp, sfp = _codes(q, "q", N, FMT_MXFP8, dev), _tensor(sf, "sf", torch.uint8, dev, (S, N // 32))
     if fp4:
-        _require(xa is not None and xa.numel() in (1, R), "x's amax must be [R] or [1]")
+        if xa is None or xa.numel() not in (1, R):
+            raise ValueError("x's amax must be [R] or [1]")
         amax = _tensor(xa, "x's amax", torch.float32, dev)
-    p = _Product(fmt, int(activation), E, 1 if fp4 and xa.numel() == R and R > 1 else 0, N, K, R, S,
+    p = _PRODUCT.pack(fmt, activation, E, 1 if fp4 and xa.numel() == R and R > 1 else 0, N, K, R, S,
                  _codes(xq, "x", K, fmt, dev), _tensor(xsf, "x's scales", torch.uint8, dev, (R, kv)), amax,
                  _tensor(rows, "rows", torch.int32, dev, (S,), optional=True), offs, cnts, wp[0], wp[1], wp[2], upp[0],
                  upp[1], upp[2], wp[3], wp[4], _tensor(bias, "bias", torch.bfloat16, dev, (E, N), optional=True),
                  _tensor(up_bias, "up_bias", torch.bfloat16, dev, (E, N), optional=True), r, ldr, o, ldo, z, ldz,
-                 0 if q is None else _codes(q, "q", N, FMT_MXFP8, dev), 0 if sf is None else sf.data_ptr())
-    lib, ref, s = load(), ctypes.byref(p), _raw_stream(stream, dev)
+                 qp, sfp)
+    lib, s = load(), _raw_stream(stream, dev)
     if workspace is not None:
         _tensor(workspace, "workspace", torch.uint8, dev)
     elif rows is not None:
-        workspace = _scratch(lib.qz_product_bytes(ref), out, stream)
-    _check(lib.qz_expert_product(ref, s, _opts(err, max_ctas, workspace)), "qz_expert_product")
+        workspace = _scratch(lib.qz_product_bytes(p), out, stream)
+    _check(lib.qz_expert_product(p, s, _opts(err, max_ctas, workspace)), "qz_expert_product")
     return out
 
 

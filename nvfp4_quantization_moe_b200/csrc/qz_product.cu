@@ -37,6 +37,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/qz.h"
 #include "../../include/qz_quant.cuh"
 #include "qz_act.cuh"
@@ -415,7 +417,11 @@ __device__ __forceinline__ void scale_row(float g, bool exists, float (&v)[N]) {
 // the kernel
 // ---------------------------------------------------------------------------
 
-enum Kind { kPlain, kGated, kWeightGrad };  // the product, its gated form (args.p), the weight gradient (args.g)
+// The product without and with an epilogue beyond its output (bias, activation,
+// residual, pre-activations), its gated form (args.p), and the weight gradient
+// (args.g).  The bare form is a kernel of its own because the others' pointers
+// cost it registers and their code instruction cache.
+enum Kind { kBare, kPlain, kGated, kWeightGrad };
 
 union Args {
     ProductArgs p;
@@ -745,6 +751,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                             for (int j = 0; j < 8; ++j) w[8 * b + j] = bf16x2_of(z[2 * j], z[2 * j + 1]);
                         }
+                    } else if (KIND == kBare) {
+                        scale_row<FMT>(scale0, exists, x);
+                        to_words(x, w);
                     } else {
                         scale_row<FMT>(scale0, exists, x);
                         if (p.bias) add_row(p.bias + t.e * p.n + at, cols, x);
@@ -904,8 +913,16 @@ static cudaError_t launch_experts(const Args& a, const CUtensorMap& ma, const CU
     // asked for at its largest: the attribute is one value per device
     constexpr size_t most = fixed + list_bytes(QZ_MAX_ROUTE_EXPERTS);
     static_assert(most <= 232448, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(experts_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    static std::atomic<uint64_t> set{0};  // devices that have it
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!(set.load(std::memory_order_acquire) & bit) || bit == 0) {
+        e = cudaFuncSetAttribute(experts_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_release);
+    }
     experts_kernel<FMT, KIND><<<grid, kProductThreads, fixed + list_bytes(n_experts), s>>>(a, ma, ml, mb, mu);
     return cudaGetLastError();
 }
@@ -969,8 +986,9 @@ cudaError_t launch_product(const qz_product& call, int ctas, cudaStream_t s, uns
     const int64_t row_bytes = fp4 ? p.k / 2 : p.k;
     const int64_t x_rows = p.x_rows > 0 ? p.x_rows : 1;
     CUtensorMap ma, ml, mb, mu;
-    if (!make_map(&ma, x, row_bytes, x_rows, 0, 0, 128) || !make_map(&ml, x, row_bytes, x_rows, 0, 0, q.gather ? 1 : 32))
-        return cudaErrorInvalidValue;
+    if (!make_map(&ml, x, row_bytes, x_rows, 0, 0, q.gather ? 1 : 32)) return cudaErrorInvalidValue;
+    ma = ml;  // of tall tiles without an index only
+    if (!q.gather && p.slots > 96 && !make_map(&ma, x, row_bytes, x_rows, 0, 0, 128)) return cudaErrorInvalidValue;
     if (!make_map(&mb, p.w_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
     mu = mb;
     if (q.gated && !make_map(&mu, p.up_q, row_bytes, p.n, p.n_experts, p.w_stride, 128)) return cudaErrorInvalidValue;
@@ -981,6 +999,9 @@ cudaError_t launch_product(const qz_product& call, int ctas, cudaStream_t s, uns
     if (q.gated)
         return fp4 ? launch_experts<QZ_FMT_NVFP4, kGated>(a, ma, ml, mb, mu, p.n_experts, grid, s)
                    : launch_experts<QZ_FMT_MXFP8, kGated>(a, ma, ml, mb, mu, p.n_experts, grid, s);
+    if (!p.bias && !p.residual && !p.pre && p.activation == QZ_ACT_NONE)
+        return fp4 ? launch_experts<QZ_FMT_NVFP4, kBare>(a, ma, ml, mb, mu, p.n_experts, grid, s)
+                   : launch_experts<QZ_FMT_MXFP8, kBare>(a, ma, ml, mb, mu, p.n_experts, grid, s);
     return fp4 ? launch_experts<QZ_FMT_NVFP4, kPlain>(a, ma, ml, mb, mu, p.n_experts, grid, s)
                : launch_experts<QZ_FMT_MXFP8, kPlain>(a, ma, ml, mb, mu, p.n_experts, grid, s);
 }
