@@ -15,8 +15,8 @@
  * Conventions that hold for every entry point:
  *  - Pointers whose name starts with d_, and every pointer inside a table, are
  *    DEVICE pointers.  The caller owns every buffer; the library allocates
- *    nothing.  Its only state is a per-device cache of launch limits and the
- *    static device scratch of qz_quantize_grouped_nvfp4_compute_noalloc (with
+ *    nothing.  Its only state is a per-device cache of launch limits (for the
+ *    expert products: of the shared memory asked for) and the static device scratch of qz_quantize_grouped_nvfp4_compute_noalloc (with
  *    that array's device address, looked up once per device).
  *  - `stream` is a cudaStream_t (NULL: the legacy default stream).  Every call
  *    is asynchronous on that stream; inputs must be ready on it.  No call
@@ -104,7 +104,8 @@ typedef enum qz_nvfp4_scale_mode {
 #define QZ_DERR_TIMEOUT 0x10u  /* a bounded wait of the single-launch computed-amax path (quantize
                                   warps waiting for an expert's amax, or the copy, amax and
                                   publishing warps waiting on one another) exceeded
-                                  qz_launch_opts.wait_limit_ns; the launch stopped early and some
+                                  qz_launch_opts.wait_limit_ns, or one of an expert product's warps
+                                  waited a second for another; the launch stopped early and some
                                   outputs are unwritten (no such wait is expected to expire) */
 #define QZ_DERR_CUT 0x20u      /* qz_split_fused_experts: the cut falls inside a scale block
                                   (FP8_BLOCK128: cut not a multiple of 128 and not the end) */
@@ -718,7 +719,7 @@ qz_status qz_expert_weight_grad(const qz_weight_grad *p, void *stream, const qz_
  *   dbias[e] = the sum of its rows' dz (du) before they are rounded, fp32, in a fixed order
  *   d_dout: bf16 [slots, n];  d_pre, d_dpre: bf16 [slots, n] (gated: [slots, 2n], z then u),
  *   row strides ld_* (multiples of 8, pointers 16-byte aligned);  d_dbias: float [n_experts, n]
- *   (gated [n_experts, 2n]) or NULL;  d_offsets: int32 [n_experts + 1], ascending
+ *   (gated [n_experts, 2n]) or NULL;  d_offsets: int32 [n_experts], ascending from 0
  * Rows of d_dpre that are no live slot are written as zeros.  d_dbias needs
  * opts->d_workspace, qz_activation_grad_bytes(slots, n, gated, n_experts) bytes,
  * 16-byte aligned, not shared with a call that may overlap.

@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint16_t* __
 // zeroes the unused slots of its share of the slots.
 
 constexpr int kDispatchThreads = 256;
+constexpr int64_t kZeroSlots = 8, kZeroCtas = 1184;  // slots a CTA looks at, CTAs that is worth (8 per SM)
 
 template <bool DOTS>
 __global__ void __launch_bounds__(kDispatchThreads)
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kDispatchThreads)
         }
     }
     const int64_t share = (n_slots + gridDim.x - 1) / gridDim.x;
-    const int64_t end = min(n_slots, (t + 1) * share);
+    const int64_t end = min(n_slots, (t + 1) * share);  // for CTAs past the last token too
     for (int64_t s = t * share; s < end; ++s) {
         if (__ldg(rows + s) >= 0) continue;
         for (int64_t c = 8 * threadIdx.x; c < H; c += 8 * kDispatchThreads)
@@ -177,6 +178,7 @@ struct GradPieces {
     const int32_t *offsets, *counts;
     int64_t slots;
     int n_experts, piece;
+    int64_t most;  // pieces that the workspace holds: all there can be, unless the ranges overlap
 };
 
 // An expert's range: first slot, live slots, end (the next expert's start; the buffer's end for the last).
@@ -190,7 +192,7 @@ __device__ __forceinline__ SlotRange slot_range(const GradPieces& a, int e) {
     r.begin = __ldg(a.offsets + e);
     r.count = __ldg(a.counts + e);
     r.next = e + 1 < a.n_experts ? (int64_t)__ldg(a.offsets + e + 1) : a.slots;
-    r.bad = r.begin < 0 || r.count < 0 || r.begin + r.count > r.next || r.next > a.slots;
+    r.bad = (e == 0 ? r.begin != 0 : r.begin < 0) || r.count < 0 || r.begin + r.count > r.next || r.next > a.slots;
     return r;
 }
 
@@ -225,6 +227,10 @@ __global__ void __launch_bounds__(kGradWarps * 32, kGradCtas)
         const int64_t first = range.begin + (int64_t)(p - s_prefix[e]) * a.piece;
         const int64_t end = min(range.next, first + a.piece), live = min(end, range.begin + range.count);
         if (c >= n) continue;
+        if (p >= a.most) {  // ranges that overlap
+            if (d_err && lane == 0) atomicOr(d_err, QZ_DERR_SHAPE);
+            continue;
+        }
         float sz[8] = {0, 0, 0, 0, 0, 0, 0, 0}, su[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int64_t s0 = first; s0 < live; s0 += kRowsAhead) {
             uint4 vd[kRowsAhead], vz[kRowsAhead], vu[kRowsAhead];
@@ -308,6 +314,7 @@ __global__ void __launch_bounds__(kGradWarps * 32)
 #pragma unroll
     for (int w = 0; w < kGradWarps; ++w) before += s_before[w];
     const int pieces = (int)((range.count + a.piece - 1) / a.piece);  // with live rows
+    if (before + pieces > a.most) return;
     const int each = (pieces + kGradWarps - 1) / kGradWarps, end = min(pieces, (warp + 1) * each);
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < width) {
@@ -349,7 +356,11 @@ cudaError_t launch_combine(const uint16_t* y, int64_t ld_y, const int32_t* slots
 cudaError_t launch_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* slots, const int32_t* rows, int64_t T,
                             int k, int64_t n_slots, int64_t H, const float* weights, uint16_t* y, int64_t ld_y,
                             const uint16_t* other, int64_t ld_o, float* dots, cudaStream_t s) {
-    const unsigned grid = (unsigned)(T > 0 ? T : 1);  // T == 0: one CTA zeroes every slot
+    // a CTA per token, and enough of them for the unused slots when there are few tokens (16 tokens over
+    // 128 experts padded to 128: 16,000 rows of zeros)
+    const int64_t zeroing = (n_slots + kZeroSlots - 1) / kZeroSlots;
+    const int64_t most = zeroing < kZeroCtas ? zeroing : kZeroCtas;
+    const unsigned grid = (unsigned)(T > most ? T : most > 0 ? most : 1);
     if (other)
         dispatch_kernel<true><<<grid, kDispatchThreads, 0, s>>>(x, ld_x, slots, rows, T, k, n_slots, H, weights, y,
                                                                 ld_y, other, ld_o, dots);
@@ -365,9 +376,11 @@ static int grad_piece(int64_t slots) {
     return piece;
 }
 
+// Each expert's last piece may be short.
+static int64_t most_pieces(int64_t slots, int n_experts) { return slots / grad_piece(slots) + n_experts; }
+
 size_t act_grad_bytes(int64_t slots, int64_t n, bool gated, int n_experts) {
-    const int64_t pieces = slots / grad_piece(slots) + n_experts;  // each expert's last may be short
-    return (size_t)pieces * (size_t)(gated ? 2 * n : n) * sizeof(float);
+    return (size_t)most_pieces(slots, n_experts) * (size_t)(gated ? 2 * n : n) * sizeof(float);
 }
 
 cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* pre, int64_t ld_p, int64_t slots,
@@ -382,9 +395,8 @@ cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* 
         {act_grad_kernel<QZ_ACT_SILU, false>, act_grad_kernel<QZ_ACT_SILU, true>},
         {act_grad_kernel<QZ_ACT_GELU, false>, act_grad_kernel<QZ_ACT_GELU, true>},
     };
-    const GradPieces a = {offsets, counts, slots, n_experts, grad_piece(slots)};
-    const int64_t most = (slots / a.piece + n_experts) * ((n + kGradCols - 1) / kGradCols);
-    const int64_t ctas = (most + kGradWarps - 1) / kGradWarps;
+    const GradPieces a = {offsets, counts, slots, n_experts, grad_piece(slots), most_pieces(slots, n_experts)};
+    const int64_t ctas = (a.most * ((n + kGradCols - 1) / kGradCols) + kGradWarps - 1) / kGradWarps;
     const unsigned grid = (unsigned)(ctas < (int64_t)sms * kGradCtas ? ctas : (int64_t)sms * kGradCtas);
     const size_t smem = (size_t)(n_experts + 1) * sizeof(int);
     kernels[act][gated]<<<grid, kGradWarps * 32, smem, s>>>(a, dout, ld_d, pre, ld_p, n, dpre, ld_q,

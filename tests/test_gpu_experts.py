@@ -181,6 +181,58 @@ def test_product_of_fused_weights(fmt):
     assert torch.equal(out, want) and out.abs().sum() > 0
 
 
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("K", [96, 256])
+def test_product_of_a_large_gather(fmt, K):
+    """From 2048 slots on the rows are copied into slot order first: the same bits as gathering them in the product."""
+    g = ref.gen(K)
+    E, N, R, S = 3, 72, 300, 2500
+    x = qz.quantize_tokens(ref.randn(g, R, K).to(torch.bfloat16).cuda(), fmt)
+    w = stacked(g, E, N, K, fmt)
+    rows = torch.randint(0, R, (S,), generator=g, dtype=torch.int32)
+    rows[5], rows[2400] = -3, R + 7   # no row of x: zeros
+    rows = rows.cuda()
+    offsets = torch.tensor([0, 1000, 1010, S], dtype=torch.int32).cuda()
+    counts = torch.tensor([990, 10, 1450], dtype=torch.int32).cuda()
+    copied, gathered = (torch.full((S, N), 3.0, dtype=torch.bfloat16).cuda() for _ in range(2))
+    qz.expert_product(fmt, x, w, offsets, counts, copied, rows=rows)
+    half = 1200  # fewer slots at a time: no copy
+    for lo, hi in ((0, half), (half, S)):
+        o = (offsets[:E].long().clamp(lo, hi) - lo).to(torch.int32)
+        end = (offsets[:E].long() + counts.long()).clamp(lo, hi) - lo
+        qz.expert_product(fmt, x, w, o, (end - o.long()).to(torch.int32), gathered[lo:hi], rows=rows[lo:hi].contiguous())
+    assert torch.equal(copied, gathered)
+    assert (copied[5] == 0).all() and (copied[2400] == 0).all() and (copied[990:1000] == 3.0).all()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_product_of_the_most_experts(fmt):
+    counts = [0] * qz.MAX_ROUTE_EXPERTS
+    for e, c in ((0, 1), (500, 3), (1000, 130), (1023, 2)):
+        counts[e] = c
+    run_product(fmt, counts, 16, 64, q=False)
+
+
+def test_product_past_32_bits():
+    """Rows whose element offsets pass 2^31 in out, pre, q and residual."""
+    g = ref.gen(1)
+    N, K, S, ld = 64, 64, 140000, 16384
+    x = qz.quantize_tokens(ref.randn(g, 8, K).to(torch.bfloat16).cuda(), MX)
+    w = stacked(g, 2, N, K, MX)
+    big = torch.empty(S, ld, dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros(S, dtype=torch.int32).cuda()
+    rows[-8:] = torch.arange(8, dtype=torch.int32).cuda()
+    residual = ref.randn(g, 8, N).to(torch.bfloat16).cuda()
+    big[-8:, N:2 * N] = residual
+    offsets = torch.tensor([S - 8, S - 3, S], dtype=torch.int32).cuda()
+    counts = torch.tensor([5, 3], dtype=torch.int32).cuda()
+    qz.expert_product(MX, x, w, offsets, counts, big[:, :N], rows=rows, residual=big[:, N:2 * N], pre=big[:, 2 * N:3 * N])
+    small = [torch.zeros(8, N, dtype=torch.bfloat16).cuda() for _ in range(2)]
+    qz.expert_product(MX, x, w, offsets - (S - 8), counts, small[0], residual=residual, pre=small[1])
+    assert torch.equal(big[-8:, :N], small[0]) and torch.equal(big[-8:, 2 * N:3 * N], small[1])
+    assert small[0].abs().sum() > 0
+
+
 def test_product_skips_bad_experts():
     g = ref.gen(6)
     x = qz.quantize_tokens(ref.randn(g, 40, 64).to(torch.bfloat16).cuda(), MX)
@@ -321,6 +373,26 @@ def test_activation_grad(gated, act, counts, N):
     assert torch.equal(first, dbias)
 
 
+@pytest.mark.parametrize("offsets,counts,bad", [([0, 100, 50], [100, 0, 60], 1), ([3, 10, 20], [7, 10, 5], 0),
+                                                ([0, 40, 80], [30, -1, 5], 1), ([0, 60, 30], [40, 5, 110], 2),
+                                                ([0, 0, 0], [0, 0, 129], 2)])
+def test_activation_grad_skips_bad_experts(offsets, counts, bad):
+    """Ranges that are not ascending, do not start at 0 or pass the end: reported, and nothing is written out of place."""
+    S, N = 128, 16
+    guard = torch.full((S + 64, N), 7.5, dtype=torch.bfloat16).cuda()
+    sums = torch.full((4, N), 7.5).cuda()
+    err = torch.zeros(1, dtype=torch.int32).cuda()
+    one = torch.ones(S, N, dtype=torch.bfloat16).cuda()
+    need = qz.load().qz_activation_grad_bytes(S, N, 0, 3)
+    work = torch.full((need + 256,), 0x5A, dtype=torch.uint8).cuda()
+    qz.expert_activation_grad(one, one, torch.tensor(offsets, dtype=torch.int32).cuda(),
+                              torch.tensor(counts, dtype=torch.int32).cuda(), guard[:S], activation=qz.ACT_RELU,
+                              dbias=sums[:3], workspace=work[:need], err=err)
+    assert err.item() == qz.DERR_SHAPE
+    assert (guard[S:] == 7.5).all() and (sums[3] == 7.5).all() and (work[need:] == 0x5A).all()
+    assert (sums[bad] == 7.5).all()
+
+
 @pytest.mark.parametrize("act", [qz.ACT_SILU, qz.ACT_GELU])
 def test_activation_grad_against_differences(act):
     """dpre against central differences of the forward epilogue: x = 1 row of the identity, so pre = bias."""
@@ -381,6 +453,17 @@ def test_dispatch_and_combine(T, E, k, H, align, weighted):
         prod = x[:, :H].double().unsqueeze(1) * y[at].double() * live.unsqueeze(-1)
         # 8 products in a chain, 5 + 3 levels of a tree and ceil(H / 2048) passes
         ref.close(dots, prod.sum(-1), (20 + H // 2048) * ref.HALF_F32 * prod.abs().sum(-1) + 1e-38, "dots")
+
+
+def test_dispatch_of_few_tokens_zeroes_many_slots():
+    g = ref.gen(2)
+    ids = torch.randint(0, 128, (3, 8), generator=g, dtype=torch.int32).cuda()
+    plan = qz.plan_experts(ids, 128, align=128)
+    x = ref.randn(g, 3, 264).to(torch.bfloat16).cuda()
+    y = torch.full((plan.rows.numel(), 264), 7.5, dtype=torch.bfloat16).cuda()
+    qz.dispatch_experts(x, plan.slots, plan.rows, y)
+    live = plan.rows >= 0
+    assert int(live.sum()) == 24 and (y[~live] == 0).all() and torch.equal(y[live], x[plan.rows[live].long()])
 
 
 def test_combine_in_place_of_the_residual_and_empty_calls():

@@ -91,13 +91,13 @@ def test_plan_sizes_and_refusals(lib):
         assert plan(**kw) == ALIGN, kw
 
 
-def product(lib, **kw):
+def product(lib, opts=None, **kw):
     base = dict(fmt=0, activation=0, n_experts=4, x_amax_per_row=0, n=64, k=128, x_rows=10, slots=20, x_q=A, x_sf=A,
                 x_amax=None, d_rows=A, d_offsets=A, d_counts=A, w_q=A, w_sf=A, w_amax=None, up_q=None, up_sf=None,
                 up_amax=None, w_stride=64 * 128, w_sf_stride=512, bias=None, up_bias=None, residual=None, ld_residual=0,
                 out=A, ld_out=64, pre=None, ld_pre=0, q=None, sf=None)
     base.update(kw)
-    return lib.qz_expert_product(ctypes.byref(qz.binding._Product(**base)), None, None)
+    return lib.qz_expert_product(ctypes.byref(qz.binding._Product(**base)), None, ctypes.byref(opts) if opts else None)
 
 
 def test_product_refusals(lib):
@@ -115,6 +115,17 @@ def test_product_refusals(lib):
                dict(pre=A + 8, ld_pre=64), dict(q=A + 8, sf=A), dict(bias=A + 2), dict(x_sf=A + 2), dict(d_rows=A + 2),
                dict(d_offsets=A + 2), dict(d_counts=A + 1), dict(up_q=A + 8, up_sf=A), dict(up_q=A, up_sf=A + 8)):
         assert product(lib, **kw) == ALIGN, kw
+    big = dict(slots=4096, x_rows=100)
+    sized = qz.binding._Product(fmt=0, k=128, slots=4096, x_rows=100, d_rows=A)
+    need = lib.qz_product_bytes(ctypes.byref(sized))
+    assert need >= 4096 * (128 + 4)
+    for field, value in (("slots", 100), ("d_rows", None), ("x_rows", 0), ("k", 48), ("fmt", 2), ("slots", -1)):
+        other = qz.binding._Product.from_buffer_copy(sized)
+        setattr(other, field, value)
+        assert lib.qz_product_bytes(ctypes.byref(other)) == 0, field
+    assert lib.qz_product_bytes(None) == 0
+    assert product(lib, opts=qz.binding._Opts(None, 0, P(A), need - 1), **big) == BAD
+    assert product(lib, opts=qz.binding._Opts(None, 0, P(A + 8), need), **big) == ALIGN
     assert product(lib, slots=0) == OK
     assert lib.qz_expert_product(None, None, None) == BAD
 
@@ -137,15 +148,22 @@ def test_weight_grad_refusals(lib):
 
 
 def test_slot_refusals(lib):
-    def act(ldd=64, ldp=64, slots=8, n=64, a=2, gated=0, off=A, cnt=A, E=3, dpre=A, ldq=64, dbias=None, dout=A, pre=A):
+    def act(ldd=64, ldp=64, slots=8, n=64, a=2, gated=0, off=A, cnt=A, E=3, dpre=A, ldq=64, dbias=None, dout=A, pre=A, opts=None):
         return lib.qz_expert_activation_grad(P(dout), ldd, P(pre), ldp, slots, n, a, gated, P(off), P(cnt), E, P(dpre), ldq,
-                                             P(dbias), None, None)
+                                             P(dbias), None, ctypes.byref(opts) if opts else None)
 
     for kw in (dict(n=4), dict(n=60), dict(a=4), dict(E=0), dict(E=1025), dict(slots=-1), dict(ldd=32), dict(ldp=60),
                dict(ldq=68), dict(gated=1), dict(off=None), dict(cnt=None), dict(dout=None), dict(pre=None), dict(dpre=None)):
         assert act(**kw) == BAD, kw
     for kw in (dict(dout=A + 8), dict(pre=A + 2), dict(dpre=A + 8), dict(dbias=A + 2), dict(off=A + 2)):
         assert act(**kw) == ALIGN, kw
+    assert act(dbias=A) == BAD  # without its workspace
+    need = lib.qz_activation_grad_bytes(8, 64, 0, 3)
+    assert need >= 4 * 64 * 3 and lib.qz_activation_grad_bytes(8, 64, 1, 3) == 2 * need
+    for bad in ((-1, 64, 0, 3), (8, 60, 0, 3), (8, 64, 0, 0), (8, 64, 0, 1025)):
+        assert lib.qz_activation_grad_bytes(*bad) == 0
+    assert act(dbias=A, opts=qz.binding._Opts(None, 0, P(A), need - 1)) == BAD
+    assert act(dbias=A, opts=qz.binding._Opts(None, 0, P(A + 8), need)) == ALIGN
 
     def dispatch(x=A, ldx=64, slots=A, rows=A, T=4, k=2, S=8, H=64, w=None, y=A, ldy=64, o=None, ldo=0, dots=None):
         return lib.qz_dispatch_experts(P(x), ldx, P(slots), P(rows), T, k, S, H, P(w), P(y), ldy, P(o), ldo, P(dots), None)
