@@ -15,8 +15,10 @@
 // Without a bias or groups the key is the fp32 logit itself.  With them two
 // experts (or groups) may differ by less than an fp32 rounding of their scores:
 // the choice is first made in fp32, and if any two neighbours that decide it are
-// closer than the fp32 error bound, this token's is made again in binary64
-// (binary64 throughout took 81 us on 16384 tokens of 256 experts in 8 groups).
+// closer than the fp32 error bound, this token's is made again in binary64: of
+// the candidates alone for a sigmoid, of all experts for a softmax or close groups
+// (binary64 throughout took 81 us on 16384 tokens of 256 experts in 8 groups, and
+// all experts of each close token, a tail of 10 us).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -42,6 +44,9 @@ struct RouteArgs {
     float scale;
     int32_t* ids;
     float* weights;
+    // filled in by each warp: its token's row of logits, and their type
+    int64_t row;
+    bool bf16;
 };
 
 // A logit as the router reads it: NaN masks like -inf, +inf counts as FLT_MAX.
@@ -144,11 +149,13 @@ __device__ __forceinline__ Pick pick_by_rounds(K (&key)[PER], int k, int lane) {
     return r;
 }
 
-// The same by candidates (see the top of the file); with VERDICT the smallest
-// difference to the next value behind a chosen one goes to *gap.  false: more
-// than 32 candidates, nothing is decided.
+// The same by candidates (see the top of the file), `n` of them.  With VERDICT
+// every expert within `margin` of the bar is one too, and *gap gets the lane's
+// difference to the next value, if it is chosen.  false: more than 32
+// candidates, nothing is decided.
 template <int PER, bool VERDICT>
-__device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, int lane, uint2* cand, Pick& r, float* gap) {
+__device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, int lane, uint2* cand, Pick& r, int& n,
+                                             float margin, float* gap) {
     uint32_t left = key[0], bar = 1;
 #pragma unroll
     for (int j = 1; j < PER; ++j) left = max(left, key[j]);
@@ -158,7 +165,8 @@ __device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, 
         if (left == bar) left = 0;
     }
     if (rounds > 32 || bar == 0) bar = 1;  // fewer lanes than choices: every key above 0
-    int n = 0;
+    else if (VERDICT) bar = max(key32(unkey32(bar) - margin), 1u);
+    n = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const bool in = key[j] >= bar;
@@ -213,12 +221,36 @@ template <int PER, typename F>
 __device__ __forceinline__ void decide(const RouteArgs& a, uint32_t (&key)[PER], int lane, uint2* cand, F bound, bool by_logit,
                                        Choice& r) {
     float gap = INFINITY;
-    if (!pick_by_rank<PER, true>(key, a.k, lane, cand, r.pick, &gap)) {
+    int n;
+    const float margin = by_logit ? 0.0f : 2.0f * (float)bound;
+    if (!pick_by_rank<PER, true>(key, a.k, lane, cand, r.pick, n, margin, &gap)) {
         r.certain = r.certain && by_logit;
         if (r.certain) r.pick = pick_by_rounds<PER>(key, a.k, lane);
         return;
     }
-    if (!by_logit && !__all_sync(kFull, gap > 2.0f * (float)bound)) r.certain = false;
+    if (by_logit || __all_sync(kFull, gap > margin)) return;
+    if (a.score != QZ_SCORE_SIGMOID) {
+        r.certain = false;
+        return;
+    }
+    // a sigmoid needs no sum over the experts: the candidates' binary64 values, one per lane
+    unsigned long long* const value = reinterpret_cast<unsigned long long*>(cand + 32);
+    int id = -1;
+    unsigned long long mine = 0;
+    if (lane < n) {
+        id = (int)cand[lane].y;
+        const double x = (double)(a.bf16 ? load_logit<true>(a.logits, a.row + id) : load_logit<false>(a.logits, a.row + id));
+        const double e = exp(-fabs(x));
+        mine = key64((x >= 0 ? 1.0 : e) / (1.0 + e) + (double)__ldg(a.bias + id));
+        value[lane] = mine;
+    }
+    __syncwarp();
+    int before = 0;
+    for (int i = 0; i < n; ++i) {
+        const unsigned long long other = value[i];
+        if (other > mine || (other == mine && (int)cand[i].y < id)) ++before;
+    }
+    if (lane < n) r.pick = {id, before};
 }
 
 // The choice by values of type F (float: with a verdict on its certainty).
@@ -281,14 +313,18 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
         const F mine = b2 > -INFINITY ? b1 + b2 : b1;
         const F value = __shfl_sync(kFull, mine, lane < a.n_groups ? lane * share : 0);  // lane g: group g's
         int before = 0;
-        bool close = false;
         for (int h = 0; h < a.n_groups; ++h) {
             const F other = __shfl_sync(kFull, value, h);
             if (other > value || (other == value && h < lane)) ++before;
-            if (h != lane && other > -INFINITY && value > -INFINITY && fabs(other - value) <= 4 * bound) close = true;
         }
-        kept = __ballot_sync(kFull, lane < a.n_groups && before < a.top_groups);
-        if (sizeof(F) == 4) certain = !__any_sync(kFull, lane < a.n_groups && close);
+        const bool mine_kept = lane < a.n_groups && before < a.top_groups;
+        kept = __ballot_sync(kFull, mine_kept);
+        if (sizeof(F) == 4) {
+            // the least value kept against the largest that is not (0: every group with an expert is kept)
+            const uint32_t low = __reduce_min_sync(kFull, mine_kept ? key32((float)value) : 0xFFFFFFFFu);
+            const uint32_t high = __reduce_max_sync(kFull, lane < a.n_groups && !mine_kept ? key32((float)value) : 0u);
+            certain = high == 0 || unkey32(low) - unkey32(high) > 4.0f * (float)bound;
+        }
     }
     int group = 0, in_group = 0;  // of expert lane + 32 j, kept up without divisions
     if (GROUPS) {
@@ -314,14 +350,19 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
     return r;
 }
 
-// SIMPLE: neither a bias nor a group limit, the logits are the keys.
+// SIMPLE: neither a bias nor a group limit, the logits are the keys.  Ten CTAs
+// per SM (48 registers; the rare binary64 path spills some) took 35 us in place of
+// 39 on 16384 tokens of 256 experts in 8 groups.
 template <int PER, bool BF16, bool SIMPLE, bool GROUPS>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, PER <= 8 ? 10 : 1) route_kernel(RouteArgs args) {
     extern __shared__ double s_values[];  // GROUPS: [warps][E + E / 32 + 1]
-    __shared__ uint2 s_cand[kRouteWarps][32];
+    __shared__ uint2 s_cand[kRouteWarps][64];  // 32 candidates, then their binary64 values
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
-    if (t >= a.T) return;
+    if (t >= args.T) return;
+    RouteArgs a = args;
+    a.row = t * a.ld;
+    a.bf16 = BF16;
     float x[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -343,7 +384,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
         uint32_t key[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) key[j] = key32(x[j]);
-        if (!pick_by_rank<PER, false>(key, a.k, lane, cand, pick, nullptr)) pick = pick_by_rounds<PER>(key, a.k, lane);
+        int n;
+        if (!pick_by_rank<PER, false>(key, a.k, lane, cand, pick, n, 0.0f, nullptr)) pick = pick_by_rounds<PER>(key, a.k, lane);
     } else {
         double* scratch = s_values + warp * (a.E + a.E / 32 + 1);
         Choice r = choose<PER, float, GROUPS>(a, x, m, reinterpret_cast<float*>(scratch), cand, lane);
@@ -676,7 +718,7 @@ cudaError_t launch_route(const void* logits, int type, int64_t T, int E, int64_t
                          const qz_router& r, int32_t* ids, float* weights, cudaStream_t s) {
     const int size = E / r.n_groups;
     const RouteArgs a = {logits,        bias,          T,         ld,        E,       r.top_k, r.score, r.n_groups,
-                         r.top_groups, r.renormalize, 32 / size, 32 % size, r.scale, ids,     weights};
+                         r.top_groups, r.renormalize, 32 / size, 32 % size, r.scale, ids,     weights,    0,       false};
     return type == QZ_TYPE_BF16 ? route_sized<true>(a, s) : route_sized<false>(a, s);
 }
 
