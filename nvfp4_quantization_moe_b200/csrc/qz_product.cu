@@ -258,38 +258,37 @@ __device__ __forceinline__ void scale_warp(const ProductArgs& p, const ExpertLis
                 v[j][i] = load_piece<W>(srow[j], kParts == 1 ? at : min(at, (kv - 1) & ~(int64_t)15), kv);
             }
     };
-    uint4 p0[2][kParts], p1[2][kParts], p2[2][kParts];
-    next_piece(p0);
-    next_piece(p1);
-    next_piece(p2);
-    int it = 0;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-        const Tile t = product_tile(p, list, u);
-        const int quads = p.gather ? max(0, min(16, (t.live - 64 * warp + 3) / 4)) : 0;
-        if (p.gather) {
-            int r[2];
-            rows_of(u, r);
-            __syncwarp();
-            index[lane] = r[0];
-            index[32 + lane] = r[1];
-            __syncwarp();
-        }
-        for (int s = 0; s < steps; ++s, ++it) {
+    // the stages, a piece at a time; tile u at step s
+    int u = blockIdx.x, s = 0, it = 0, quads = 0;
+    auto open_tile = [&]() {
+        if (u >= total || !p.gather) return;
+        quads = max(0, min(16, (product_tile(p, list, u).live - 64 * warp + 3) / 4));
+        int r[2];
+        rows_of(u, r);
+        __syncwarp();
+        index[lane] = r[0];
+        index[32 + lane] = r[1];
+        __syncwarp();
+    };
+    // false: the last tile is done, or a wait ran out
+    auto use_piece = [&](uint4 (&v)[2][kParts]) -> bool {
+        const int n = min(kPiece, steps - s);
+        for (int q = 0; q < n; ++q, ++it) {
             const int st = it % kStages;
-            if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) return;
+            if (!__all_sync(kFull, mbar_wait(smem_addr(&ctl->empty[st]), ((it / kStages) & 1) ^ 1, abort))) return false;
             const uint32_t bar = smem_addr(&ctl->full[st]);
             // row r's four scales of a 512-byte tile: word r / 32 of its 16-byte line r % 32
             const uint32_t dst = base + kStages * kBytesData + st * kScaleStage<FMT> + 16 * lane + 8 * warp;
             if (FMT == QZ_FMT_NVFP4) {
-                const uint4 a = (s & 1) ? p0[0][kParts - 1] : p0[0][0], b = (s & 1) ? p0[1][kParts - 1] : p0[1][0];
+                const uint4 a = q ? v[0][kParts - 1] : v[0][0], b = q ? v[1][kParts - 1] : v[1][0];
                 st_shared_v2(dst, a.x, b.x);
                 st_shared_v2(dst + 512, a.y, b.y);
                 st_shared_v2(dst + 1024, a.z, b.z);
                 st_shared_v2(dst + 1536, a.w, b.w);
             } else {
-                const uint4 a = p0[0][0], b = p0[1][0];
-                st_shared_v2(dst, (s & 2) ? ((s & 1) ? a.w : a.z) : ((s & 1) ? a.y : a.x),
-                             (s & 2) ? ((s & 1) ? b.w : b.z) : ((s & 1) ? b.y : b.x));
+                const uint4 a = v[0][0], b = v[1][0];
+                st_shared_v2(dst, (q & 2) ? ((q & 1) ? a.w : a.z) : ((q & 1) ? a.y : a.x),
+                             (q & 2) ? ((q & 1) ? b.w : b.z) : ((q & 1) ? b.y : b.x));
             }
             fence_async();
             __syncwarp();
@@ -299,24 +298,33 @@ __device__ __forceinline__ void scale_warp(const ProductArgs& p, const ExpertLis
                     const uint32_t to = base + st * kBytesData + 64 * warp * kRowBytes;
 #pragma unroll 4
                     for (int i = 0; i < quads; ++i)
-                        tma_gather4(to + i * 4 * kRowBytes, &map_low, bar, s * (int)kRowBytes,
+                        tma_gather4(to + i * 4 * kRowBytes, &map_low, bar, (s + q) * (int)kRowBytes,
                                     *reinterpret_cast<const int4*>(index + 4 * i));
                 } else {
                     mbar_arrive(bar);
                 }
             }
             __syncwarp();
-            if ((s & (kPiece - 1)) == kPiece - 1 || s + 1 == steps) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 0; i < kParts; ++i) {
-                        p0[j][i] = p1[j][i];
-                        p1[j][i] = p2[j][i];
-                    }
-                next_piece(p2);
-            }
         }
+        s += n;
+        if (s == steps) {
+            s = 0;
+            u += gridDim.x;
+            if (u >= total) return false;
+            open_tile();
+        }
+        next_piece(v);
+        return true;
+    };
+    // Three pieces in registers, each refilled as soon as it is used: a load has two pieces' time.  (Passing
+    // them on from one to the next instead waits for a load one piece after it was issued.)
+    uint4 v0[2][kParts], v1[2][kParts], v2[2][kParts];
+    next_piece(v0);
+    next_piece(v1);
+    next_piece(v2);
+    if (u >= total) return;
+    open_tile();
+    while (use_piece(v0) && use_piece(v1) && use_piece(v2)) {
     }
 }
 
