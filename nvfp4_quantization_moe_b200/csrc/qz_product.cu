@@ -11,8 +11,11 @@
 // tensor cores.  A CTA therefore computes 128 slots x 256 accumulator columns
 // (gated: 128 of the gate and 128 of the up projection, so that the gate is
 // applied in registers): per 128 bytes of contraction it reads 16 KB of x and
-// 32 KB of weights, and four such stages (192 KB, almost the whole shared
-// memory) keep enough bytes in flight for HBM when the tile has few live rows.
+// 32 KB of weights, and four such stages (three for NVFP4, whose scales take
+// more; almost the whole shared memory) keep enough bytes in flight for HBM when
+// the tile has few live rows.  A stage's products take 512 clocks at the tensor
+// cores' rate and 575 here (MXFP8; NVFP4 880: twelve copies of scales go with
+// them); long runs are held back by the 1000 W limit (1.4 to 1.7 GHz).
 //
 // Roles of the 12 warps of the one CTA per SM (persistent over its tiles).
 // Twelve, because that leaves a thread 168 registers: with the shared memory in
@@ -164,17 +167,17 @@ __device__ __forceinline__ Tile product_tile(const ProductArgs& a, const ExpertL
     return t;
 }
 
-__device__ __forceinline__ bool grad_tile(const GradArgs& a, int u, Tile& t) {
+// The gradient's list: first slot, and in place of the prefix the live slots (-1: a bad expert).
+__device__ __forceinline__ bool grad_tile(const GradArgs& a, const ExpertList& list, int u, Tile& t) {
     const int per = a.m_blocks * a.n_blocks;
     t.e = u / per;
     const int v = u - t.e * per;
     t.n = v / a.m_blocks;
     t.m = v - t.n * a.m_blocks;
-    const Range r = expert_range(a.offsets, a.counts, t.e, a.slots);
-    t.first = r.off;
+    t.first = list.first[t.e];
     t.live = kTileM;
-    t.depth = r.cnt;
-    return r.bad == 0 && (r.off & 127) == 0;
+    t.depth = list.prefix[t.e];
+    return t.depth >= 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -456,8 +459,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     Control* const ctl = reinterpret_cast<Control*>(staging + kEpilogueWarps * kStagingBytes);
     ExpertList list;
     list.prefix = reinterpret_cast<int*>(ctl + 1);
-    list.first = list.prefix + (GRAD ? 0 : args.p.n_experts + 1);
-    list.last = reinterpret_cast<uint8_t*>(list.first + (GRAD ? 0 : args.p.n_experts));
+    const int n_experts = GRAD ? args.g.n_experts : args.p.n_experts;
+    list.first = list.prefix + n_experts + 1;
+    list.last = reinterpret_cast<uint8_t*>(list.first + n_experts);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ProductArgs& p = args.p;
@@ -480,12 +484,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     int total;
     if (GRAD) {
         total = g.n_experts * g.m_blocks * g.n_blocks;
-        if (blockIdx.x == 0 && g.d_err) {
-            for (int e = threadIdx.x; e < g.n_experts; e += blockDim.x) {
-                const Range r = expert_range(g.offsets, g.counts, e, g.slots);
-                const unsigned bad = r.bad | ((r.off & 127) ? QZ_DERR_ALIGN : 0u);
-                if (bad) atomicOr(g.d_err, bad);
-            }
+        for (int e = threadIdx.x; e < n_experts; e += blockDim.x) {
+            const Range r = expert_range(g.offsets, g.counts, e, g.slots);
+            const unsigned bad = r.bad | ((r.off & 127) ? QZ_DERR_ALIGN : 0u);
+            list.first[e] = (int)r.off;
+            list.prefix[e] = bad ? -1 : (int)r.cnt;
+            if (bad && blockIdx.x == 0 && g.d_err) atomicOr(g.d_err, bad);
         }
         __syncthreads();
     } else {
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
     // what each role needs to know of tile u; false: nothing is to be done
     auto tile_of = [&](int u, Tile& t) -> bool {
-        if (GRAD) return grad_tile(g, u, t);
+        if (GRAD) return grad_tile(g, list, u, t);
         t = product_tile(p, list, u);
         return true;
     };

@@ -44,23 +44,26 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// No wait of these kernels is longer than the work of one tile; one second
-// means that something is broken, not slow.
-constexpr uint64_t kWaitNs = 1000000000ull;
+// No wait of these kernels is longer than the work of one tile; one second of
+// polling means that something is broken, not slow.  (The time between two looks
+// at the clock counts a millisecond at most: the GPU may have been someone else's
+// in between.)
+constexpr uint64_t kWaitNs = 1000000000ull, kLookNs = 1000000ull;
 
 // Waits for the phase `parity` of a barrier to complete.  false: the limit ran
 // out here or in another thread of the CTA (*abort), and the caller leaves its
 // loop so that the CTA can end.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
     if (mbar_try(bar, parity)) return true;
-    uint64_t start = 0;
+    uint64_t last = 0, waited = 0;
     for (uint32_t i = 1;; ++i) {
         if (mbar_try(bar, parity)) return true;
         if ((i & 63u) == 0) {
             if (*abort) return false;
             const uint64_t now = global_ns();
-            if (start == 0) start = now;
-            if (now - start > kWaitNs) {
+            if (last != 0) waited += now - last < kLookNs ? now - last : kLookNs;
+            last = now;
+            if (waited > kWaitNs) {
                 *abort = 1;
                 return false;
             }
