@@ -9,6 +9,7 @@ raises.  PyTorch supplies device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -674,7 +675,9 @@ def _parts(x, name: str):
     return x[0], x[1], None
 
 
+@functools.lru_cache(maxsize=64)
 def _router(top_k, score, n_groups, top_groups, renormalize, scale):
+    """struct qz_router of these values (only ever read)."""
     return ctypes.byref(_Router(int(score), int(top_k), int(n_groups), int(top_groups), 1 if renormalize else 0,
                                 float(scale)))
 
@@ -756,6 +759,16 @@ class ExpertPlan(NamedTuple):
     slots: torch.Tensor
 
 
+@functools.lru_cache(maxsize=256)
+def _plan_sizes(T: int, k: int, n_experts: int, align: int):
+    return load().qz_plan_slots(T, k, n_experts, align), load().qz_plan_bytes(T, k, n_experts)
+
+
+@functools.lru_cache(maxsize=256)
+def _region(N: int, K: int, fmt: int) -> int:
+    return load().qz_sf_bytes(N, K, fmt, SF_SWIZZLED)
+
+
 def plan_experts(ids: torch.Tensor, n_experts: int, *, align: int = 1, plan: Optional[ExpertPlan] = None,
                  workspace: Optional[torch.Tensor] = None, stream=None) -> ExpertPlan:
     """Sort the choices ``ids`` [T, top_k] by expert (qz_plan_experts), each
@@ -766,12 +779,11 @@ def plan_experts(ids: torch.Tensor, n_experts: int, *, align: int = 1, plan: Opt
     dev = ids.get_device()
     i = _tensor(ids, "ids", torch.int32, dev)
     lib = load()
-    n = lib.qz_plan_slots(T, k, n_experts, align)
-    need = lib.qz_plan_bytes(T, k, n_experts)
+    n, need = _plan_sizes(T, k, n_experts, align)
     if plan is None:
         _require(n_experts >= 1, "n_experts must be at least 1")
         buf = ids.new_empty(2 * n_experts + 1 + n + T * k)
-        offsets, counts, rows, slots = buf.split((n_experts + 1, n_experts, n, T * k))
+        offsets, counts, rows, slots = buf.split_with_sizes((n_experts + 1, n_experts, n, T * k))
         plan = ExpertPlan(offsets, counts, rows, slots.view(T, k))
         at = buf.data_ptr()
         parts = (at, at + 4 * (n_experts + 1), at + 4 * (2 * n_experts + 1), at + 4 * (2 * n_experts + 1 + n))
@@ -847,7 +859,7 @@ def expert_product(fmt: int, x, w, offsets: torch.Tensor, counts: torch.Tensor, 
         K *= 2
     kv = K // (16 if fp4 else 32)
 
-    region = load().qz_sf_bytes(N, K, fmt, SF_SWIZZLED)
+    region = _region(N, K, fmt)
     wp = _stacked((wq, wsf, wa), "w", fmt, E, N, K, region, dev)
     upp = (0, 0, 0)
     if up is not None:
