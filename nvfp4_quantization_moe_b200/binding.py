@@ -640,7 +640,7 @@ def _matrix(t, name: str, dtype, dev: int, shape, optional: bool = False):
         raise ValueError(f"the rows of {name} must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on another device: {t.device}")
-    return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
 def _codes(t, name: str, cols: int, fmt: int, dev: int) -> int:
@@ -654,6 +654,14 @@ def _codes(t, name: str, cols: int, fmt: int, dev: int) -> int:
     return t.data_ptr()
 
 
+def _torch_stream(stream):
+    """The torch stream of a stream argument (a torch stream, an object with cuda_stream, or a handle)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
+
+
 def _scratch(nbytes: int, like: torch.Tensor, stream):
     """Device scratch of one call from torch's allocator, None for none.  The
     allocator may hand it to the current stream's next user, so a call on
@@ -662,7 +670,7 @@ def _scratch(nbytes: int, like: torch.Tensor, stream):
         return None
     t = like.new_empty(nbytes, dtype=torch.uint8)
     if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+        t.record_stream(_torch_stream(stream))
     return t
 
 
@@ -1031,39 +1039,56 @@ def quantize_experts(xs: Sequence[torch.Tensor], fmt: int, layout: int, mode: in
     return entries
 
 
+def _on(stream):
+    """A context in which torch allocates, copies and frees on the call's
+    stream: the table of pointers is scratch of the launch that reads it."""
+    return torch.cuda.stream(None if stream is None else _torch_stream(stream))
+
+
 def quantize_expert_weights(w: torch.Tensor, fmt: int, stream=None):
     """Quantize stacked bf16 expert weights [E, N, K] in one launch into the
     form expert_product takes: (payload [E, N, K or K/2], swizzled scales
-    [E, region], NVFP4: amax [E], computed)."""
+    [E, region], NVFP4: amax [E], computed).  The outputs are allocated on the
+    stream; not for a captured stream (the table comes from the host)."""
+    _require(w.dim() == 3, "w must be [E, N, K]")
     E, N, K = w.shape
-    q = torch.empty((E, N, K if fmt == FMT_MXFP8 else K // 2), dtype=torch.uint8, device=w.device)
-    sf = torch.empty((E, sf_bytes(N, K, fmt, SF_SWIZZLED)), dtype=torch.uint8, device=w.device)
-    amax = torch.empty(E, dtype=torch.float32, device=w.device) if fmt == FMT_NVFP4 else None
-    table = ExpertTable([Entry(w[e], q[e], sf[e], None if amax is None else amax[e:e + 1]) for e in range(E)],
-                        device=w.device)
-    if fmt == FMT_MXFP8:
-        quantize_grouped_mxfp8(table, SF_SWIZZLED, stream)
-    else:
-        quantize_grouped_nvfp4(table, NVFP4_PER_TENSOR_COMPUTE, SF_SWIZZLED, stream)
+    with _on(stream):
+        q = torch.empty((E, N, K if fmt == FMT_MXFP8 else K // 2), dtype=torch.uint8, device=w.device)
+        sf = torch.empty((E, sf_bytes(N, K, fmt, SF_SWIZZLED)), dtype=torch.uint8, device=w.device)
+        amax = torch.empty(E, dtype=torch.float32, device=w.device) if fmt == FMT_NVFP4 else None
+        table = ExpertTable([Entry(w[e], q[e], sf[e], None if amax is None else amax[e:e + 1]) for e in range(E)],
+                            device=w.device)
+        if fmt == FMT_MXFP8:
+            quantize_grouped_mxfp8(table, SF_SWIZZLED)
+        else:
+            quantize_grouped_nvfp4(table, NVFP4_PER_TENSOR_COMPUTE, SF_SWIZZLED)
+        del table
     return q, sf, amax
 
 
 def quantize_tokens(x: torch.Tensor, fmt: int, stream=None):
     """Quantize bf16 rows [R, K] into the form expert_product takes as x:
-    (payload, linear scales [R, K/block], NVFP4: amax [R], one per row)."""
+    (payload, linear scales [R, K/block], NVFP4: amax [R], one per row); streams
+    as in quantize_expert_weights."""
+    _require(x.dim() == 2, "x must be [R, K]")
+    with _on(stream):
+        (e,) = quantize_experts([x], fmt, SF_LINEAR, NVFP4_PER_ROW)
     R, K = x.shape
-    (e,) = quantize_experts([x], fmt, SF_LINEAR, NVFP4_PER_ROW, stream=stream)
-    return e.q, e.sf.view(R, -1), (None if e.amax is None else e.amax[:R])
+    return e.q, e.sf.view(R, K // (32 if fmt == FMT_MXFP8 else 16)), (None if e.amax is None else e.amax[:R])
 
 
 def quantize_slots_colwise(x: torch.Tensor, fmt: int, amax: Optional[torch.Tensor] = None, stream=None):
     """Quantize bf16 [slots, n] down its columns into the form
     expert_weight_grad takes: (payload [n, slots or slots/2], swizzled scales,
-    NVFP4: amax [1], max |x| unless given)."""
+    NVFP4: amax [1], max |x| unless given); streams as in
+    quantize_expert_weights."""
+    _require(x.dim() == 2, "x must be [slots, n]")
     S, n = x.shape
-    q = torch.empty((n, S if fmt == FMT_MXFP8 else S // 2), dtype=torch.uint8, device=x.device)
-    sf = torch.empty(max(sf_bytes(n, S, fmt, SF_SWIZZLED), 16), dtype=torch.uint8, device=x.device)
-    if fmt == FMT_NVFP4 and amax is None:
-        amax = x.abs().amax().to(torch.float32).reshape(1)
-    quantize_grouped_colwise(ExpertTable([Entry(x, q, sf, amax)]), fmt, SF_SWIZZLED, stream)
+    with _on(stream):
+        q = torch.empty((n, S if fmt == FMT_MXFP8 else S // 2), dtype=torch.uint8, device=x.device)
+        sf = torch.empty(max(sf_bytes(n, S, fmt, SF_SWIZZLED), 16), dtype=torch.uint8, device=x.device)
+        if fmt == FMT_NVFP4 and amax is None:
+            amax = (x.abs().amax().to(torch.float32).reshape(1) if x.numel() else
+                    torch.zeros(1, dtype=torch.float32, device=x.device))
+        quantize_grouped_colwise(ExpertTable([Entry(x, q, sf, amax)]), fmt, SF_SWIZZLED)
     return q, sf, amax

@@ -484,6 +484,42 @@ def test_combine_in_place_of_the_residual_and_empty_calls():
     assert (want == 0).all()
 
 
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("raw", [False, True])
+def test_quantizers_of_the_operands_on_another_stream(fmt, raw):
+    """Their table of pointers belongs to the launch: nothing allocated meanwhile may take its place."""
+    g = ref.gen(31)
+    w = ref.randn(g, 5, 64, 96).to(torch.bfloat16).cuda()
+    x = ref.randn(g, 128, 96).to(torch.bfloat16).cuda()
+    want = (qz.quantize_expert_weights(w, fmt), qz.quantize_tokens(x, fmt), qz.quantize_slots_colwise(x, fmt))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for call, t in ((qz.quantize_expert_weights, w), (qz.quantize_tokens, x), (qz.quantize_slots_colwise, x)):
+        got.append(call(t, fmt, stream=side.cuda_stream if raw else side))
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in (16, 64, 512, 512, 512, 4096)]
+    torch.cuda.synchronize()
+    del junk
+    regions = [(64, 96), None, (96, 128)]
+    for a, b, region in zip(got, want, regions):
+        assert torch.equal(a[0], b[0])
+        n = qz.sf_bytes(*region, fmt, qz.SF_SWIZZLED) if region else None
+        assert torch.equal(a[1][..., :n], b[1][..., :n])
+        assert (a[2] is None) == (fmt == MX) and (a[2] is None or torch.equal(a[2], b[2]))
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_weight_grad_without_slots(fmt):
+    empty = torch.empty(0, 64, dtype=torch.bfloat16).cuda()
+    part = qz.quantize_slots_colwise(empty, fmt)
+    lists = torch.zeros(3, dtype=torch.int32).cuda()
+    out = torch.full((2, 64, 64), 3.0).cuda()
+    qz.expert_weight_grad(fmt, part, part, lists, lists[:2], out, accumulate=True)
+    assert torch.all(out == 3.0)
+    qz.expert_weight_grad(fmt, part, part, lists, lists[:2], out)
+    assert torch.all(out == 0.0)
+
+
 # --- the layer --------------------------------------------------------------
 
 def test_serving_layer():

@@ -201,3 +201,10 @@ def test_binding_refuses_what_it_cannot_pass_on(lib):
     with pytest.raises(ValueError, match="fmt"):
         q, w = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(2, 8, 32, dtype=torch.uint8)
         qz.expert_product(qz.FMT_FP8_BLOCK128, (q, q), (w, q), None, None, torch.zeros(4, 8))
+
+
+def test_the_stride_of_a_single_row_does_not_matter():
+    t = torch.zeros(64, dtype=torch.bfloat16).as_strided((1, 8), (13, 1))
+    assert qz.binding._matrix(t, "t", torch.bfloat16, -1, (1, 8)) == (t.data_ptr(), 8)
+    t = torch.zeros(64, dtype=torch.bfloat16).as_strided((2, 8), (16, 1))
+    assert qz.binding._matrix(t, "t", torch.bfloat16, -1, (2, 8)) == (t.data_ptr(), 16)
