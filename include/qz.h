@@ -577,7 +577,7 @@ typedef struct qz_router {
  * of +inf counts as the largest finite float.
  *   d_logits: [T, E] of `type`, row stride ld elements, any alignment of the type
  *   d_bias:   float [E] or NULL;  d_ids: int32 [T, top_k];  d_weights: float [T, top_k]
- * Errors: QZ_ERR_INVALID_ARG for T < 0, E outside 1 .. QZ_MAX_ROUTE_EXPERTS,
+ * Errors: QZ_ERR_INVALID_ARG for T outside 0 .. 2^26 - 1, E outside 1 .. QZ_MAX_ROUTE_EXPERTS,
  * ld < E, unknown enums, top_k outside 1 .. min(E, QZ_MAX_TOP_K), n_groups outside
  * 1 .. QZ_MAX_GROUPS or not dividing E, top_groups outside 1 .. n_groups, top_k
  * larger than the experts of top_groups groups, a scale that is not finite, null
@@ -617,7 +617,7 @@ size_t qz_plan_bytes(int64_t T, int top_k, int E);
  *   d_workspace: qz_plan_bytes(T, top_k, E) bytes, 4-byte aligned (NULL when that is 0);
  *              calls sharing it must not overlap
  * Results do not depend on the launch's timing.  T == 0 writes offsets and counts of 0.
- * Errors: QZ_ERR_INVALID_ARG for T < 0, top_k outside 1 .. QZ_MAX_TOP_K, E outside
+ * Errors: QZ_ERR_INVALID_ARG for T outside 0 .. 2^26 - 1, top_k outside 1 .. QZ_MAX_TOP_K, E outside
  * 1 .. QZ_MAX_ROUTE_EXPERTS, align outside 1 .. 1024 or not a power of two, more than 2^31 - 1
  * slots, null pointers, a workspace smaller than needed; QZ_ERR_ALIGNMENT. */
 qz_status qz_plan_experts(const int32_t *d_ids, int64_t T, int top_k, int E, int align, int32_t *d_offsets,
@@ -643,7 +643,7 @@ typedef struct qz_product {
     const int32_t *d_offsets; /* [n_experts] (or more) first slot of each expert */
     const int32_t *d_counts;  /* [n_experts] live slots of each expert */
     const void *w_q;       /* expert e's [n, k] (packed) payload at w_q + e * w_stride bytes, 16-byte aligned */
-    const uint8_t *w_sf;   /* expert e's swizzled scales of an [n, k] matrix at w_sf + e * w_sf_stride */
+    const uint8_t *w_sf;   /* expert e's swizzled scales of an [n, k] matrix (padding 0x00) at w_sf + e * w_sf_stride */
     const float *w_amax;   /* NVFP4: [n_experts], each expert's tensor amax */
     const void *up_q;      /* gated: a second weight of the same layout and strides, or NULL */
     const uint8_t *up_sf;

@@ -494,15 +494,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         __syncthreads();
     } else {
         unsigned bad = 0;
-        total = p.n_blocks * block_prefix(p.n_experts, list.prefix, ctl->scratch,
-                                          [&](int e) -> long long {
-                                              const Range r = expert_range(p.offsets, p.counts, e, p.slots);
-                                              bad |= r.bad;
-                                              list.first[e] = (int)r.off;
-                                              list.last[e] = (uint8_t)((r.cnt + kTileM - 1) % kTileM);
-                                              return r.bad ? 0 : (r.cnt + kTileM - 1) / kTileM;
-                                          },
-                                          p.d_err);  // ends with a barrier
+        const int row_tiles = block_prefix(p.n_experts, list.prefix, ctl->scratch,
+                                           [&](int e) -> long long {
+                                               const Range r = expert_range(p.offsets, p.counts, e, p.slots);
+                                               bad |= r.bad;
+                                               list.first[e] = (int)r.off;
+                                               list.last[e] = (uint8_t)((r.cnt + kTileM - 1) % kTileM);
+                                               return r.bad ? 0 : (r.cnt + kTileM - 1) / kTileM;
+                                           },
+                                           p.d_err);  // ends with a barrier
+        const int64_t tiles = (int64_t)row_tiles * p.n_blocks;
+        // ranges that overlap could make more tiles than an int counts (the roles step past the last)
+        total = tiles <= 0x7FFF0000 ? (int)tiles : 0;
+        if (tiles > 0x7FFF0000) bad |= QZ_DERR_TOO_LARGE;
         if (bad && blockIdx.x == 0 && p.d_err) atomicOr(p.d_err, bad);
     }
     tc_fence_after();
@@ -1045,7 +1049,7 @@ cudaError_t launch_weight_grad(const qz_weight_grad& p, int ctas, cudaStream_t s
     if (!make_map(&ma, none ? p.out : p.dz_q, none ? 16 : row_bytes, none ? 1 : p.n, 0, 0, 128)) return cudaErrorInvalidValue;
     if (!make_map(&mb, none ? p.out : p.x_q, none ? 16 : row_bytes, none ? 1 : p.k, 0, 0, 128)) return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)p.n_experts * q.m_blocks * q.n_blocks;
-    if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    if (tiles > 0x7FFF0000LL) return cudaErrorInvalidValue;  // the roles step past the last
     const int grid = (int)(tiles < ctas ? tiles : ctas);
     return fp4 ? launch_experts<QZ_FMT_NVFP4, kWeightGrad>(a, ma, ma, mb, mb, p.n_experts, grid, s)
                : launch_experts<QZ_FMT_MXFP8, kWeightGrad>(a, ma, ma, mb, mb, p.n_experts, grid, s);
