@@ -19,6 +19,7 @@
 // the candidates alone for a sigmoid, of all experts for a softmax or close groups
 // (binary64 throughout took 81 us on 16384 tokens of 256 experts in 8 groups, and
 // all experts of each close token, a tail of 10 us).
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -31,6 +32,8 @@
 #include "qz_device.cuh"
 
 namespace qz {
+
+namespace cg = cooperative_groups;
 
 constexpr int kRouteWarps = 4;  // tokens per CTA
 constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -56,6 +59,52 @@ template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
     if (BF16) return clean_logit(__uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16));
     return clean_logit(__ldg(static_cast<const float*>(p) + i));
+}
+
+// Where the experts of a row live in the warp: lane l's value j is expert
+// l + 32 j, or with DENSE (32 PER experts, rows that 16-byte loads can read)
+// expert PER l + j.  Dense rows load and reach the groups, which then are whole
+// lanes, in far fewer instructions: 24 us in place of 35 on 16384 tokens of 256
+// experts in 8 groups (19 in place of 22 without the groups).
+template <int PER, bool DENSE>
+__device__ __forceinline__ int expert_at(int lane, int j) {
+    return DENSE ? PER * lane + j : lane + 32 * j;
+}
+
+template <int PER, bool BF16, bool DENSE>
+__device__ __forceinline__ void load_row(const void* p, int64_t row, int E, int lane, float (&x)[PER]) {
+    if (!DENSE) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) x[j] = lane + 32 * j < E ? load_logit<BF16>(p, row + lane + 32 * j) : -INFINITY;
+    } else if (BF16) {
+        const uint16_t* const at = static_cast<const uint16_t*>(p) + row + PER * lane;
+        uint32_t w[(PER + 1) / 2];
+        if (PER == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+            w[0] = v.x;
+            w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER / 8; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(at) + i);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) x[j] = clean_logit(j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + row + PER * lane) + i);
+            x[4 * i] = clean_logit(v.x);
+            x[4 * i + 1] = clean_logit(v.y);
+            x[4 * i + 2] = clean_logit(v.z);
+            x[4 * i + 3] = clean_logit(v.w);
+        }
+    }
 }
 
 // Order-preserving integers: a < b exactly when key(a) < key(b); 0 is below
@@ -111,24 +160,22 @@ __device__ __forceinline__ float warp_max(float v) {
 constexpr float kNoScore = -745.0f;
 
 // The warp's best key is taken out of `key` and its index returned (-1: no key
-// is left).  Lane l's key j belongs to index l + 32 j.
-template <int PER, typename K>
+// is left).
+template <int PER, bool DENSE, typename K>
 __device__ __forceinline__ int take_best(K (&key)[PER], int lane) {
     K best = key[0];
-    uint32_t idx = lane;
+    uint32_t idx = expert_at<PER, DENSE>(lane, 0);
 #pragma unroll
     for (int j = 1; j < PER; ++j) {
         if (key[j] > best) {
             best = key[j];
-            idx = lane + 32 * j;
+            idx = expert_at<PER, DENSE>(lane, j);
         }
     }
     if (warp_best(best, idx) == 0) return -1;
-    if ((int)(idx & 31) == lane) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (j == (int)(idx >> 5)) key[j] = 0;
-    }
+    for (int j = 0; j < PER; ++j)
+        if ((int)idx == expert_at<PER, DENSE>(lane, j)) key[j] = 0;
     return (int)idx;
 }
 
@@ -138,11 +185,11 @@ struct Pick {
 };
 
 // top_k rounds of a warp-wide argmax.
-template <int PER, typename K>
+template <int PER, bool DENSE, typename K>
 __device__ __forceinline__ Pick pick_by_rounds(K (&key)[PER], int k, int lane) {
     Pick r = {-1, lane};
     for (int c = 0; c < k; ++c) {
-        const int idx = take_best<PER>(key, lane);
+        const int idx = take_best<PER, DENSE>(key, lane);
         if (idx < 0) break;  // no expert is left
         if (lane == c) r.id = idx;
     }
@@ -153,7 +200,7 @@ __device__ __forceinline__ Pick pick_by_rounds(K (&key)[PER], int k, int lane) {
 // every expert within `margin` of the bar is one too, and *gap gets the lane's
 // difference to the next value, if it is chosen.  false: more than 32
 // candidates, nothing is decided.
-template <int PER, bool VERDICT>
+template <int PER, bool DENSE, bool VERDICT>
 __device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, int lane, uint2* cand, Pick& r, int& n,
                                              float margin, float* gap) {
     uint32_t left = key[0], bar = 1;
@@ -172,7 +219,7 @@ __device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, 
         const bool in = key[j] >= bar;
         const unsigned mask = __ballot_sync(kFull, in);
         const int at = n + __popc(mask & ((1u << lane) - 1u));
-        if (in && at < 32) cand[at] = make_uint2(key[j], (uint32_t)(lane + 32 * j));
+        if (in && at < 32) cand[at] = make_uint2(key[j], (uint32_t)expert_at<PER, DENSE>(lane, j));
         n += __popc(mask);
     }
     if (n > 32) return false;
@@ -212,20 +259,20 @@ struct Choice {
 };
 
 // The picks, and for fp32 values whether the differences allow them.
-template <int PER, typename F>
+template <int PER, bool DENSE, typename F>
 __device__ __forceinline__ void decide(const RouteArgs& a, unsigned long long (&key)[PER], int lane, uint2*, F, bool, Choice& r) {
-    r.pick = pick_by_rounds<PER>(key, a.k, lane);
+    r.pick = pick_by_rounds<PER, DENSE>(key, a.k, lane);
 }
 
-template <int PER, typename F>
+template <int PER, bool DENSE, typename F>
 __device__ __forceinline__ void decide(const RouteArgs& a, uint32_t (&key)[PER], int lane, uint2* cand, F bound, bool by_logit,
                                        Choice& r) {
     float gap = INFINITY;
     int n;
     const float margin = by_logit ? 0.0f : 2.0f * (float)bound;
-    if (!pick_by_rank<PER, true>(key, a.k, lane, cand, r.pick, n, margin, &gap)) {
+    if (!pick_by_rank<PER, DENSE, true>(key, a.k, lane, cand, r.pick, n, margin, &gap)) {
         r.certain = r.certain && by_logit;
-        if (r.certain) r.pick = pick_by_rounds<PER>(key, a.k, lane);
+        if (r.certain) r.pick = pick_by_rounds<PER, DENSE>(key, a.k, lane);
         return;
     }
     if (by_logit || __all_sync(kFull, gap > margin)) return;
@@ -255,8 +302,8 @@ __device__ __forceinline__ void decide(const RouteArgs& a, uint32_t (&key)[PER],
 
 // The choice by values of type F (float: with a verdict on its certainty).
 // `by_logit`: the logits order the experts themselves (no bias); the values
-// then only rank the groups.  `scratch` holds E + E / 32 + 1 values of F.
-template <int PER, typename F, bool GROUPS>
+// then only rank the groups.  `scratch` holds E + E / 32 + 1 values of F (not DENSE).
+template <int PER, typename F, bool GROUPS, bool DENSE>
 __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PER], float m, F* scratch, uint2* cand, int lane) {
     const bool sigmoid = a.score == QZ_SCORE_SIGMOID, by_logit = a.bias == nullptr;
     F v[PER];
@@ -273,11 +320,23 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
 #pragma unroll
         for (int j = 0; j < PER; ++j) v[j] = v[j] * scale;
     }
+    float bias[PER];
+    if (DENSE && !by_logit) {
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + PER * lane) + i);
+            bias[4 * i] = b.x;
+            bias[4 * i + 1] = b.y;
+            bias[4 * i + 2] = b.z;
+            bias[4 * i + 3] = b.w;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int i = lane + 32 * j;
         if (sizeof(F) == 4) largest = fmax(largest, v[j]);
-        if (!by_logit && i < a.E) v[j] += (F)__ldg(a.bias + i);
+        if (!by_logit && DENSE) v[j] += (F)bias[j];
+        else if (!by_logit && i < a.E) v[j] += (F)__ldg(a.bias + i);
         if (!(x[j] > -INFINITY) || v[j] != v[j]) v[j] = -INFINITY;
         else if (sizeof(F) == 4 && fabs(v[j]) < INFINITY) largest = fmax(largest, (F)fabs(v[j]));
     }
@@ -289,21 +348,28 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
     decltype(key_of(F())) key[PER];
     unsigned kept = 0xFFFFFFFFu;
     const int size = a.E / a.n_groups;
+    int share = 1;  // lanes that share a group, a power of two
     if (GROUPS) {
-        // 32 / n_groups lanes (a power of two) share a group: its two largest values
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (lane + 32 * j < a.E) scratch[lane + 33 * j] = v[j];  // a column of padding per 32: no bank conflicts
-        __syncwarp();
-        int share = 1;
         while (2 * share * a.n_groups <= 32) share *= 2;
-        const int g = lane / share;
-        F b1 = -INFINITY, b2 = -INFINITY;
-        if (g < a.n_groups) {
-            for (int i = lane % share; i < size; i += share) {
-                const int e = g * size + i;
-                merge_two(b1, b2, scratch[e + e / 32], (F)-INFINITY);
+        F b1 = -INFINITY, b2 = -INFINITY;  // the group's two largest values
+        if (DENSE) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                b2 = fmax(b2, fmin(b1, v[j]));
+                b1 = fmax(b1, v[j]);
+            }
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 32 * j < a.E) scratch[lane + 33 * j] = v[j];  // a column of padding per 32: no bank conflicts
+            __syncwarp();
+            const int g = lane / share;
+            if (g < a.n_groups) {
+                for (int i = lane % share; i < size; i += share) {
+                    const int e = g * size + i;
+                    merge_two(b1, b2, scratch[e + e / 32], (F)-INFINITY);
+                }
             }
         }
         for (int o = 1; o < share; o <<= 1) {
@@ -327,14 +393,16 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
         }
     }
     int group = 0, in_group = 0;  // of expert lane + 32 j, kept up without divisions
-    if (GROUPS) {
+    if (GROUPS && !DENSE) {
         group = lane / size;
         in_group = lane - group * size;
     }
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         key[j] = by_logit ? (v[j] > -INFINITY ? key_of((F)x[j]) : 0) : key_of(v[j]);
-        if (GROUPS) {
+        if (GROUPS && DENSE) {
+            if (!((kept >> (lane / share)) & 1u)) key[j] = 0;
+        } else if (GROUPS) {
             if (lane + 32 * j < a.E && !((kept >> group) & 1u)) key[j] = 0;
             group += a.step_groups;
             in_group += a.step_rest;
@@ -346,16 +414,16 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
     }
 
     Choice r = {{-1, lane}, certain};
-    decide(a, key, lane, cand, bound, by_logit, r);
+    decide<PER, DENSE>(a, key, lane, cand, bound, by_logit, r);
     return r;
 }
 
 // SIMPLE: neither a bias nor a group limit, the logits are the keys.  Ten CTAs
 // per SM (48 registers; the rare binary64 path spills some) took 35 us in place of
 // 39 on 16384 tokens of 256 experts in 8 groups.
-template <int PER, bool BF16, bool SIMPLE, bool GROUPS>
+template <int PER, bool BF16, bool SIMPLE, bool GROUPS, bool DENSE>
 __global__ void __launch_bounds__(kRouteWarps * 32, PER <= 8 ? 10 : 1) route_kernel(RouteArgs args) {
-    extern __shared__ double s_values[];  // GROUPS: [warps][E + E / 32 + 1]
+    extern __shared__ double s_values[];  // GROUPS, not DENSE: [warps][E + E / 32 + 1]
     __shared__ uint2 s_cand[kRouteWarps][64];  // 32 candidates, then their binary64 values
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
@@ -364,11 +432,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, PER <= 8 ? 10 : 1) route_ker
     a.row = t * a.ld;
     a.bf16 = BF16;
     float x[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int i = lane + 32 * j;
-        x[j] = i < a.E ? load_logit<BF16>(a.logits, t * a.ld + i) : -INFINITY;
-    }
+    load_row<PER, BF16, DENSE>(a.logits, a.row, a.E, lane, x);
     const bool sigmoid = a.score == QZ_SCORE_SIGMOID;
     float m = 0.0f;
     if (!sigmoid && !(SIMPLE && a.renorm)) {  // what subtracts the row's maximum
@@ -385,11 +449,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, PER <= 8 ? 10 : 1) route_ker
 #pragma unroll
         for (int j = 0; j < PER; ++j) key[j] = key32(x[j]);
         int n;
-        if (!pick_by_rank<PER, false>(key, a.k, lane, cand, pick, n, 0.0f, nullptr)) pick = pick_by_rounds<PER>(key, a.k, lane);
+        if (!pick_by_rank<PER, DENSE, false>(key, a.k, lane, cand, pick, n, 0.0f, nullptr)) pick = pick_by_rounds<PER, DENSE>(key, a.k, lane);
     } else {
         double* scratch = s_values + warp * (a.E + a.E / 32 + 1);
-        Choice r = choose<PER, float, GROUPS>(a, x, m, reinterpret_cast<float*>(scratch), cand, lane);
-        if (!r.certain) r = choose<PER, double, GROUPS>(a, x, m, scratch, cand, lane);
+        Choice r = choose<PER, float, GROUPS, DENSE>(a, x, m, reinterpret_cast<float*>(scratch), cand, lane);
+        if (!r.certain) r = choose<PER, double, GROUPS, DENSE>(a, x, m, scratch, cand, lane);
         pick = r.pick;
     }
 
@@ -531,13 +595,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(RouteGradA
 // A stable counting sort.  The pairs are cut into one chunk per CTA, a chunk
 // into one contiguous piece per warp; a warp ranks its pairs 32 at a time with
 // match_any, on top of the counts of everything before it (other chunks, then
-// the warps before it in the chunk).  One launch when one chunk holds all
-// pairs; otherwise a launch that counts each chunk and one that places.
+// the warps before it in the chunk).  Three forms, by the number of pairs:
+//   one CTA of 8 warps: no exchange (256 experts: 3.2 us for 8 pairs, against 5.3
+//     for a cluster; 512 pairs take 6.9 against 6.0);
+//   one cluster of 8 CTAs, which exchange their counts through distributed
+//     shared memory (8192 pairs: 8.5 us, 25 for one CTA, 13.5 for two launches);
+//   two launches, one that counts each chunk and one that places, whose many CTAs
+//     scatter faster (131072 pairs: 15 us against 42).
 
 constexpr int kPlanWarps = 16;
-constexpr int kPlanChunk = 2048;  // least pairs of a chunk when there are several
-constexpr int kPlanMost = 128;    // most chunks: each CTA of the second launch reads every chunk's counts
-constexpr int kPlanOne = 8192;    // pairs up to which one CTA sorts alone
+constexpr int kPlanChunk = 2048;   // least pairs of a chunk of the two launches
+constexpr int kPlanMost = 128;     // most chunks: each CTA of the second launch reads every chunk's counts
+constexpr int kPlanOne = 256;      // pairs up to which one CTA sorts alone,
+constexpr int kPlanOneWarps = 8;
+constexpr int kPlanCluster = 16384;  // and one cluster
+constexpr int kClusterCtas = 8;
 
 struct PlanArgs {
     const int32_t* ids;
@@ -553,7 +625,7 @@ struct PlanArgs {
 // The CTA's counts per warp and expert, s_cnt[warp][E].
 __device__ __forceinline__ void plan_count(const PlanArgs& a, int64_t begin, int64_t end, int64_t piece, int* s_cnt) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += blockDim.x) s_cnt[i] = 0;
+    for (int i = threadIdx.x; i < (int)(blockDim.x >> 5) * a.E; i += blockDim.x) s_cnt[i] = 0;
     __syncthreads();
     const int64_t lo = begin + warp * piece, hi = min(end, lo + piece);
     for (int64_t p = lo; p < hi; p += 32) {
@@ -581,28 +653,42 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_count_kernel(PlanArgs a)
         a.rows[s] = -1;
 }
 
-__global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a) {
-    extern __shared__ int s_cnt[];  // [warps][E], then [E] first slots, [warps] scan scratch, [E] pairs before
-    int* s_first = s_cnt + kPlanWarps * a.E;
+enum PlanForm { kOneCta, kCluster, kSecondLaunch };
+
+template <int WARPS, int FORM>
+__global__ void __launch_bounds__(WARPS * 32) plan_place_kernel(PlanArgs a) {
+    constexpr bool CLUSTER = FORM == kCluster;
+    // [warps][E], [E] first slots, [warps] scan scratch, [E] pairs before, CLUSTER: [E] own counts
+    extern __shared__ int s_cnt[];
+    int* s_first = s_cnt + WARPS * a.E;
     int* s_scan = s_first + a.E;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(a.n, begin + a.chunk);
-    const int64_t piece = (a.chunk + kPlanWarps - 1) / kPlanWarps;
+    const int64_t piece = (a.chunk + WARPS - 1) / WARPS;
     plan_count(a, begin, end, piece, s_cnt);
-    if (a.chunks == 1) {
-        for (int64_t s = threadIdx.x; s < a.slots; s += blockDim.x) a.rows[s] = -1;
+    if (FORM != kSecondLaunch) {
+        for (int64_t s = blockIdx.x * blockDim.x + threadIdx.x; s < a.slots; s += gridDim.x * blockDim.x) a.rows[s] = -1;
     }
     // per expert: all pairs (its count) and the pairs of the chunks before this one, by `share` threads
-    // each (a power of two; E <= 1024 = 2 threads' experts).  Sums of whole numbers: any order is the same.
-    const int threads = kPlanWarps * 32;
+    // each.  Sums of whole numbers: any order is the same.
+    constexpr int threads = WARPS * 32, kPer = (QZ_MAX_ROUTE_EXPERTS + threads - 1) / threads;
     int* s_total = s_first;               // [E], then [E] before
-    int* s_before = s_scan + kPlanWarps;
-    for (int e = threadIdx.x; e < a.E; e += threads) s_total[e] = s_before[e] = 0;
-    __syncthreads();
-    if (a.chunks == 1) {
+    int* s_before = s_scan + WARPS;
+    int* s_own = s_before + a.E;
+    if (CLUSTER) {
         for (int e = threadIdx.x; e < a.E; e += threads) {
             int c = 0;
-            for (int w = 0; w < kPlanWarps; ++w) c += s_cnt[w * a.E + e];
+            for (int w = 0; w < WARPS; ++w) c += s_cnt[w * a.E + e];
+            s_own[e] = c;
+        }
+        cg::this_cluster().sync();  // every CTA's counts, and the unused slots' rows
+    }
+    for (int e = threadIdx.x; e < a.E; e += threads) s_total[e] = s_before[e] = 0;
+    __syncthreads();
+    if (FORM == kOneCta) {
+        for (int e = threadIdx.x; e < a.E; e += threads) {
+            int c = 0;
+            for (int w = 0; w < WARPS; ++w) c += s_cnt[w * a.E + e];
             s_total[e] = c;
         }
     } else {
@@ -612,7 +698,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a)
             int all = 0, early = 0;
 #pragma unroll 4
             for (int c = i / a.E; c < a.chunks; c += share) {
-                const int v = __ldg(a.hist + (int64_t)c * a.E + e);
+                const int v = CLUSTER ? cg::this_cluster().map_shared_rank(s_own, c)[e] : __ldg(a.hist + (int64_t)c * a.E + e);
                 all += v;
                 early += c < (int)blockIdx.x ? v : 0;
             }
@@ -625,11 +711,13 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a)
             }
         }
     }
-    __syncthreads();
-    int total[2] = {0, 0}, before[2] = {0, 0}, padded = 0;
+    if (CLUSTER) cg::this_cluster().sync();  // a CTA's counts stay until all have read them
+    else __syncthreads();
+    int total[kPer], before[kPer], padded = 0;  // of kPer experts
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int e = 2 * threadIdx.x + h;
+    for (int h = 0; h < kPer; ++h) {
+        const int e = kPer * threadIdx.x + h;
+        total[h] = before[h] = 0;
         if (e >= a.E) continue;
         total[h] = s_total[e];
         before[h] = s_before[e];
@@ -647,8 +735,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a)
     int first = incl - padded;
     for (int w = 0; w < warp; ++w) first += s_scan[w];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int e = 2 * threadIdx.x + h;
+    for (int h = 0; h < kPer; ++h) {
+        const int e = kPer * threadIdx.x + h;
         if (e >= a.E) continue;
         s_first[e] = first + before[h];
         if (blockIdx.x == 0) {
@@ -662,7 +750,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a)
     // each warp's counter of an expert starts at the slot of its first pair there
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         int at = s_first[e];
-        for (int w = 0; w < kPlanWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const int c = s_cnt[w * a.E + e];
             s_cnt[w * a.E + e] = at;
             at += c;
@@ -691,15 +779,23 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_place_kernel(PlanArgs a)
 // launches
 // ---------------------------------------------------------------------------
 
-template <int PER, bool BF16>
-static cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
+template <int PER, bool BF16, bool DENSE>
+static void route_kinds(const RouteArgs& a, cudaStream_t s) {
     const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
     const int threads = kRouteWarps * 32;
-    const size_t smem = (size_t)kRouteWarps * (a.E + a.E / 32 + 1) * sizeof(double);  // at most 33 KB
+    const size_t smem = DENSE ? 0 : (size_t)kRouteWarps * (a.E + a.E / 32 + 1) * sizeof(double);  // at most 33 KB
     const bool groups = a.top_groups < a.n_groups;
-    if (groups) route_kernel<PER, BF16, false, true><<<grid, threads, smem, s>>>(a);
-    else if (a.bias) route_kernel<PER, BF16, false, false><<<grid, threads, 0, s>>>(a);
-    else route_kernel<PER, BF16, true, false><<<grid, threads, 0, s>>>(a);
+    if (groups) route_kernel<PER, BF16, false, true, DENSE><<<grid, threads, smem, s>>>(a);
+    else if (a.bias) route_kernel<PER, BF16, false, false, DENSE><<<grid, threads, 0, s>>>(a);
+    else route_kernel<PER, BF16, true, false, DENSE><<<grid, threads, 0, s>>>(a);
+}
+
+template <int PER, bool BF16>
+static cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
+    const uintptr_t addresses = (uintptr_t)a.logits | (uintptr_t)a.bias;
+    const bool dense = PER >= 4 && a.E == 32 * PER && addresses % 16 == 0 && a.ld % (BF16 ? 8 : 4) == 0;
+    if (dense) route_kinds<PER, BF16, (PER >= 4)>(a, s);
+    else route_kinds<PER, BF16, false>(a, s);
     return cudaGetLastError();
 }
 
@@ -743,15 +839,38 @@ cudaError_t launch_route_grad(const void* logits, int type, int64_t T, int E, in
 
 static int64_t plan_chunk(int64_t n) {
     if (n <= kPlanOne) return n > 0 ? n : 1;
+    if (n <= kPlanCluster) return (n + kClusterCtas - 1) / kClusterCtas;
     const int64_t c = (n + kPlanMost - 1) / kPlanMost;
     return c > kPlanChunk ? c : kPlanChunk;
 }
 
-static int64_t plan_chunks(int64_t n) { return n > 0 ? (n + plan_chunk(n) - 1) / plan_chunk(n) : 1; }
-
 size_t plan_bytes(int64_t n, int E) {
-    const int64_t c = plan_chunks(n);
-    return c == 1 ? 0 : (size_t)c * (size_t)E * sizeof(int);
+    return n <= kPlanCluster ? 0 : (size_t)((n + plan_chunk(n) - 1) / plan_chunk(n)) * (size_t)E * sizeof(int);
+}
+
+template <int WARPS, int FORM>
+static cudaError_t launch_place(const PlanArgs& a, int ctas, cudaStream_t s) {
+    const auto kernel = plan_place_kernel<WARPS, FORM>;
+    const auto bytes = [](int experts) { return (size_t)((WARPS + (FORM == kCluster ? 3 : 2)) * experts + WARPS) * sizeof(int); };
+    if (bytes(a.E) > 48 * 1024) {
+        // asked for at its largest every time: the attribute is one value per device and
+        // a smaller value of another call must not take it back
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(QZ_MAX_ROUTE_EXPERTS));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = kClusterCtas;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(ctas);
+    config.blockDim = dim3(WARPS * 32);
+    config.dynamicSmemBytes = bytes(a.E);
+    config.stream = s;
+    config.attrs = &cluster;
+    config.numAttrs = FORM == kCluster ? 1 : 0;
+    return cudaLaunchKernelEx(&config, kernel, a);
 }
 
 cudaError_t launch_plan(const int32_t* ids, int64_t T, int k, int E, int align, int64_t slots, int32_t* offsets,
@@ -763,31 +882,23 @@ cudaError_t launch_plan(const int32_t* ids, int64_t T, int k, int E, int align, 
     a.k = k;
     a.E = E;
     a.align = align;
-    a.chunks = (int)plan_chunks(a.n);
     a.chunk = plan_chunk(a.n);
+    a.chunks = (int)(a.n <= kPlanOne ? 1 : a.n <= kPlanCluster ? kClusterCtas : (a.n + a.chunk - 1) / a.chunk);
     a.offsets = offsets;
     a.counts = counts;
     a.rows = rows;
     a.pair_slots = pair_slots;
     a.hist = static_cast<int*>(ws);
-    const int threads = kPlanWarps * 32;
-    const size_t smem_count = (size_t)kPlanWarps * E * sizeof(int);
-    const size_t smem_place = smem_count + (size_t)(2 * E + kPlanWarps) * sizeof(int);  // at most 72 KB
-    // asked for at its largest every time: the attribute is one value per device and
-    // a smaller value of another call must not take it back
-    const int most = (kPlanWarps * QZ_MAX_ROUTE_EXPERTS + 2 * QZ_MAX_ROUTE_EXPERTS + kPlanWarps) * (int)sizeof(int);
-    if (smem_place > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (a.n <= kPlanOne) return launch_place<kPlanOneWarps, kOneCta>(a, 1, s);
+    if (a.n <= kPlanCluster) return launch_place<kPlanWarps, kCluster>(a, kClusterCtas, s);
+    const size_t smem = (size_t)kPlanWarps * E * sizeof(int), most = (size_t)kPlanWarps * QZ_MAX_ROUTE_EXPERTS * sizeof(int);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
     }
-    if (a.chunks > 1) {
-        plan_count_kernel<<<a.chunks, threads, smem_count, s>>>(a);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    plan_place_kernel<<<a.chunks, threads, smem_place, s>>>(a);
-    return cudaGetLastError();
+    plan_count_kernel<<<a.chunks, kPlanWarps * 32, smem, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_place<kPlanWarps, kSecondLaunch>(a, a.chunks, s);
 }
 
 }  // namespace qz

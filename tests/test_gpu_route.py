@@ -192,11 +192,41 @@ def test_route_grad_of_tiny_scores():
     ref.close(got, grad_reference(x, ids, dw, True, True, 1.0), 64 * ref.HALF_F32 * 3, "dlogits")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("E,groups", [(128, 1), (128, 4), (256, 8), (256, 32), (512, 2), (1024, 16)])
+def test_router_of_rows_that_wide_loads_cannot_read(dtype, score, E, groups):
+    """Rows from an odd element on (or with an odd stride, or an odd bias) are read otherwise: the same choice."""
+    T, k = 70, 8
+    g = ref.gen(E + groups)
+    x = ref.randn(g, T, E).to(dtype).cuda()
+    x[3] = -torch.inf
+    x[4, : E - 2] = torch.nan
+    bias = (ref.randn(g, E) * 0.1).cuda() if groups > 1 else None
+    kw = dict(score=score, n_groups=groups, top_groups=(groups + 1) // 2, renormalize=groups != 4)
+    ids, w = qz.route_experts(x, k, bias=bias, **kw)
+    wide = torch.zeros(T, E + 1, dtype=dtype).cuda()
+    wide[:, 1:] = x
+    flat = torch.zeros(T * E + 1, dtype=dtype).cuda()
+    flat[1:] = x.reshape(-1)
+    others = [(wide[:, 1:], bias), (flat[1:].view(T, E), bias)]
+    if bias is not None:
+        odd = torch.zeros(E + 1).cuda()
+        odd[1:] = bias
+        others.append((x, odd[1:]))
+    for y, b in others:
+        ids2, w2 = qz.route_experts(y, k, bias=b, **kw)
+        assert torch.equal(ids, ids2)
+        # a softmax's sum in another order: at most 32 + 5 additions on either side
+        ref.close(w2, w.double().cpu(), 2 * 37 * 2 * ref.HALF_F32 * w.double().cpu().abs(), "weights")
+
+
 # --- expert order -----------------------------------------------------------
 
 @pytest.mark.parametrize("T,E,k,align", [(0, 4, 2, 8), (1, 1, 1, 1), (1, 128, 8, 128), (5, 7, 3, 16), (333, 60, 4, 1),
                                          (1024, 128, 8, 128), (1025, 256, 8, 32), (3000, 1024, 8, 4), (70000, 16, 2, 128),
-                                         (8192, 1, 1, 1024)])
+                                         (8192, 1, 1, 1024), (32, 1024, 8, 64), (33, 8, 8, 1), (257, 1, 1, 1),
+                                         (100, 1024, 8, 8), (2048, 300, 8, 16), (2049, 1000, 8, 1)])
 def test_plan(T, E, k, align):
     g = ref.gen(T + E)
     ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
@@ -217,3 +247,20 @@ def test_plan_of_one_expert_and_of_none():
     assert torch.equal(plan.slots.reshape(-1).cpu(), torch.arange(18000, dtype=torch.int32))
     plan = qz.plan_experts(torch.full_like(ids, -1), 8, align=128)
     assert plan.counts.sum() == 0 and plan.offsets.sum() == 0 and (plan.rows == -1).all() and (plan.slots == -1).all()
+
+
+@pytest.mark.parametrize("T", [20, 300, 4000])  # one CTA, one cluster, two launches
+def test_plan_in_a_graph(T):
+    E, k = 40, 8
+    g = ref.gen(T)
+    ids = torch.zeros(T, k, dtype=torch.int32).cuda()
+    plan = qz.plan_experts(ids, E, align=16)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan = qz.plan_experts(ids, E, align=16)
+    for _ in range(3):
+        new = torch.randint(-1, E, (T, k), generator=g, dtype=torch.int32)
+        ids.copy_(new)
+        graph.replay()
+        for name, a, b in zip(plan._fields, plan, ref.plan(new.numpy(), E, 16)):
+            assert np.array_equal(a.cpu().numpy(), b), name

@@ -78,7 +78,7 @@ def test_plan_sizes_and_refusals(lib):
     for bad in ((-1, 2, 3, 16), (4, 0, 3, 16), (4, 33, 64, 16), (4, 2, 0, 16), (4, 2, 1025, 16), (4, 2, 3, 0), (4, 2, 3, 3),
                 (4, 2, 3, 2048)):
         assert qz.plan_slots(*bad) == 0
-    assert lib.qz_plan_bytes(1024, 8, 128) == 0 and lib.qz_plan_bytes(1025, 8, 128) > 0
+    assert lib.qz_plan_bytes(2048, 8, 128) == 0 and lib.qz_plan_bytes(2049, 8, 128) > 0
     assert lib.qz_plan_bytes(-1, 8, 128) == 0 and lib.qz_plan_bytes(1 << 20, 8, 0) == 0
 
     def plan(T=4, k=2, E=8, align=16, ids=A, off=A, cnt=A, rows=A, slots=A, ws=None, n=0):
