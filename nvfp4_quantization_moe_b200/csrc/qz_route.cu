@@ -342,7 +342,10 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
     }
     // fp32: 2^x within 2 ulp, its argument's rounding (|x - m| e^(x - m) <= 1 / e), a sum of E terms in
     // a tree, a reciprocal within 1 ulp, a product and a sum: below 24 half ulps of the largest magnitude
-    const F bound = sizeof(F) == 4 ? (F)warp_max((float)largest) * (F)(24.0 / 16777216.0) : (F)0;
+    // (`largest` is not negative: its bits are ordered like it)
+    const F bound = sizeof(F) == 4 ? (F)(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint((float)largest))) *
+                                         (24.0f / 16777216.0f))
+                                   : (F)0;
     bool certain = true;
 
     decltype(key_of(F())) key[PER];
@@ -419,8 +422,8 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
 }
 
 // SIMPLE: neither a bias nor a group limit, the logits are the keys.  Ten CTAs
-// per SM (48 registers; the rare binary64 path spills some) took 35 us in place of
-// 39 on 16384 tokens of 256 experts in 8 groups.
+// per SM (48 registers; the rare binary64 path spills some) took 23.9 us, eight 24.2 and
+// twelve 25.6 on 16384 tokens of 256 experts in 8 groups.
 template <int PER, bool BF16, bool SIMPLE, bool GROUPS, bool DENSE>
 __global__ void __launch_bounds__(kRouteWarps * 32, PER <= 8 ? 10 : 1) route_kernel(RouteArgs args) {
     extern __shared__ double s_values[];  // GROUPS, not DENSE: [warps][E + E / 32 + 1]
@@ -460,7 +463,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, PER <= 8 ? 10 : 1) route_ker
     // weights: the lane's choice again from memory (the row is in L1), with the accurate exponential
     const bool live = pick.id >= 0 && pick.at < a.k;
     const float chosen = live ? load_logit<BF16>(a.logits, t * a.ld + pick.id) : -INFINITY;
-    const float top = warp_max(chosen);
+    const uint32_t best = __reduce_max_sync(kFull, key32(chosen));
+    const float top = best ? unkey32(best) : -INFINITY;
     float w = 0.0f;
     if (sigmoid && !(a.renorm && top < -20.0f)) {
         const float e = expf(-fabsf(chosen));
@@ -641,6 +645,7 @@ __device__ __forceinline__ void plan_count(const PlanArgs& a, int64_t begin, int
 
 __global__ void __launch_bounds__(kPlanWarps * 32) plan_count_kernel(PlanArgs a) {
     extern __shared__ int s_cnt[];
+    cudaTriggerProgrammaticLaunchCompletion();  // the second launch waits for this one's end where it must
     const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(a.n, begin + a.chunk);
     plan_count(a, begin, end, (a.chunk + kPlanWarps - 1) / kPlanWarps, s_cnt);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
@@ -669,6 +674,8 @@ __global__ void __launch_bounds__(WARPS * 32) plan_place_kernel(PlanArgs a) {
     if (FORM != kSecondLaunch) {
         for (int64_t s = blockIdx.x * blockDim.x + threadIdx.x; s < a.slots; s += gridDim.x * blockDim.x) a.rows[s] = -1;
     }
+    // (the count of this chunk needs the choices only and runs beside the first launch's end)
+    if (FORM == kSecondLaunch) cudaGridDependencySynchronize();
     // per expert: all pairs (its count) and the pairs of the chunks before this one, by `share` threads
     // each.  Sums of whole numbers: any order is the same.
     constexpr int threads = WARPS * 32, kPer = (QZ_MAX_ROUTE_EXPERTS + threads - 1) / threads;
@@ -859,17 +866,22 @@ static cudaError_t launch_place(const PlanArgs& a, int ctas, cudaStream_t s) {
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(QZ_MAX_ROUTE_EXPERTS));
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute cluster;
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = kClusterCtas;
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchAttribute form;
+    if (FORM == kCluster) {
+        form.id = cudaLaunchAttributeClusterDimension;
+        form.val.clusterDim.x = kClusterCtas;
+        form.val.clusterDim.y = form.val.clusterDim.z = 1;
+    } else {
+        form.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        form.val.programmaticStreamSerializationAllowed = 1;
+    }
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(ctas);
     config.blockDim = dim3(WARPS * 32);
     config.dynamicSmemBytes = bytes(a.E);
     config.stream = s;
-    config.attrs = &cluster;
-    config.numAttrs = FORM == kCluster ? 1 : 0;
+    config.attrs = &form;
+    config.numAttrs = FORM == kOneCta ? 0 : 1;
     return cudaLaunchKernelEx(&config, kernel, a);
 }
 
