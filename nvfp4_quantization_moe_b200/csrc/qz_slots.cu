@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, kGradCtas)
                     unsigned* d_err) {
     extern __shared__ int s_prefix[];
     __shared__ long long s_scratch[33];
+    cudaTriggerProgrammaticLaunchCompletion();  // the bias sums wait for this launch's end before they read
     const int lane = threadIdx.x & 31;
     const int blocks = (int)((n + kGradCols - 1) / kGradCols);
     const int64_t total = (int64_t)piece_prefix(a, s_prefix, s_scratch, d_err) * blocks;
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(kGradWarps * 32)
     if (before + pieces > a.most) return;
     const int each = (pieces + kGradWarps - 1) / kGradWarps, end = min(pieces, (warp + 1) * each);
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    cudaGridDependencySynchronize();
     if (c < width) {
         const float* from = sums + (int64_t)before * width + c;
 #pragma unroll 4
@@ -404,9 +406,16 @@ cudaError_t launch_act_grad(const uint16_t* dout, int64_t ld_d, const uint16_t* 
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || dbias == nullptr) return e;
     const int64_t width = gated ? 2 * n : n;
-    bias_sum_kernel<<<dim3((unsigned)((width + kSumCols - 1) / kSumCols), (unsigned)n_experts), kGradWarps * 32, 0, s>>>(
-        a, sums, width, dbias);
-    return cudaGetLastError();
+    cudaLaunchAttribute beside;  // its lists are read beside the first launch's end
+    beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    beside.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((unsigned)((width + kSumCols - 1) / kSumCols), (unsigned)n_experts);
+    config.blockDim = dim3(kGradWarps * 32);
+    config.stream = s;
+    config.attrs = &beside;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, bias_sum_kernel, a, (const float*)sums, width, dbias);
 }
 
 }  // namespace qz
