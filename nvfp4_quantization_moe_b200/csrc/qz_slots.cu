@@ -39,6 +39,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 constexpr int kRowThreads = 128;               // 1024 columns per CTA
 constexpr int kRowCols = 8 * kRowThreads;
+constexpr int kU = 4;  // rows of a token whose loads are in flight together
 
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint16_t* __restrict__ y, int64_t ld_y,
                                                               const int32_t* __restrict__ slots, int k,
@@ -51,7 +52,6 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint16_t* __
     if (c >= H) return;
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (residual != nullptr) unpack8(*reinterpret_cast<const uint4*>(residual + t * ld_r + c), acc);
-    constexpr int kU = 4;
     for (int j = 0; j < k; j += kU) {
         uint4 v[kU];
         float w[kU];
@@ -82,8 +82,10 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint16_t* __
 // ---------------------------------------------------------------------------
 //
 // CTA t holds token t's row in registers, writes it (times each weight) to its
-// slots and forms the dot products with the slots' rows of `other`; it also
-// zeroes the unused slots of its share of the slots.
+// slots and forms the dot products with the slots' rows of `other`, four choices
+// at a time (4096 tokens of 2048 columns in 8 slots each, 418 MB with the zeros:
+// 70 us one by one, 65 so); it also zeroes the unused slots of its share of the
+// slots.
 
 constexpr int kDispatchThreads = 256;
 constexpr int64_t kZeroSlots = 8, kZeroCtas = 1184;  // slots a CTA looks at, CTAs that is worth (8 per SM)
@@ -108,31 +110,47 @@ __global__ void __launch_bounds__(kDispatchThreads)
                 raw = ld_stream(x + t * ld_x + c);
                 unpack8(raw, f);
             }
-            for (int j = 0; j < k; ++j) {
-                const int64_t s = __ldg(slots + t * k + j);
-                if (s < 0 || s >= n_slots) continue;  // the same for the whole CTA
-                uint4 o = make_uint4(0, 0, 0, 0);
-                if (DOTS && in) o = ld_stream(other + s * ld_o + c);
-                if (in) {
-                    if (weights) {
-                        const float w = __ldg(weights + t * k + j);
-                        float g[8];
+            for (int j = 0; j < k; j += kU) {
+                int64_t at[kU];  // -1: no slot; the same for the whole CTA
+                uint4 o[kU];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) g[i] = w * f[i];
-                        st_v4(y + s * ld_y + c, pack8(g));
-                    } else {
-                        st_v4(y + s * ld_y + c, raw);
+                for (int u = 0; u < kU; ++u) {
+                    at[u] = j + u < k ? (int64_t)__ldg(slots + t * k + j + u) : -1;
+                    if (at[u] >= n_slots) at[u] = -1;
+                    o[u] = make_uint4(0, 0, 0, 0);
+                    if (DOTS && in && at[u] >= 0) o[u] = ld_stream(other + at[u] * ld_o + c);
+                }
+                float d[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    d[u] = 0.0f;
+                    if (in && at[u] >= 0) {
+                        uint4 v = raw;
+                        if (weights) {
+                            const float w = __ldg(weights + t * k + j + u);
+                            float g[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) g[i] = w * f[i];
+                            v = pack8(g);
+                        }
+                        st_v4(y + at[u] * ld_y + c, v);
+                    }
+                    if (DOTS) {
+                        float g[8];
+                        unpack8(o[u], g);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) d[u] = fmaf(f[i], g[i], d[u]);
                     }
                 }
                 if (DOTS) {
-                    float g[8];
-                    unpack8(o, g);
-                    float d = 0.0f;
+                    // four sums over the warp at once: lanes 8 u .. 8 u + 7 end up with choice u's
+                    const bool hi = lane & 16, odd = lane & 8;
+                    const float a = (hi ? d[2] : d[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? d[0] : d[2], 16);
+                    const float b = (hi ? d[3] : d[1]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? d[1] : d[3], 16);
+                    float e = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d = fmaf(f[i], g[i], d);
-#pragma unroll
-                    for (int b = 16; b > 0; b >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, b);
-                    if (lane == 0) s_dot[warp][j] += d;
+                    for (int m = 4; m > 0; m >>= 1) e += __shfl_xor_sync(0xFFFFFFFFu, e, m);
+                    if ((lane & 7) == 0 && j + lane / 8 < k) s_dot[warp][j + lane / 8] += e;
                 }
             }
         }
@@ -162,11 +180,12 @@ __global__ void __launch_bounds__(kDispatchThreads)
 // expert's start, so that the unused slots are zeroed on the way) x 256 columns,
 // and one warp's: 8 columns per lane, four rows' loads in flight, no barriers.  A
 // persistent grid takes the pieces in turn, which evens out experts of any
-// length.  (A cluster per expert and column block, joined through distributed
-// shared memory, was measured first: 98 us on 4096 x 8 rows of 2 x 768 over 128
-// experts, most of it waiting at barriers for uneven warps and for stores.)  A
-// warp leaves its piece's column sums in the workspace and a second launch adds
-// an expert's pieces in order.
+// length.  On 4096 x 8 rows of 2 x 768 over 128 experts that takes 71 us.  (A cluster
+// per expert and column block, joined through distributed shared memory: 98 us,
+// most of it waiting at barriers for uneven warps and for stores.  Refilling each
+// row's registers as soon as they are used: 86 us; three CTAs per SM with two rows
+// each: 82.)  A warp leaves its piece's column sums in the workspace and a second
+// launch adds an expert's pieces in order.
 
 constexpr int kGradWarps = 8;
 constexpr int kGradCols = 256;
