@@ -603,9 +603,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(RouteGradA
 //   one CTA of 8 warps: no exchange (256 experts: 3.2 us for 8 pairs, against 5.3
 //     for a cluster; 512 pairs take 6.9 against 6.0);
 //   one cluster of 8 CTAs, which exchange their counts through distributed
-//     shared memory (8192 pairs: 8.5 us, 25 for one CTA, 13.5 for two launches);
+//     shared memory (8192 pairs: 8.3 us against 25 for one CTA; 16384: 10.4);
 //   two launches, one that counts each chunk and one that places, whose many CTAs
-//     scatter faster (131072 pairs: 15 us against 42).
+//     scatter faster (32768 pairs: 10.5 us, 131072: 12, against 15 and 42).
 
 constexpr int kPlanWarps = 16;
 constexpr int kPlanChunk = 2048;   // least pairs of a chunk of the two launches
