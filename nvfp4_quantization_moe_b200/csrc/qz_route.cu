@@ -196,23 +196,23 @@ __device__ __forceinline__ Pick pick_by_rounds(K (&key)[PER], int k, int lane) {
     return r;
 }
 
-// The same by candidates (see the top of the file), `n` of them.  With VERDICT
+// The same by candidates (see the top of the file), `n` of them.  With GAPS
 // every expert within `margin` of the bar is one too, and *gap gets the lane's
 // difference to the next value, if it is chosen.  false: more than 32
 // candidates, nothing is decided.
-template <int PER, bool DENSE, bool VERDICT>
+template <int PER, bool DENSE, bool GAPS>
 __device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, int lane, uint2* cand, Pick& r, int& n,
                                              float margin, float* gap) {
     uint32_t left = key[0], bar = 1;
 #pragma unroll
     for (int j = 1; j < PER; ++j) left = max(left, key[j]);
-    const int rounds = VERDICT ? k + 1 : k;  // the verdict wants the value behind the last choice too
+    const int rounds = GAPS ? k + 1 : k;  // the gaps need the value behind the last choice too
     for (int c = 0; c < rounds; ++c) {
         bar = __reduce_max_sync(kFull, left);
         if (left == bar) left = 0;
     }
     if (rounds > 32 || bar == 0) bar = 1;  // fewer lanes than choices: every key above 0
-    else if (VERDICT) bar = max(key32(unkey32(bar) - margin), 1u);
+    else if (GAPS) bar = max(key32(unkey32(bar) - margin), 1u);
     n = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -231,11 +231,11 @@ __device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, 
         const uint2 other = cand[i];
         const bool ahead = other.x > mine.x || (other.x == mine.x && other.y < mine.y);
         if (ahead) ++before;
-        else if (VERDICT && i != lane) behind = max(behind, other.x);
+        else if (GAPS && i != lane) behind = max(behind, other.x);
     }
     r.id = lane < n ? (int)mine.y : -1;
     r.at = lane < n ? before : lane;
-    if (VERDICT) *gap = lane < n && before < k && behind != 0 ? unkey32(mine.x) - unkey32(behind) : INFINITY;
+    if (GAPS) *gap = lane < n && before < k && behind != 0 ? unkey32(mine.x) - unkey32(behind) : INFINITY;
     return true;
 }
 
@@ -300,7 +300,7 @@ __device__ __forceinline__ void decide(const RouteArgs& a, uint32_t (&key)[PER],
     if (lane < n) r.pick = {id, before};
 }
 
-// The choice by values of type F (float: with a verdict on its certainty).
+// The choice by values of type F (float: and whether it is certain).
 // `by_logit`: the logits order the experts themselves (no bias); the values
 // then only rank the groups.  `scratch` holds E + E / 32 + 1 values of F (not DENSE).
 template <int PER, typename F, bool GROUPS, bool DENSE>
