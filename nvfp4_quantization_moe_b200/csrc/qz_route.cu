@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(WARPS * 32) plan_place_kernel(PlanArgs a) {
             int all = 0, early = 0;
 #pragma unroll 4
             for (int c = i / a.E; c < a.chunks; c += share) {
-                const int v = CLUSTER ? cg::this_cluster().map_shared_rank(s_own, c)[e] : __ldg(a.hist + (int64_t)c * a.E + e);
+                const int v = CLUSTER ? cg::this_cluster().map_shared_rank(s_own, c)[e]
+                                      : (int)ld_written(a.hist + (int64_t)c * a.E + e);
                 all += v;
                 early += c < (int)blockIdx.x ? v : 0;
             }

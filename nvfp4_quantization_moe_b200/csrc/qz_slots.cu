@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, kGradCtas)
 constexpr int kSumCols = 128;
 
 __global__ void __launch_bounds__(kGradWarps * 32)
-    bias_sum_kernel(GradPieces a, const float* __restrict__ sums, int64_t width, float* __restrict__ dbias) {
+    bias_sum_kernel(GradPieces a, const float* sums, int64_t width, float* __restrict__ dbias) {
     __shared__ int s_before[kGradWarps];
     __shared__ float4 s_part[kGradWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.y;
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kGradWarps * 32)
         const float* from = sums + (int64_t)before * width + c;
 #pragma unroll 4
         for (int p = warp * each; p < end; ++p) {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(from + (int64_t)p * width));
+            const float4 u = ld_written_v4(from + (int64_t)p * width);
             v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
         }
     }

@@ -373,6 +373,24 @@ def test_activation_grad(gated, act, counts, N):
     assert torch.equal(first, dbias)
 
 
+def test_activation_grads_back_to_back_in_one_workspace():
+    """The bias sums begin beside the gradient's end: each call adds its own pieces, not an earlier one's."""
+    E, N, S = 12, 264, 3000
+    counts = torch.tensor([250] * E, dtype=torch.int32)
+    offsets = offsets_of(counts.long()).cuda()
+    ws = torch.empty(qz.load().qz_activation_grad_bytes(S, N, 0, E), dtype=torch.uint8).cuda()
+    pre = torch.ones(S, N, dtype=torch.bfloat16).cuda()
+    # whole numbers: the sums are exact
+    douts = [torch.randint(-8, 9, (S, N), generator=ref.gen(i)).to(torch.bfloat16).cuda() for i in range(4)]
+    dpre, sums = torch.empty_like(pre), [torch.empty(E, N).cuda() for _ in range(40)]
+    for i, s in enumerate(sums):
+        qz.expert_activation_grad(douts[i % 4], pre, offsets, counts.cuda(), dpre, activation=qz.ACT_RELU, dbias=s,
+                                  workspace=ws)
+    want = [d.float().reshape(E, 250, N).sum(1) for d in douts]
+    for i, s in enumerate(sums):
+        assert torch.equal(s, want[i % 4]), i
+
+
 @pytest.mark.parametrize("offsets,counts,bad", [([0, 100, 50], [100, 0, 60], 1), ([3, 10, 20], [7, 10, 5], 0),
                                                 ([0, 40, 80], [30, -1, 5], 1), ([0, 60, 30], [40, 5, 110], 2),
                                                 ([0, 0, 0], [0, 0, 129], 2)])

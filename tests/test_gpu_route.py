@@ -264,3 +264,18 @@ def test_plan_in_a_graph(T):
         graph.replay()
         for name, a, b in zip(plan._fields, plan, ref.plan(new.numpy(), E, 16)):
             assert np.array_equal(a.cpu().numpy(), b), name
+
+
+def test_plans_back_to_back_in_one_workspace():
+    """The second launch begins beside the first one's end: every plan counts its own choices, not an earlier one's."""
+    E, k, T = 200, 4, 20000
+    g = ref.gen(77)
+    lists = [torch.randint(-1, E, (T, k), generator=g, dtype=torch.int32) for _ in range(4)]
+    lists[1].clamp_(max=3)
+    sorted_ = [ref.plan(i.numpy(), E, 8) for i in lists]
+    ids = [i.cuda() for i in lists]
+    ws = torch.empty(qz.load().qz_plan_bytes(T, k, E), dtype=torch.uint8).cuda()
+    plans = [qz.plan_experts(ids[i % 4], E, align=8, workspace=ws) for i in range(40)]
+    for i, plan in enumerate(plans):
+        for name, a, b in zip(plan._fields, plan, sorted_[i % 4]):
+            assert np.array_equal(a.cpu().numpy(), b), (i, name)
