@@ -592,6 +592,7 @@ def swizzle_scales(table: SfPairTable, stream=None, err=None, max_ctas: int = 0)
 
 # A decode step makes these calls once per layer and is bound by the host, so
 # the checks below read each property once and format a message only to raise it.
+# What a call allocates, outputs and scratch, belongs to the stream it runs on.
 
 def _require(ok: bool, what: str):
     if not ok:
@@ -662,16 +663,26 @@ def _torch_stream(stream):
     return torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
 
 
+def _on(stream):
+    """A context in which torch allocates, copies and frees on the call's stream
+    (a table of pointers too is scratch of the launch that reads it)."""
+    return torch.cuda.stream(None if stream is None else _torch_stream(stream))
+
+
+def _empty(like: torch.Tensor, shape, dtype, stream):
+    """A buffer that a call writes, from the pool of the call's stream: a block of
+    the current stream's pool may still be in use there by what it was freed from,
+    and the call does not wait for that."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _scratch(nbytes: int, like: torch.Tensor, stream):
-    """Device scratch of one call from torch's allocator, None for none.  The
-    allocator may hand it to the current stream's next user, so a call on
-    another stream is recorded."""
-    if nbytes == 0:
-        return None
-    t = like.new_empty(nbytes, dtype=torch.uint8)
-    if stream is not None:
-        t.record_stream(_torch_stream(stream))
-    return t
+    """Device scratch of one call from torch's allocator, None for none.  Freed
+    after the launch, it goes to the next user on the same stream."""
+    return _empty(like, nbytes, torch.uint8, stream) if nbytes else None
 
 
 def _parts(x, name: str):
@@ -714,12 +725,12 @@ def route_experts(logits: torch.Tensor, top_k: int, *, score: int = SCORE_SOFTMA
     b = _tensor(bias, "bias", torch.float32, dev, (E,), optional=True)
     _require(top_k >= 1, "top_k must be at least 1")
     if ids is None:
-        ids = logits.new_empty((T, top_k), dtype=torch.int32)
+        ids = _empty(logits, (T, top_k), torch.int32, stream)
         i = ids.data_ptr()
     else:
         i = _tensor(ids, "ids", torch.int32, dev, (T, top_k))
     if weights is None:
-        weights = logits.new_empty((T, top_k), dtype=torch.float32)
+        weights = _empty(logits, (T, top_k), torch.float32, stream)
         w = weights.data_ptr()
     else:
         w = _tensor(weights, "weights", torch.float32, dev, (T, top_k))
@@ -743,7 +754,7 @@ def route_experts_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
     i = _tensor(ids, "ids", torch.int32, dev, (T, k))
     g = _tensor(dweights, "dweights", torch.float32, dev, (T, k))
     if dlogits is None:
-        dlogits = logits.new_empty((T, E))
+        dlogits = _empty(logits, (T, E), logits.dtype, stream)
         d, ldd = dlogits.data_ptr(), E
     else:
         d, ldd = _matrix(dlogits, "dlogits", logits.dtype, dev, (T, E))
@@ -790,7 +801,7 @@ def plan_experts(ids: torch.Tensor, n_experts: int, *, align: int = 1, plan: Opt
     n, need = _plan_sizes(T, k, n_experts, align)
     if plan is None:
         _require(n_experts >= 1, "n_experts must be at least 1")
-        buf = ids.new_empty(2 * n_experts + 1 + n + T * k)
+        buf = _empty(ids, 2 * n_experts + 1 + n + T * k, torch.int32, stream)
         offsets, counts, rows, slots = buf.split_with_sizes((n_experts + 1, n_experts, n, T * k))
         plan = ExpertPlan(offsets, counts, rows, slots.view(T, k))
         at = buf.data_ptr()
@@ -1037,12 +1048,6 @@ def quantize_experts(xs: Sequence[torch.Tensor], fmt: int, layout: int, mode: in
         rows, cols = e.x.shape
         e.sf = e.sf[: sf_bytes(rows, cols, fmt, layout)]
     return entries
-
-
-def _on(stream):
-    """A context in which torch allocates, copies and frees on the call's
-    stream: the table of pointers is scratch of the launch that reads it."""
-    return torch.cuda.stream(None if stream is None else _torch_stream(stream))
 
 
 def quantize_expert_weights(w: torch.Tensor, fmt: int, stream=None):

@@ -526,6 +526,61 @@ def test_quantizers_of_the_operands_on_another_stream(fmt, raw):
         assert (a[2] is None) == (fmt == MX) and (a[2] is None or torch.equal(a[2], b[2]))
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_that_allocate_on_another_stream(raw):
+    """Outputs and scratch of a call on a side stream: neither blocks that the current stream's work still uses, nor
+    blocks that the current stream may take while the call runs."""
+    g = ref.gen(41)
+    T, E, k, H, N = 5000, 32, 4, 256, 96   # more than 16384 pairs: a plan with scratch; and a product with one
+    logits = ref.randn(g, T, E).cuda()
+    x = qz.quantize_tokens(ref.randn(g, T, H).to(torch.bfloat16).cuda(), MX)
+    w = stacked(g, E, N, H, MX)
+    dw = ref.randn(g, T, k).cuda()
+    ids, weights = qz.route_experts(logits, k)
+    plan = qz.plan_experts(ids, E, align=16)
+    S = plan.rows.numel()
+    pre, dout = ref.randn(g, S, N).to(torch.bfloat16).cuda(), ref.randn(g, S, N).to(torch.bfloat16).cuda()
+    assert qz.load().qz_plan_bytes(T, k, E) > 0 and S >= 4096
+
+    def calls(stream):
+        """(outputs that are kept, outputs that are dropped at once) of each call."""
+        out, dpre = (torch.zeros(S, N, dtype=torch.bfloat16).cuda() for _ in range(2))
+        dbias = torch.zeros(E, N).cuda()
+        if stream is not None:
+            torch.cuda.current_stream().synchronize()
+        kw = dict(stream=stream)
+        yield lambda: qz.route_experts(logits, k, **kw)[1]  # the ids are freed while the router runs
+        yield lambda: qz.route_experts_grad(logits, ids, dw, **kw)
+        yield lambda: qz.plan_experts(ids, E, align=16, **kw).slots
+        yield lambda: qz.expert_product(MX, x, w, plan.offsets, plan.counts, out, rows=plan.rows, **kw)
+        yield lambda: (qz.expert_activation_grad(dout, pre, plan.offsets, plan.counts, dpre, activation=qz.ACT_SILU,
+                                                 dbias=dbias, **kw), dbias)[1]
+
+    want = [call().clone() for call in calls(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.zeros(1 << 26, device="cuda")
+    sizes = [T * k * 4, T * E * 4, 4 * (2 * E + 1 + S + T * k), S * H, 1 << 20, 1 << 16]
+    got, kept = [], []
+    for call in calls(side.cuda_stream if raw else side):
+        blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        for _ in range(20):
+            busy.add_(1.0)
+        for b in blocks:
+            b.fill_(0xFF)   # still to come when the call is made
+        kept.append([b.sum(dtype=torch.int64) for b in blocks])
+        del b, blocks
+        got.append(call())
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes]
+        side.synchronize()
+        del junk
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for sums in kept:   # nothing of a call's was written into what the current stream still read
+        assert [int(v) for v in sums] == [255 * n for n in sizes]
+
+
 @pytest.mark.parametrize("fmt", [MX, NV])
 def test_weight_grad_without_slots(fmt):
     empty = torch.empty(0, 64, dtype=torch.bfloat16).cuda()

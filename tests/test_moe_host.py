@@ -1,6 +1,7 @@
 """Host side of the mixture-of-experts entry points, without a GPU: every
 refusal is returned before any launch, sizes of the plan, ctypes mirrors of the
 structs, and the binding's own checks."""
+import contextlib
 import ctypes
 import os
 import subprocess
@@ -208,3 +209,52 @@ def test_the_stride_of_a_single_row_does_not_matter():
     assert qz.binding._matrix(t, "t", torch.bfloat16, -1, (1, 8)) == (t.data_ptr(), 8)
     t = torch.zeros(64, dtype=torch.bfloat16).as_strided((2, 8), (16, 1))
     assert qz.binding._matrix(t, "t", torch.bfloat16, -1, (2, 8)) == (t.data_ptr(), 16)
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
+    """Outputs and scratch of a call with a stream of its own come from that stream's pool: a block of the current
+    stream's may still be in use there.  (The launches are stubs: this runs without a GPU.)"""
+    b = qz.binding
+    inside, made = [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        inside.append(stream)
+        yield
+        inside.pop()
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 64 if name.endswith("bytes") else 0
+
+    new_empty = torch.Tensor.new_empty
+
+    def recorded(t, *a, **kw):
+        made.append(list(inside))
+        return new_empty(t, *a, **kw)
+
+    monkeypatch.setattr(b, "_on", on)
+    monkeypatch.setattr(b, "load", Library)
+    monkeypatch.setattr(b, "_raw_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(b, "_plan_sizes", lambda *a: (64, 64))
+    monkeypatch.setattr(b, "_region", lambda *a: 512)
+    monkeypatch.setattr(torch.Tensor, "new_empty", recorded)
+    i32, bf, u8 = torch.int32, torch.bfloat16, torch.uint8
+    x, ids, lists = torch.zeros(4, 8), torch.zeros(4, 2, dtype=i32), torch.zeros(3, dtype=i32)
+    rows = torch.zeros(4, 8, dtype=bf)
+    calls = {
+        "route": (2, lambda s: qz.route_experts(x, 2, stream=s)),
+        "route_grad": (1, lambda s: qz.route_experts_grad(x, ids, torch.zeros(4, 2), stream=s)),
+        "plan": (2, lambda s: qz.plan_experts(ids, 5, stream=s)),
+        "product": (1, lambda s: qz.expert_product(
+            qz.FMT_MXFP8, (torch.zeros(4, 32, dtype=u8), torch.zeros(4, 1, dtype=u8)),
+            (torch.zeros(3, 8, 32, dtype=u8), torch.zeros(3, 512, dtype=u8)), lists, lists, rows, rows=lists.new_zeros(4),
+            stream=s)),
+        "activation_grad": (1, lambda s: qz.expert_activation_grad(
+            rows, rows, lists, lists, rows.clone(), activation=qz.ACT_SILU, dbias=torch.zeros(3, 8), stream=s)),
+    }
+    for name, (n, call) in calls.items():
+        for stream in (object(), None):
+            made.clear()
+            call(stream)
+            assert made == [[] if stream is None else [stream]] * n, name
