@@ -194,6 +194,19 @@ def test_route_grad_of_tiny_scores():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_route_grad_of_one_renormalized_choice_is_zero(score, dtype):
+    """Its weight is the constant ``scale``: w = s / s, and g - g w = 0 exactly."""
+    g = ref.gen(13)
+    x = (ref.randn(g, 300, 64) * 2).to(dtype).cuda()
+    x[0] = -200.0
+    ids, w = qz.route_experts(x, 1, score=score, scale=2.5)
+    assert (w == 2.5).all()
+    got = qz.route_experts_grad(x, ids, ref.randn(g, 300, 1).cuda(), score=score, scale=2.5)
+    assert (got == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
 @pytest.mark.parametrize("E,groups", [(128, 1), (128, 4), (256, 8), (256, 32), (512, 2), (1024, 16)])
 def test_router_of_rows_that_wide_loads_cannot_read(dtype, score, E, groups):
     """Rows from an odd element on (or with an odd stride, or an odd bias) are read otherwise: the same choice."""
