@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kDispatchThreads)
                         }
                         st_v4(y + at[u] * ld_y + c, v);
                     }
-                    if (DOTS) {
+                    if (DOTS && at[u] >= 0) {  // a pair without a slot has 0, whatever the token's row holds
                         float g[8];
                         unpack8(o[u], g);
 #pragma unroll

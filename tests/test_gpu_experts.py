@@ -473,6 +473,27 @@ def test_dispatch_and_combine(T, E, k, H, align, weighted):
         ref.close(dots, prod.sum(-1), (20 + H // 2048) * ref.HALF_F32 * prod.abs().sum(-1) + 1e-38, "dots")
 
 
+@pytest.mark.parametrize("H", [8, 264, 2056])
+def test_dots_of_pairs_without_a_slot(H):
+    """They are 0, also where the token's row holds NaN or infinities."""
+    g = ref.gen(H)
+    T, k, S = 6, 6, 40
+    x = ref.randn(g, T, H).to(torch.bfloat16)
+    x[0], x[1, H - 1], x[2, 0], x[3, H // 2] = torch.nan, torch.inf, -torch.inf, torch.nan
+    slots = torch.arange(T * k, dtype=torch.int32).reshape(T, k)
+    slots[0], slots[1], slots[2, ::2], slots[3, 1], slots[4] = -1, S, -7, -1, -1
+    rows = torch.full((S,), -1, dtype=torch.int32)
+    live = (slots >= 0) & (slots < S)
+    for t in range(T):
+        rows[slots[t][live[t]].long()] = t
+    y, w = ref.randn(g, S, H).to(torch.bfloat16).cuda(), ref.randn(g, T, k).cuda()
+    out, dots = torch.empty(S, H, dtype=torch.bfloat16).cuda(), torch.full((T, k), 7.5).cuda()
+    qz.dispatch_experts(x.cuda(), slots.cuda(), rows.cuda(), out, weights=w, other=y, dots=dots)
+    assert (dots.cpu()[~live] == 0).all()
+    for t in (1, 2, 3):
+        assert not torch.isfinite(dots.cpu()[t][live[t]]).any()
+
+
 def test_dispatch_of_few_tokens_zeroes_many_slots():
     g = ref.gen(2)
     ids = torch.randint(0, 128, (3, 8), generator=g, dtype=torch.int32).cuda()
