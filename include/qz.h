@@ -546,7 +546,7 @@ typedef enum qz_score {
 
 typedef enum qz_activation {
     QZ_ACT_NONE = 0,
-    QZ_ACT_RELU = 1, /* max(z, 0) */
+    QZ_ACT_RELU = 1, /* max(z, 0); NaN stays NaN */
     QZ_ACT_SILU = 2, /* z / (1 + exp(-z)) */
     QZ_ACT_GELU = 3  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
 } qz_activation;

@@ -32,6 +32,9 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return r;
 }
 
+// max(z, 0) that keeps NaN (fmaxf returns its other operand).
+__device__ __forceinline__ float relu(float z) { return z <= 0.0f ? 0.0f : z; }
+
 // 1 / (1 + exp(-x)); exp(-x) overflows to inf below -88 and the quotient is 0.
 __device__ __forceinline__ float sigmoid32(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
 
@@ -58,7 +61,7 @@ __device__ __forceinline__ ActPair act_with_grad(float z) {
         p.value = z * s;
         p.grad = ACT == QZ_ACT_GELU ? fmaf(zr, fmaf(3.0f * kGelu2 * kGeluC, z2, kGelu2), s) : zr + s;
     } else if (ACT == QZ_ACT_RELU) {
-        p.value = fmaxf(z, 0.0f);
+        p.value = relu(z);
         p.grad = z > 0.0f ? 1.0f : 0.0f;
     } else {
         p.value = z;

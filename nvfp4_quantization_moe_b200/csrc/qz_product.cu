@@ -399,7 +399,7 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
     if (act == QZ_ACT_NONE) return;
     if (act == QZ_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = fmaxf(v[i], 0.0f);
+        for (int i = 0; i < N; ++i) v[i] = relu(v[i]);
         return;
     }
     const float a = act == QZ_ACT_GELU ? kGelu2 : 1.0f, b = act == QZ_ACT_GELU ? kGelu2 * kGeluC : 0.0f;

@@ -425,6 +425,43 @@ def test_activation_grad_against_differences(act):
     ref.close(d[0], diff, ref.HALF_BF16 * diff.abs() + h * h / 6 * 1.5 + 1e-6, "dpre")
 
 
+# --- activations of values that are not ordinary numbers ---------------------
+
+def activated(act, z, gated):
+    """expert_product's activation of the values z (as a bias on products of zeros), and expert_activation_grad's
+    outputs for them: (act(z), act'(z)), gated also act(z) as du."""
+    N, z = z.numel(), z.to(torch.bfloat16).reshape(1, -1).cuda()
+    x = qz.quantize_tokens(torch.zeros(1, 32, dtype=torch.bfloat16).cuda(), MX)
+    w = stacked(ref.gen(1), 1, N, 32, MX)
+    off, cnt = torch.zeros(1, dtype=torch.int32).cuda(), torch.ones(1, dtype=torch.int32).cuda()
+    out, one = torch.zeros(1, N, dtype=torch.bfloat16).cuda(), torch.ones(1, N, dtype=torch.bfloat16).cuda()
+    kw = dict(up=w, up_bias=one) if gated else {}
+    qz.expert_product(MX, x, w, off, cnt, out, bias=z, activation=act, **kw)
+    d = torch.zeros(1, 2 * N if gated else N, dtype=torch.bfloat16).cuda()
+    qz.expert_activation_grad(one, torch.cat([z, one], 1) if gated else z, off, cnt, d, activation=act, gated=gated)
+    d = d[0].double().cpu()
+    return (out[0].double().cpu(), d[:N]) + ((d[N:],) if gated else ())
+
+
+def same_values(got, want):
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got, nan=7.0), torch.nan_to_num(want, nan=7.0))
+
+
+SPECIAL = torch.tensor([torch.nan, torch.inf, -torch.inf, 3e38, -3e38, 1e-38, -1e-38, 0.0, -0.0, 2.5, -2.5, 1.0, -1.0, 0.5,
+                        -0.5, 64.0])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_relu_keeps_nan(gated):
+    z = SPECIAL.to(torch.bfloat16).double()
+    got = activated(qz.ACT_RELU, SPECIAL, gated)
+    same_values(got[0], z.clamp(min=0))
+    same_values(got[1], (z > 0).double())
+    if gated:
+        same_values(got[2], z.clamp(min=0))
+
+
 # --- dispatch and combine ---------------------------------------------------
 
 @pytest.mark.parametrize("T,E,k,H,align", [(1, 4, 2, 8, 1), (1, 1, 1, 8, 128), (5, 7, 3, 72, 16), (64, 16, 8, 1032, 1),
