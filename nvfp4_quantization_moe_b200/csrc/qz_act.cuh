@@ -40,6 +40,9 @@ __device__ __forceinline__ float sigmoid32(float x) { return fast_rcp(1.0f + fas
 
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
+// z^2 is taken of at most this |z|, far behind where GELU's sigmoid is 0 or 1: an
+// infinite z^2 would make 0 z^2 (SiLU's term of it) NaN.
+constexpr float kActFlat = 1e4f;
 
 struct ActPair {
     float value, grad;

@@ -404,7 +404,10 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
     }
     const float a = act == QZ_ACT_GELU ? kGelu2 : 1.0f, b = act == QZ_ACT_GELU ? kGelu2 * kGeluC : 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= sigmoid32(v[i] * fmaf(b * v[i], v[i], a));
+    for (int i = 0; i < N; ++i) {
+        const float w = fminf(fabsf(v[i]), kActFlat);
+        v[i] *= sigmoid32(v[i] * fmaf(b * w, w, a));
+    }
 }
 
 __device__ __forceinline__ float amax_scale(const float* amax, int64_t i) {

@@ -462,6 +462,30 @@ def test_relu_keeps_nan(gated):
         same_values(got[2], z.clamp(min=0))
 
 
+def same_function(got, want, z, what):
+    """NaN and infinities where the definition has them; elsewhere the rounding to bf16 and below 16 fp32 roundings of
+    1.2 (1 + |z|), and of an exponential's argument (|z| from 64 on makes no difference any more)."""
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+    assert torch.equal(torch.isinf(got), torch.isinf(want)) and torch.equal(got[torch.isinf(got)], want[torch.isinf(want)]), what
+    on = torch.isfinite(want)
+    size = 1.2 * (1 + z[on].abs().clamp(max=64))
+    each = 16 * ref.HALF_F32 * size + 2 * 80 * ref.HALF_F32 * want[on].abs()
+    ref.close(got[on], want[on], each + ref.HALF_BF16 * (want[on].abs() + each) + 1e-38, what)
+
+
+@pytest.mark.parametrize("act", [qz.ACT_SILU, qz.ACT_GELU])
+@pytest.mark.parametrize("gated", [False, True])
+def test_activations_of_infinities(act, gated):
+    """Both are inf at inf; at -inf the definitions' quotient and product are NaN."""
+    z = SPECIAL.to(torch.bfloat16).double()
+    want = z / (1 + torch.exp(-z)) if act == qz.ACT_SILU else ref.act(act, z)
+    assert want[1] == torch.inf and torch.isnan(want[2]) and want[4] == 0
+    got = activated(act, SPECIAL, gated)
+    same_function(got[0], want, z, "act")
+    if gated:
+        same_function(got[2], want, z, "du")
+
+
 # --- dispatch and combine ---------------------------------------------------
 
 @pytest.mark.parametrize("T,E,k,H,align", [(1, 4, 2, 8, 1), (1, 1, 1, 8, 128), (5, 7, 3, 72, 16), (64, 16, 8, 1032, 1),
