@@ -41,7 +41,8 @@ __device__ __forceinline__ float sigmoid32(float x) { return fast_rcp(1.0f + fas
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
 // z^2 is taken of at most this |z|, far behind where GELU's sigmoid is 0 or 1: an
-// infinite z^2 would make 0 z^2 (SiLU's term of it) NaN.
+// infinite z^2 would make 0 z^2 NaN (SiLU's term of it, GELU's derivative where the
+// sigmoid is flat).
 constexpr float kActFlat = 1e4f;
 
 struct ActPair {
@@ -54,7 +55,7 @@ template <int ACT>
 __device__ __forceinline__ ActPair act_with_grad(float z) {
     ActPair p;
     if (ACT == QZ_ACT_SILU || ACT == QZ_ACT_GELU) {
-        const float z2 = z * z;
+        const float w = fminf(fabsf(z), kActFlat), z2 = w * w;
         const float v = ACT == QZ_ACT_GELU ? z * fmaf(kGelu2 * kGeluC, z2, kGelu2) : z;
         const float e = fast_exp(-fabsf(v));
         const float q = fast_rcp(1.0f + e);

@@ -486,6 +486,17 @@ def test_activations_of_infinities(act, gated):
         same_function(got[2], want, z, "du")
 
 
+@pytest.mark.parametrize("act", [qz.ACT_SILU, qz.ACT_GELU])
+@pytest.mark.parametrize("gated", [False, True])
+def test_derivatives_of_large_values(act, gated):
+    """0 or 1 where the activation is flat or straight, up to the largest bf16."""
+    z = torch.tensor([3e38, -3e38, 2e19, -2e19, 1e13, -1e13, 2e4, -2e4, 9e3, -9e3, 300.0, -300.0, 64.0, -64.0, 5.0, -5.0])
+    got = activated(act, z, gated)
+    z = z.to(torch.bfloat16).double()
+    same_function(got[1], ref.act_grad(act, z), z, "act'")
+    assert got[1][:12].tolist() == [1.0, 0.0] * 6
+
+
 # --- dispatch and combine ---------------------------------------------------
 
 @pytest.mark.parametrize("T,E,k,H,align", [(1, 4, 2, 8, 1), (1, 1, 1, 8, 128), (5, 7, 3, 72, 16), (64, 16, 8, 1032, 1),
