@@ -86,6 +86,7 @@ constexpr uint32_t kStagesBytes = Shape<FMT>::kStages * (kBytesData + kScaleStag
 struct ProductArgs {
     int act, n_experts, gated, x_per_row, gather, n_blocks;
     int64_t n, k, x_rows, slots, w_sf_stride, ld_sf;
+    int64_t ids;  // what an entry of rows (a slot number without rows) must be below to have a row of x
     const uint8_t *x_sf, *w_sf, *up_sf;
     const float *x_amax, *w_amax, *up_amax;
     const int32_t *rows, *offsets, *counts;
@@ -236,7 +237,7 @@ __device__ __forceinline__ void scale_warp(const ProductArgs& p, const ExpertLis
         for (int j = 0; j < 2; ++j) {
             const int at = 64 * warp + 32 * j + lane;
             int64_t i = t.first + at;
-            if (p.rows && at < t.live) i = __ldg(p.rows + i);
+            if (p.gather && at < t.live) i = __ldg(p.rows + i);
             r[j] = i >= 0 && i < p.x_rows ? (int)i : 0;
         }
     };
@@ -669,11 +670,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             if (GRAD) {
                 if (FMT == QZ_FMT_NVFP4) scale0 = scale1 = amax_scale(g.dz_amax, 0) * amax_scale(g.x_amax, 0);
             } else if (r < t.live) {
-                int64_t row = slot;
-                if (p.gather) row = __ldg(p.rows + slot);
-                exists = row >= 0 && row < p.x_rows;
+                // (rows in slot order still have their index: a slot without a row is zeros whatever the weights hold)
+                const int64_t id = p.rows ? (int64_t)__ldg(p.rows + slot) : slot;
+                exists = id >= 0 && id < p.ids;
                 if (FMT == QZ_FMT_NVFP4 && exists) {
-                    const float ga = amax_scale(p.x_amax, p.x_per_row ? row : 0);
+                    const float ga = amax_scale(p.x_amax, !p.x_per_row ? 0 : p.gather ? id : slot);
                     scale0 = ga * amax_scale(p.w_amax, t.e);
                     scale1 = GATED ? ga * amax_scale(p.up_amax, t.e) : scale0;
                 }
@@ -951,6 +952,7 @@ static cudaError_t launch_experts(const Args& a, const CUtensorMap& ma, const CU
 
 cudaError_t launch_product(const qz_product& call, int ctas, cudaStream_t s, unsigned* d_err, void* ws) {
     qz_product p = call;
+    bool gather = p.d_rows != nullptr;
     int64_t ld_sf = p.k / (p.fmt == QZ_FMT_NVFP4 ? 16 : 32);
     if (ws != nullptr && product_bytes(p) > 0) {
         const CopyLayout l = copy_layout(p);
@@ -965,7 +967,7 @@ cudaError_t launch_product(const qz_product& call, int ctas, cudaStream_t s, uns
         p.x_sf = w + l.sf;
         if (amax) p.x_amax = amax;
         p.x_rows = p.slots;
-        p.d_rows = nullptr;
+        gather = false;
         ld_sf = l.ld_sf;
     }
     Args a = {};
@@ -974,11 +976,12 @@ cudaError_t launch_product(const qz_product& call, int ctas, cudaStream_t s, uns
     q.n_experts = p.n_experts;
     q.gated = p.up_q != nullptr;
     q.x_per_row = p.x_amax_per_row;
-    q.gather = p.d_rows != nullptr;
+    q.gather = gather;
     q.n_blocks = (int)(q.gated ? (p.n + 127) / 128 : (p.n + 255) / 256);
     q.n = p.n;
     q.k = p.k;
     q.x_rows = p.x_rows;
+    q.ids = call.x_rows;
     q.slots = p.slots;
     q.w_sf_stride = p.w_sf_stride;
     q.ld_sf = ld_sf;

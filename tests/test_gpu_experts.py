@@ -206,6 +206,35 @@ def test_product_of_a_large_gather(fmt, K):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("S", [300, 2500])  # gathered in the product, copied first
+def test_slots_without_a_row_are_zeros_for_any_weight(fmt, gated, S):
+    """A row of zeros times a weight of NaN or of an infinite amax: the slot has no row, so its products are 0."""
+    g = ref.gen(S)
+    E, N, K, R = 2, 64, 128, 50
+    x = qz.quantize_tokens(ref.randn(g, R, K).to(torch.bfloat16).cuda(), fmt)
+    w, up = stacked(g, E, N, K, fmt), stacked(g, E, N, K, fmt)
+    for q, sf, amax in (w, up):
+        if fmt == MX:
+            q[0, 3, 5] = 0x7F  # NaN
+        else:
+            amax[0] = torch.inf
+    rows = torch.randint(0, R, (S,), generator=g, dtype=torch.int32)
+    none = [5, 7, 130, S - 1]
+    rows[none] = torch.tensor([-1, R, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    out, pre = torch.full((S, N), 3.0, dtype=torch.bfloat16).cuda(), torch.full((S, 2 * N if gated else N), 3.0,
+                                                                                dtype=torch.bfloat16).cuda()
+    offsets = torch.tensor([0, S // 2], dtype=torch.int32).cuda()
+    counts = torch.full((2,), S // 2, dtype=torch.int32).cuda()
+    bias = ref.randn(g, E, N).to(torch.bfloat16).cuda()
+    qz.expert_product(fmt, x, w, offsets, counts, out, rows=rows.cuda(), up=up if gated else None, bias=bias, pre=pre)
+    for s in none:
+        assert torch.equal(pre[s, :N], bias[2 * s // S]) and (not gated or (pre[s, N:] == 0).all())
+        assert torch.equal(out[s], torch.zeros_like(bias[0]) if gated else bias[2 * s // S])
+    assert torch.isnan(out[4, 3]) if fmt == MX else not torch.isfinite(out[4]).any()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
 def test_product_of_the_most_experts(fmt):
     counts = [0] * qz.MAX_ROUTE_EXPERTS
     for e, c in ((0, 1), (500, 3), (1000, 130), (1023, 2)):
