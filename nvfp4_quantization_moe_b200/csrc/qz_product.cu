@@ -834,8 +834,9 @@ done:
 // with the copy against without: 128 experts of 2 x 768 x 2048 MXFP8, 32768 slots
 // 146 us against 213, 8192 85 against 100, 4096 83 against 82, 2048 81 against 78;
 // 16 experts of 4096 x 2048 NVFP4, 16384 slots 96 against 153, 2048 26 against 34,
-// 1024 24 either way.  A warp copies a slot's row; an index that is no row of x
-// leaves zeros.
+// 1024 24 either way.  A warp copies a slot's row.  A slot without one (a plan's
+// unused slots above all) is left as it is: the epilogue does not store it, or
+// writes zeros.
 
 constexpr int kCopyWarps = 8;
 
@@ -847,29 +848,28 @@ __global__ void __launch_bounds__(kCopyWarps * 32)
     const int64_t s = (int64_t)blockIdx.x * kCopyWarps + (threadIdx.x >> 5);
     if (s >= slots) return;
     const int64_t r = __ldg(rows + s);
-    const bool in = r >= 0 && r < x_rows;
-    const uint8_t* from = x_q + (in ? r : 0) * row_bytes;
+    if (r < 0 || r >= x_rows) return;
+    const uint8_t* from = x_q + r * row_bytes;
     uint8_t* to = q + s * row_bytes;
     for (int64_t c = 16 * lane; c < row_bytes; c += 4 * 512) {
         uint4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (in && c + 512 * i < row_bytes) v[i] = *reinterpret_cast<const uint4*>(from + c + 512 * i);
+            if (c + 512 * i < row_bytes) v[i] = *reinterpret_cast<const uint4*>(from + c + 512 * i);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (c + 512 * i < row_bytes) st_v4(to + c + 512 * i, v[i]);
     }
-    const uint8_t* sfrom = x_sf + (in ? r : 0) * kv;
+    const uint8_t* sfrom = x_sf + r * kv;
     uint8_t* sto = sf + s * ld_sf;
     if ((kv & 3) == 0) {
         for (int64_t c = 4 * lane; c < kv; c += 128)
-            st_u32(sto + c, in ? __ldg(reinterpret_cast<const uint32_t*>(sfrom + c)) : 0u);
+            st_u32(sto + c, __ldg(reinterpret_cast<const uint32_t*>(sfrom + c)));
     } else {
-        for (int64_t c = lane; c < kv; c += 32) sto[c] = in ? __ldg(sfrom + c) : (uint8_t)0;
+        for (int64_t c = lane; c < kv; c += 32) sto[c] = __ldg(sfrom + c);
     }
-    if (amax != nullptr && lane == 0) amax[s] = in ? __ldg(x_amax + r) : 0.0f;
+    if (amax != nullptr && lane == 0) amax[s] = __ldg(x_amax + r);
 }
 
 constexpr int64_t kCopySlots = 2048;  // slots from which the copy pays

@@ -1,5 +1,7 @@
 """The experts' products, their gradients and the moves between token order and
 expert order, against binary64."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -232,6 +234,28 @@ def test_slots_without_a_row_are_zeros_for_any_weight(fmt, gated, S):
         assert torch.equal(pre[s, :N], bias[2 * s // S]) and (not gated or (pre[s, N:] == 0).all())
         assert torch.equal(out[s], torch.zeros_like(bias[0]) if gated else bias[2 * s // S])
     assert torch.isnan(out[4, 3]) if fmt == MX else not torch.isfinite(out[4]).any()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_product_of_few_tokens_in_many_padded_slots(fmt):
+    """A plan's unused slots are not copied: what their part of the workspace holds reaches no output."""
+    g = ref.gen(17)
+    E, N, K, T, k = 24, 264, 256, 60, 4
+    x = qz.quantize_tokens(ref.randn(g, T, K).to(torch.bfloat16).cuda(), fmt)
+    w = stacked(g, E, N, K, fmt)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32).cuda()
+    wide, tight = qz.plan_experts(ids, E, align=128), qz.plan_experts(ids, E)
+    S = wide.rows.numel()
+    p = qz.binding._Product(fmt=fmt, n=N, k=K, slots=S, x_rows=T, d_rows=0x1000, x_amax_per_row=1)
+    need = qz.load().qz_product_bytes(ctypes.byref(p))
+    assert need > 0 and S > 12 * T * k
+    workspace = torch.full((need,), 0xFF, dtype=torch.uint8).cuda()  # NaN as codes, as scales and as an amax
+    out = torch.full((S, N), 3.0, dtype=torch.bfloat16).cuda()
+    qz.expert_product(fmt, x, w, wide.offsets, wide.counts, out, rows=wide.rows, workspace=workspace)
+    want = torch.zeros(T * k, N, dtype=torch.bfloat16).cuda()
+    qz.expert_product(fmt, x, w, tight.offsets, tight.counts, want, rows=tight.rows)
+    assert torch.equal(out[wide.slots.long()], want[tight.slots.long()])
+    assert (out[wide.rows < 0] == 3.0).all()
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
