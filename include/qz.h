@@ -683,7 +683,8 @@ typedef struct qz_product {
 qz_status qz_expert_product(const qz_product *p, void *stream, const qz_launch_opts *opts);
 
 /* Device scratch with which qz_expert_product is faster, in bytes; 0 where it
- * would use none (few slots, no d_rows) and for sizes it refuses. */
+ * would use none (no d_rows, few slots, very many of one column block, many more
+ * than rows) and for sizes it refuses. */
 size_t qz_product_bytes(const qz_product *p);
 
 /* The experts' weight gradients (HOST struct, read during the call).  Operands

@@ -830,13 +830,21 @@ done:
 // Gathering inside the product takes about 1,150 clocks a stage (32 gathers of
 // four rows), twice the products, and repeats for every column block.  A large
 // call with a workspace therefore copies the rows (payload, scales, amax) into
-// slot order first, at the HBM's rate, and runs without an index.  Slots in all,
-// with the copy against without: 128 experts of 2 x 768 x 2048 MXFP8, 32768 slots
-// 146 us against 213, 8192 85 against 100, 4096 83 against 82, 2048 81 against 78;
-// 16 experts of 4096 x 2048 NVFP4, 16384 slots 96 against 153, 2048 26 against 34,
-// 1024 24 either way.  A warp copies a slot's row.  A slot without one (a plan's
-// unused slots above all) is left as it is: the epilogue does not store it, or
-// writes zeros.
+// slot order first, at the HBM's rate, and runs without an index.  A warp copies
+// a slot's row.  A slot without one (a plan's unused slots above all) is left as
+// it is: the epilogue does not store it, or writes zeros.
+//
+// The rule, with both sides measured (us in a graph, copy against gather; K 2048;
+// "2 x 768" is gated):
+//   slots from which the copy pays     2 x 768, 128 experts, MXFP8: 1024 slots 78 : 76, 2048 80 : 79,
+//                                      4096 83 : 94, 16384 99 : 144; 4096 columns, 16 experts, NVFP4:
+//                                      2048 26 : 34, 16384 93 : 153
+//   one column block gathers only      256 columns, 16 experts, MXFP8: 4096 slots 16 : 20, 8192 17 : 20,
+//   once: the copy pays up to 8192     16384 22 : 21, 65536 81 : 67; NVFP4: 8192 15.1 : 15.1,
+//                                      16384 17.8 : 15.4
+//   padded plans of few tokens are     2 x 768, 128 experts, aligned to 128, MXFP8: 16 tokens in 16384
+//   mostly unused slots: up to 64      slots (1024 a token) 54 : 50, 128 in 17280 (135) 81 : 77, 256 in
+//   slots a row, twice QZ_MAX_TOP_K    18304 (71) 82 : 83, 512 in 20352 (39) 83 : 88
 
 constexpr int kCopyWarps = 8;
 
@@ -872,7 +880,7 @@ __global__ void __launch_bounds__(kCopyWarps * 32)
     if (amax != nullptr && lane == 0) amax[s] = __ldg(x_amax + r);
 }
 
-constexpr int64_t kCopySlots = 2048;  // slots from which the copy pays
+constexpr int64_t kCopySlots = 2048, kCopySlotsOneBlock = 8192, kCopySlotsPerRow = 2 * QZ_MAX_TOP_K;
 
 struct CopyLayout {
     int64_t ld_sf, q, sf, amax, total;  // scale stride, offsets and size in bytes
@@ -889,8 +897,12 @@ static CopyLayout copy_layout(const qz_product& p) {
     return l;
 }
 
+static int64_t column_blocks(const qz_product& p) { return p.up_q ? (p.n + 127) / 128 : (p.n + 255) / 256; }
+
 size_t product_bytes(const qz_product& p) {
-    return p.d_rows && p.slots >= kCopySlots && p.x_rows > 0 ? (size_t)copy_layout(p).total : 0;
+    const bool copies = p.d_rows && p.slots >= kCopySlots && (column_blocks(p) > 1 || p.slots <= kCopySlotsOneBlock) &&
+                        p.slots <= kCopySlotsPerRow * p.x_rows;
+    return copies ? (size_t)copy_layout(p).total : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -977,7 +989,7 @@ cudaError_t launch_product(const qz_product& call, int ctas, cudaStream_t s, uns
     q.gated = p.up_q != nullptr;
     q.x_per_row = p.x_amax_per_row;
     q.gather = gather;
-    q.n_blocks = (int)(q.gated ? (p.n + 127) / 128 : (p.n + 255) / 256);
+    q.n_blocks = (int)column_blocks(p);
     q.n = p.n;
     q.k = p.k;
     q.x_rows = p.x_rows;

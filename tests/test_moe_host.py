@@ -131,6 +131,22 @@ def test_product_refusals(lib):
     assert lib.qz_expert_product(None, None, None) == BAD
 
 
+def test_rows_are_copied_where_that_pays(lib):
+    """By slots, column blocks (256 columns, gated 128) and slots a row; the size is the workspace of such a call."""
+    def size(slots, n=1024, x_rows=None, gated=False, fmt=0):
+        p = qz.binding._Product(fmt=fmt, k=128, n=n, slots=slots, x_rows=slots if x_rows is None else x_rows, d_rows=A,
+                                up_q=A if gated else None)
+        return lib.qz_product_bytes(ctypes.byref(p))
+
+    for gated in (False, True):
+        assert size(2047, gated=gated) == 0 and size(2048, gated=gated) >= 2048 * (128 + 4)
+        one = 128 if gated else 256
+        assert size(8192, one, gated=gated) > 0 and size(8193, one, gated=gated) == 0
+        assert size(8193, one + 8, gated=gated) > 0 and size(1 << 20, one + 8, gated=gated) > 0
+        assert size(6400, x_rows=100, gated=gated) > 0 and size(6401, x_rows=100, gated=gated) == 0
+    assert size(2048, fmt=1) >= 2048 * (64 + 8) and size(1 << 31) == 0 and size(4096, x_rows=0) == 0
+
+
 def test_weight_grad_refusals(lib):
     def grad(**kw):
         base = dict(fmt=0, n_experts=4, out_type=1, accumulate=0, n=64, k=128, slots=256, dz_q=A, dz_sf=A, dz_amax=None,
