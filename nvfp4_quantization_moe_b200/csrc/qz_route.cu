@@ -342,11 +342,21 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
     }
     // fp32: 2^x within 2 ulp, its argument's rounding (|x - m| e^(x - m) <= 1 / e), a sum of E terms in
     // a tree, a reciprocal within 1 ulp, a product and a sum: below 24 half ulps of the largest magnitude
-    // (`largest` is not negative: its bits are ordered like it)
-    const F bound = sizeof(F) == 4 ? (F)(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint((float)largest))) *
-                                         (24.0f / 16777216.0f))
-                                   : (F)0;
+    // (`largest` is not negative: its bits are ordered like it).  A sigmoid's argument is not below a
+    // maximum's: with its rounding and the constant's, s is off by s (9 + 1.22 |x|) half ulps, which is
+    // largest for the largest s, and there |x| is -ln s at most.
+    F bound = 0;
     bool certain = true;
+    if (sizeof(F) == 4) {
+        const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint((float)largest)));
+        const float steps = sigmoid ? 24.0f + fmaxf(-1.25f * __logf(top), 0.0f) : 24.0f;
+        bound = (F)(top * (steps / 16777216.0f));
+        // scores that are flushed to 0 (below 2^-126) are off by more than that only beside ones as small
+        if (sigmoid && top < 1e-26f) {
+            bound = 0;
+            certain = false;
+        }
+    }
 
     decltype(key_of(F())) key[PER];
     unsigned kept = 0xFFFFFFFFu;
@@ -392,7 +402,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
             // the least value kept against the largest that is not (0: every group with an expert is kept)
             const uint32_t low = __reduce_min_sync(kFull, mine_kept ? key32((float)value) : 0xFFFFFFFFu);
             const uint32_t high = __reduce_max_sync(kFull, lane < a.n_groups && !mine_kept ? key32((float)value) : 0u);
-            certain = high == 0 || unkey32(low) - unkey32(high) > 4.0f * (float)bound;
+            certain = certain && (high == 0 || unkey32(low) - unkey32(high) > 4.0f * (float)bound);
         }
     }
     int group = 0, in_group = 0;  // of expert lane + 32 j, kept up without divisions

@@ -70,6 +70,28 @@ def test_scores_closer_than_fp32_are_told_apart():
     assert ids[0, 0].item() == 40 and ids[1, 0].item() == 7
 
 
+@pytest.mark.parametrize("at", [-85.0, -70.0, -59.0, -46.0, -30.0, -12.0, -1.0])
+def test_close_groups_and_biased_scores_of_small_sigmoids(at):
+    """Their fp32 values are off by more, relative to themselves, the further the logits are below 0."""
+    if at == -46.0:
+        check_route(torch.tensor([[-46.489601, -46.718143, -46.608604, -46.586235]]).cuda(), 1, SIGMOID, groups=2)
+    g = ref.gen(int(-at))
+    T = 1500
+    logit = lambda p: torch.log(p) - torch.log1p(-p)  # noqa: E731
+    # two groups of two: the last logit makes their sums equal but for its own rounding
+    x = (at + 2 * torch.rand(T, 1, generator=g) - 0.4 * torch.rand(T, 4, generator=g)).double()
+    s = torch.sigmoid(x.float().double())
+    x[:, 3] = logit((s[:, 0] + s[:, 1] - s[:, 2]).clamp(min=float(s.min()) / 4))
+    check_route(x.float().cuda(), 1, SIGMOID, groups=2)
+    # biases of the scores' size: expert j's logit makes its biased score expert 0's but for its own rounding
+    size = float(torch.sigmoid(torch.tensor(at, dtype=torch.float64)))
+    bias = (torch.rand(40, generator=g) * size).float()
+    x = (at + 2 * torch.rand(T, 40, generator=g)).double()
+    s0 = torch.sigmoid(x[:, :1].float().double())
+    x[:, 1:4] = logit((s0 + bias[0].double() - bias[1:4].double()).clamp(min=size / 8))
+    check_route(x.float().cuda(), 6, SIGMOID, bias.cuda())
+
+
 def test_masked_experts():
     g = ref.gen(5)
     x = ref.randn(g, 12, 40)
