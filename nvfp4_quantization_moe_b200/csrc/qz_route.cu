@@ -340,16 +340,19 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
         if (!(x[j] > -INFINITY) || v[j] != v[j]) v[j] = -INFINITY;
         else if (sizeof(F) == 4 && fabs(v[j]) < INFINITY) largest = fmax(largest, (F)fabs(v[j]));
     }
-    // fp32: 2^x within 2 ulp, its argument's rounding (|x - m| e^(x - m) <= 1 / e), a sum of E terms in
-    // a tree, a reciprocal within 1 ulp, a product and a sum: below 24 half ulps of the largest magnitude
-    // (`largest` is not negative: its bits are ordered like it).  A sigmoid's argument is not below a
-    // maximum's: with its rounding and the constant's, s is off by s (9 + 1.22 |x|) half ulps, which is
-    // largest for the largest s, and there |x| is -ln s at most.
+    // The fp32 error of a value, in half ulps (2^-24) of the largest magnitude (`largest` is not negative: its
+    // bits are ordered like it).  A softmax's exponential at d below the maximum is off by e^-d (4 + 2.22 d)
+    // (2^x within 2 ulp; the difference, the product and the constant are rounded), 4 at most.  Its sum is off
+    // by the terms' mean of 4 + 2.22 d, below 15 for 1024 terms, and by PER + 5 additions (a lane's in a row,
+    // then a tree); reciprocal, product and the bias's addition add 4.  24 + PER covers it, as differences are
+    // held against two and of groups against four of them, and two values share the sum's error.  A sigmoid has
+    // no sum, but its argument is not below a maximum's: it is off by s (9 + 1.22 |x|), which is largest for the
+    // largest s, and there |x| is -ln s at most.
     F bound = 0;
     bool certain = true;
     if (sizeof(F) == 4) {
         const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint((float)largest)));
-        const float steps = sigmoid ? 24.0f + fmaxf(-1.25f * __logf(top), 0.0f) : 24.0f;
+        const float steps = sigmoid ? 24.0f + fmaxf(-1.25f * __logf(top), 0.0f) : 24.0f + (float)PER;
         bound = (F)(top * (steps / 16777216.0f));
         // scores that are flushed to 0 (below 2^-126) are off by more than that only beside ones as small
         if (sigmoid && top < 1e-26f) {

@@ -92,6 +92,22 @@ def test_close_groups_and_biased_scores_of_small_sigmoids(at):
     check_route(x.float().cuda(), 6, SIGMOID, bias.cuda())
 
 
+@pytest.mark.parametrize("E", [256, 1000, 1024])
+def test_close_biased_scores_of_long_softmax_rows(E):
+    """A sum whose small terms are lost in a row of additions to a large one: the choice is binary64's all the same."""
+    g = ref.gen(E)
+    T = 300
+    x = (-16.65 + 0.02 * torch.rand(T, E, generator=g)).float()
+    x[:, 0] = 0.0
+    x[T // 2:, 0] = x[T // 2:, 32] = -4.0 * torch.rand(T - T // 2, generator=g)
+    p = ref.scores(x.double(), False)
+    # biases that make eight experts' biased scores those of expert 0 in one row, and close in the others
+    bias = torch.zeros(E)
+    bias[100:108] = (p[3, 0] - p[3, 100:108]).float()
+    check_route(x.cuda(), 6, SOFTMAX, bias.cuda(), renorm=False)
+    check_route(x.cuda(), 6, SOFTMAX, bias.cuda(), groups=4, top=2)
+
+
 def test_masked_experts():
     g = ref.gen(5)
     x = ref.randn(g, 12, 40)
