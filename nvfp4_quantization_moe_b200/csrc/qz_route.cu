@@ -196,13 +196,20 @@ __device__ __forceinline__ Pick pick_by_rounds(K (&key)[PER], int k, int lane) {
     return r;
 }
 
+// How far a value of magnitude |v| may be off is `unit` |v|, or that of the row's scores.
+struct Error {
+    float score, unit;
+    __device__ __forceinline__ float of(float v) const { return fmaxf(score, unit * fabsf(v)); }
+};
+
 // The same by candidates (see the top of the file), `n` of them.  With GAPS
-// every expert within `margin` of the bar is one too, and *gap gets the lane's
-// difference to the next value, if it is chosen.  false: more than 32
-// candidates, nothing is decided.
+// every expert that the errors could lift to the bar is one too, and *close says
+// that the lane's value is chosen and could be the next one's.  (A value below
+// another by more than the errors of the other is so for its own too: |v| grows
+// by the difference at most.)  false: more than 32 candidates, nothing is decided.
 template <int PER, bool DENSE, bool GAPS>
 __device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, int lane, uint2* cand, Pick& r, int& n,
-                                             float margin, float* gap) {
+                                             Error error, bool* close) {
     uint32_t left = key[0], bar = 1;
 #pragma unroll
     for (int j = 1; j < PER; ++j) left = max(left, key[j]);
@@ -212,7 +219,7 @@ __device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, 
         if (left == bar) left = 0;
     }
     if (rounds > 32 || bar == 0) bar = 1;  // fewer lanes than choices: every key above 0
-    else if (GAPS) bar = max(key32(unkey32(bar) - margin), 1u);
+    else if (GAPS) bar = max(key32(unkey32(bar) - 2.0f * error.of(unkey32(bar))), 1u);
     n = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -235,7 +242,10 @@ __device__ __forceinline__ bool pick_by_rank(const uint32_t (&key)[PER], int k, 
     }
     r.id = lane < n ? (int)mine.y : -1;
     r.at = lane < n ? before : lane;
-    if (GAPS) *gap = lane < n && before < k && behind != 0 ? unkey32(mine.x) - unkey32(behind) : INFINITY;
+    if (GAPS) {
+        const float value = unkey32(mine.x);
+        *close = lane < n && before < k && behind != 0 && !(value - unkey32(behind) > 2.0f * error.of(value));
+    }
     return true;
 }
 
@@ -259,23 +269,23 @@ struct Choice {
 };
 
 // The picks, and for fp32 values whether the differences allow them.
-template <int PER, bool DENSE, typename F>
-__device__ __forceinline__ void decide(const RouteArgs& a, unsigned long long (&key)[PER], int lane, uint2*, F, bool, Choice& r) {
+template <int PER, bool DENSE>
+__device__ __forceinline__ void decide(const RouteArgs& a, unsigned long long (&key)[PER], int lane, uint2*, Error, bool, Choice& r) {
     r.pick = pick_by_rounds<PER, DENSE>(key, a.k, lane);
 }
 
-template <int PER, bool DENSE, typename F>
-__device__ __forceinline__ void decide(const RouteArgs& a, uint32_t (&key)[PER], int lane, uint2* cand, F bound, bool by_logit,
+template <int PER, bool DENSE>
+__device__ __forceinline__ void decide(const RouteArgs& a, uint32_t (&key)[PER], int lane, uint2* cand, Error error, bool by_logit,
                                        Choice& r) {
-    float gap = INFINITY;
+    bool close = false;
     int n;
-    const float margin = by_logit ? 0.0f : 2.0f * (float)bound;
-    if (!pick_by_rank<PER, DENSE, true>(key, a.k, lane, cand, r.pick, n, margin, &gap)) {
+    if (by_logit) error = {0.0f, 0.0f};
+    if (!pick_by_rank<PER, DENSE, true>(key, a.k, lane, cand, r.pick, n, error, &close)) {
         r.certain = r.certain && by_logit;
         if (r.certain) r.pick = pick_by_rounds<PER, DENSE>(key, a.k, lane);
         return;
     }
-    if (by_logit || __all_sync(kFull, gap > margin)) return;
+    if (by_logit || !__any_sync(kFull, close)) return;
     if (a.score != QZ_SCORE_SIGMOID) {
         r.certain = false;
         return;
@@ -314,7 +324,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
         v[j] = !sigmoid ? e : !(x[j] > -INFINITY) ? (F)0 : (x[j] >= 0 ? (F)1 : e) * score_rcp((F)1 + e);
         part += v[j];
     }
-    F largest = 0;  // score or |v|, for the error bound
+    F largest = 0;  // score or v, for the error bound: how far below 0 an expert is biased (masked, even) is no matter
     if (!sigmoid) {
         const F scale = score_rcp(warp_sum(part));
 #pragma unroll
@@ -338,7 +348,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
         if (!by_logit && DENSE) v[j] += (F)bias[j];
         else if (!by_logit && i < a.E) v[j] += (F)__ldg(a.bias + i);
         if (!(x[j] > -INFINITY) || v[j] != v[j]) v[j] = -INFINITY;
-        else if (sizeof(F) == 4 && fabs(v[j]) < INFINITY) largest = fmax(largest, (F)fabs(v[j]));
+        else if (sizeof(F) == 4 && v[j] < INFINITY) largest = fmax(largest, v[j]);
     }
     // The fp32 error of a value, in half ulps (2^-24) of the largest magnitude (`largest` is not negative: its
     // bits are ordered like it).  A softmax's exponential at d below the maximum is off by e^-d (4 + 2.22 d)
@@ -348,15 +358,16 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
     // held against two and of groups against four of them, and two values share the sum's error.  A sigmoid has
     // no sum, but its argument is not below a maximum's: it is off by s (9 + 1.22 |x|), which is largest for the
     // largest s, and there |x| is -ln s at most.
-    F bound = 0;
+    Error error = {0.0f, 0.0f};
     bool certain = true;
     if (sizeof(F) == 4) {
         const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint((float)largest)));
         const float steps = sigmoid ? 24.0f + fmaxf(-1.25f * __logf(top), 0.0f) : 24.0f + (float)PER;
-        bound = (F)(top * (steps / 16777216.0f));
+        error.unit = steps / 16777216.0f;
+        error.score = top * error.unit;
         // scores that are flushed to 0 (below 2^-126) are off by more than that only beside ones as small
         if (sigmoid && top < 1e-26f) {
-            bound = 0;
+            error = {0.0f, 0.0f};
             certain = false;
         }
     }
@@ -405,7 +416,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
             // the least value kept against the largest that is not (0: every group with an expert is kept)
             const uint32_t low = __reduce_min_sync(kFull, mine_kept ? key32((float)value) : 0xFFFFFFFFu);
             const uint32_t high = __reduce_max_sync(kFull, lane < a.n_groups && !mine_kept ? key32((float)value) : 0u);
-            certain = certain && (high == 0 || unkey32(low) - unkey32(high) > 4.0f * (float)bound);
+            certain = certain && (high == 0 || unkey32(low) - unkey32(high) > 4.0f * error.of(unkey32(low)));
         }
     }
     int group = 0, in_group = 0;  // of expert lane + 32 j, kept up without divisions
@@ -430,7 +441,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
     }
 
     Choice r = {{-1, lane}, certain};
-    decide<PER, DENSE>(a, key, lane, cand, bound, by_logit, r);
+    decide<PER, DENSE>(a, key, lane, cand, error, by_logit, r);
     return r;
 }
 
@@ -465,7 +476,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, PER <= 8 ? 10 : 1) route_ker
 #pragma unroll
         for (int j = 0; j < PER; ++j) key[j] = key32(x[j]);
         int n;
-        if (!pick_by_rank<PER, DENSE, false>(key, a.k, lane, cand, pick, n, 0.0f, nullptr)) pick = pick_by_rounds<PER, DENSE>(key, a.k, lane);
+        if (!pick_by_rank<PER, DENSE, false>(key, a.k, lane, cand, pick, n, Error{0.0f, 0.0f}, nullptr)) pick = pick_by_rounds<PER, DENSE>(key, a.k, lane);
     } else {
         double* scratch = s_values + warp * (a.E + a.E / 32 + 1);
         Choice r = choose<PER, float, GROUPS, DENSE>(a, x, m, reinterpret_cast<float*>(scratch), cand, lane);

@@ -108,6 +108,26 @@ def test_close_biased_scores_of_long_softmax_rows(E):
     check_route(x.cuda(), 6, SOFTMAX, bias.cuda(), groups=4, top=2)
 
 
+@pytest.mark.parametrize("mask", [-1e9, -3.4028234663852886e38, -50.0])
+@pytest.mark.parametrize("E,groups,top,k", [(256, 8, 4, 8), (128, 1, 1, 8), (60, 4, 2, 6), (40, 1, 1, 32)])
+def test_experts_masked_by_a_finite_bias(mask, E, groups, top, k):
+    """Disabled experts, whole groups of them, and rows where too few others are left, so that masked ones are chosen."""
+    g = ref.gen(E)
+    x = ref.randn(g, 60, E).float()
+    x[7] = 0.25
+    x[8:30] = (x[8:30] * 4).round() / 4  # many ties
+    for off in ([3], list(range(E // 2)), list(range(E - 4))):
+        bias = (ref.randn(g, E) * 0.1).float()
+        bias[5] = bias[6]
+        bias[off] = mask
+        for score in (SOFTMAX, SIGMOID):
+            check_route(x.cuda(), k, score, bias.cuda(), groups, top)
+        bias -= 3.0  # every biased score below 0
+        check_route(x.cuda(), k, SIGMOID, bias.cuda(), groups, top)
+        bias[[9, 11]] = torch.inf  # always chosen first, the lower one before the other
+        check_route(x.cuda(), k, SIGMOID, bias.cuda(), groups, top)
+
+
 def test_masked_experts():
     g = ref.gen(5)
     x = ref.randn(g, 12, 40)
