@@ -338,6 +338,60 @@ def test_product_on_a_stream_and_in_a_graph():
     assert torch.equal(outs[3][16:32], outs[0][16:32]) and (outs[3][32:48] == 0).all() and (outs[3][1:16] == 0).all()
 
 
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("gated", [False, True])
+def test_every_output_is_the_same_for_any_number_of_ctas(fmt, gated):
+    outputs = [run_product(fmt, [300, 0, 7, 260], 288, 160, gated=gated, act=qz.ACT_GELU, bias=True, residual=True, pre=True,
+                           q=True, max_ctas=ctas) for ctas in (0, 1, 5)]
+    for other in outputs[1:]:
+        for a, b in zip(outputs[0], other):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("gather", [False, True])
+def test_product_of_no_rows(fmt, gather):
+    """An x without rows: every slot has none, and its products are zeros."""
+    g = ref.gen(12)
+    N, K, S = 72, 96, 150
+    w = stacked(g, 2, N, K, fmt)
+    x = (torch.empty(0, K if fmt == MX else K // 2, dtype=torch.uint8).cuda(),
+         torch.empty(0, K // (32 if fmt == MX else 16), dtype=torch.uint8).cuda(), torch.ones(1).cuda())
+    b = ref.randn(g, 2, N).to(torch.bfloat16).cuda()
+    rows = torch.arange(S, dtype=torch.int32).cuda() if gather else None
+    out = torch.full((S, N), 3.0, dtype=torch.bfloat16).cuda()
+    lists = torch.tensor([0, 131], dtype=torch.int32).cuda(), torch.tensor([130, 19], dtype=torch.int32).cuda()
+    qz.expert_product(fmt, x, w, *lists, out, rows=rows, bias=b)
+    assert torch.equal(out[:130], b[0].expand(130, N)) and torch.equal(out[131:], b[1].expand(19, N))
+    assert (out[130] == 3.0).all()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_data_gradient_of_columnwise_weights(fmt):
+    """dA = dZ W as the product with the weights quantized down their columns, by the column-wise quantizer."""
+    g = ref.gen(44)
+    E, N, K, S = 3, 160, 288, 90
+    W = (ref.randn(g, E, N, K) * 0.1).to(torch.bfloat16).cuda()
+    parts = [qz.quantize_slots_colwise(W[e], fmt) for e in range(E)]
+    region = qz.sf_bytes(K, N, fmt, qz.SF_SWIZZLED)
+    w = (torch.stack([p[0] for p in parts]), torch.stack([p[1][:region] for p in parts]),
+         torch.cat([p[2] for p in parts]) if fmt == NV else None)
+    dz = qz.quantize_tokens(ref.randn(g, S, N).to(torch.bfloat16).cuda(), fmt)
+    counts, offsets = torch.tensor([40, 0, 50], dtype=torch.int32), torch.tensor([0, 40, 40], dtype=torch.int32)
+    out = torch.zeros(S, K, dtype=torch.bfloat16).cuda()
+    qz.expert_product(fmt, dz, w, offsets.cuda(), counts.cuda(), out)
+    A = tokens64(dz, N, fmt)
+    for e in (0, 2):
+        at = slice(int(offsets[e]), int(offsets[e] + counts[e]))
+        T = weight64(w, e, N, fmt)  # [K, N]
+        want, size = A[at] @ T.T, A[at].abs() @ T.abs().T
+        tol = size * (N // 32 + 8) * 2.0 ** -22
+        ref.close(out[at], want, tol + ref.HALF_BF16 * (want.abs() + tol) + 1e-38, "dA")
+        # and close to the gradient of the unquantized weights: both operands are off by 2^-3 (e4m3: 2^-4) in norm at most
+        exact = A[at] @ W[e].double().cpu()
+        assert (want - exact).norm() < (2.0 ** -3 if fmt == NV else 2.0 ** -4) * exact.norm()
+
+
 # --- weight gradient --------------------------------------------------------
 
 @pytest.mark.parametrize("fmt", [MX, NV])
@@ -728,6 +782,20 @@ def test_calls_that_allocate_on_another_stream(raw):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_weight_grad_is_the_same_for_any_number_of_ctas(fmt, dtype):
+    g = ref.gen(51)
+    counts, offsets = torch.tensor([200, 0, 384], dtype=torch.int32).cuda(), torch.tensor([0, 256, 256], dtype=torch.int32).cuda()
+    live = torch.ones(640, 1)
+    live[200:256] = 0
+    dz, x = (qz.quantize_slots_colwise((ref.randn(g, 640, n) * live).to(torch.bfloat16).cuda(), fmt) for n in (264, 520))
+    outs = [torch.ones(3, 264, 520, dtype=dtype).cuda() for _ in range(3)]
+    for out, ctas in zip(outs, (0, 1, 5)):
+        qz.expert_weight_grad(fmt, dz, x, offsets, counts, out, accumulate=True, max_ctas=ctas)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]) and outs[0].abs().sum() > 0
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
 def test_weight_grad_without_slots(fmt):
     empty = torch.empty(0, 64, dtype=torch.bfloat16).cuda()
     part = qz.quantize_slots_colwise(empty, fmt)
@@ -845,3 +913,58 @@ def test_training_layer():
     for name, a, b in zip(("dx", "dgate", "dup", "ddown", "dlogits", "dbias"), got, grads):
         rel = (a.double().cpu() - b).norm() / b.norm()
         assert rel < 3 * ref.HALF_E4M3, (name, float(rel))
+
+
+def test_training_layer_in_nvfp4():
+    """The same layer with NVFP4 operands: hidden rows in bf16, quantized between the products; every gradient."""
+    T, E, k, H, I = 60, 4, 2, 128, 96
+    g = ref.gen(35)
+    x = ref.randn(g, T, H).to(torch.bfloat16).cuda()
+    gate, up, down = ((ref.randn(g, E, *s) * 0.1).to(torch.bfloat16).cuda() for s in ((I, H), (I, H), (H, I)))
+    logits = ref.randn(g, T, E).cuda()
+    dy = ref.randn(g, T, H).to(torch.bfloat16).cuda()
+    ids, w = qz.route_experts(logits, k)
+    off, cnt, rows, slots = plan = qz.plan_experts(ids, E, align=128)
+    S = plan.rows.numel()
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16).cuda()  # noqa: E731
+    qg, qu, qd = (qz.quantize_expert_weights(v, NV) for v in (gate, up, down))
+    pre, mid, o, out = bf(S, 2 * I), bf(S, I), bf(S, H), bf(T, H)
+    qz.expert_product(NV, qz.quantize_tokens(x, NV), qg, off, cnt, mid, rows=rows, up=qu, activation=qz.ACT_SILU, pre=pre)
+    qz.expert_product(NV, qz.quantize_tokens(mid, NV), qd, off, cnt, o)
+    qz.combine_experts(o, slots, out, weights=w, residual=x)
+    # backward: the weights quantized down their columns
+    def columns(v):
+        parts = [qz.quantize_slots_colwise(v[e], NV) for e in range(E)]
+        return tuple(torch.stack([p[i] for p in parts]) for i in (0, 1)) + (torch.cat([p[2] for p in parts]),)
+
+    do, dots, dmid = bf(S, H), torch.empty(T, k).cuda(), bf(S, I)
+    qz.dispatch_experts(dy, slots, rows, do, weights=w, other=o, dots=dots)
+    dlogits = qz.route_experts_grad(logits, ids, dots)
+    qz.expert_product(NV, qz.quantize_tokens(do, NV), columns(down), off, cnt, dmid)
+    ddown = torch.zeros(E, H, I).cuda()
+    qz.expert_weight_grad(NV, qz.quantize_slots_colwise(do, NV), qz.quantize_slots_colwise(mid, NV), off, cnt, ddown)
+    dpre, dbias = bf(S, 2 * I), torch.zeros(E, 2 * I).cuda()
+    qz.expert_activation_grad(dmid, pre, off, cnt, dpre, activation=qz.ACT_SILU, gated=True, dbias=dbias)
+    dgate = torch.zeros(E, 2 * I, H).cuda()
+    xs = qz.dispatch_experts(x, slots, rows, bf(S, H))
+    qz.expert_weight_grad(NV, qz.quantize_slots_colwise(dpre, NV), qz.quantize_slots_colwise(xs, NV), off, cnt, dgate)
+    dxs, dx = bf(S, H), bf(T, H)
+    qz.expert_product(NV, qz.quantize_tokens(dpre, NV), columns(torch.cat([gate, up], 1)), off, cnt, dxs)
+    qz.combine_experts(dxs, slots, dx)
+
+    X, G, U, D, L = (v.double().cpu().requires_grad_() for v in (x, gate, up, down, logits))
+    ic = ids.cpu()
+    p = torch.softmax(torch.gather(L, 1, ic.long()), -1)
+    bg = torch.zeros(E, 2 * I, dtype=torch.float64, requires_grad=True)
+    want = torch.zeros(T, H, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            z = torch.cat([G[ic[t, j]], U[ic[t, j]]]) @ X[t] + bg[ic[t, j]]
+            want[t] = want[t] + p[t, j] * (D[ic[t, j]] @ (ref.act(2, z[:I]) * z[I:]))
+    grads = torch.autograd.grad((want * dy.double().cpu()).sum(), [X, G, U, D, L, bg])
+    # a quantized operand is off by 0.1 of its norm (steps of 0.5, 1 and 2 on values of which the largest of 16 is 6),
+    # 2^-3 at most; fewer than eight of them, with independent errors, stand behind one another: sqrt(8) < 3
+    got = [out.double() - x.double(), dx, dgate[:, :I], dgate[:, I:], ddown, dlogits, dbias]
+    for name, a, b in zip(("out", "dx", "dgate", "dup", "ddown", "dlogits", "dbias"), got, (want.detach(), *grads)):
+        rel = (a.double().cpu() - b).norm() / b.norm()
+        assert rel < 3 * 2.0 ** -3, (name, float(rel))
