@@ -17,8 +17,8 @@
 // the choice is first made in fp32, and if any two neighbours that decide it are
 // closer than the fp32 error bound, this token's is made again in binary64: of
 // the candidates alone for a sigmoid, of all experts for a softmax or close groups
-// (binary64 throughout took 81 us on 16384 tokens of 256 experts in 8 groups, and
-// all experts of each close token, a tail of 10 us).
+// (16384 tokens of 256 experts in 8 groups take 25 us so; every token again in
+// binary64, 65).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -64,8 +64,8 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 // Where the experts of a row live in the warp: lane l's value j is expert
 // l + 32 j, or with DENSE (32 PER experts, rows that 16-byte loads can read)
 // expert PER l + j.  Dense rows load and reach the groups, which then are whole
-// lanes, in far fewer instructions: 24 us in place of 35 on 16384 tokens of 256
-// experts in 8 groups (19 in place of 22 without the groups).
+// lanes, in far fewer instructions: 25 us in place of 36 on 16384 tokens of 256
+// experts in 8 groups (19 in place of 21.5 without the groups).
 template <int PER, bool DENSE>
 __device__ __forceinline__ int expert_at(int lane, int j) {
     return DENSE ? PER * lane + j : lane + 32 * j;
@@ -446,8 +446,9 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float (&x)[PE
 }
 
 // SIMPLE: neither a bias nor a group limit, the logits are the keys.  Ten CTAs
-// per SM (48 registers; the rare binary64 path spills some) took 23.9 us, eight 24.2 and
-// twelve 25.6 on 16384 tokens of 256 experts in 8 groups.
+// per SM (48 registers; the rare binary64 path spills some) take 25.0 us, eight 25.4 and
+// twelve 27.2 on 16384 tokens of 256 experts in 8 groups (rows without 16-byte loads
+// 35.8, 37.8 and 35.4).
 template <int PER, bool BF16, bool SIMPLE, bool GROUPS, bool DENSE>
 __global__ void __launch_bounds__(kRouteWarps * 32, PER <= 8 ? 10 : 1) route_kernel(RouteArgs args) {
     extern __shared__ double s_values[];  // GROUPS, not DENSE: [warps][E + E / 32 + 1]
